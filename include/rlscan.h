@@ -89,7 +89,8 @@ typedef enum rlscan_status {
   RLSCAN_ERR_PARAM = 3,
   RLSCAN_ERR_HIP = 4,
   RLSCAN_ERR_ALIGN = 5,
-  RLSCAN_ERR_ALIAS = 6
+  RLSCAN_ERR_ALIAS = 6,
+  RLSCAN_ERR_WORKSPACE = 7
 } rlscan_status;
 
 /* Static, NUL-terminated description of a status code (never NULL). */
@@ -354,6 +355,144 @@ rlscan_status rlscan_eligibility_traces_vec_ex(rlscan_format fmt, rlscan_layout 
 rlscan_status rlscan_linear_scan_segmented_ex(rlscan_format fmt, rlscan_layout layout, const void *a, const void *b,
                                               const uint8_t *done, const void *carry, void *x, int64_t E, int64_t T,
                                               int reverse, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Policy operators: what stands between a policy network and the estimators
+ * above.  A memory over the episode (linear attention: a first-order linear
+ * recurrence whose value is a matrix), the choice of an action from its logits,
+ * and the log-probabilities that V-trace's log_rhos are made of, with their
+ * gradients.  They take values in any rlscan_format; states, decays, uniform
+ * numbers, log-probabilities and entropies are float32.
+ *
+ * Errors      As above, and RLSCAN_ERR_WORKSPACE if workspace_bytes is less
+ *             than the matching _workspace function returns (which returns -1
+ *             for sizes the call refuses; 0 needs no workspace).  A workspace is
+ *             16-byte aligned scratch memory: nothing in it outlives the call.
+ */
+
+/* One [E, T, heads, D] tensor: element (e, t, h, d) at data + e*env + t*step +
+ * h*head + d, strides in elements and >= 0 (time-major tensors, slices of a
+ * fused projection, and inputs broadcast with stride 0 are all views of this
+ * kind).  An output must not hold an element twice, and outputs may interleave
+ * only as slices of one buffer with equal env and step strides. */
+typedef struct rlscan_heads {
+  void *data;
+  int64_t env, step, head;
+} rlscan_heads;
+
+/* Largest K and V of the linear-attention entries. */
+#define RLSCAN_MAX_HEAD_DIM 128
+
+/* Linear attention with a decay for each head, over whole rows:
+ *   S_t = a_t S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t,   a_t = exp(g_t),
+ * S [K, V] for each row and head.  This is the generic recurrence
+ * x_t = a_t x_{t-1} + b_t with b_t = k_t v_t^T, cut into episodes like
+ * rlscan_linear_scan_segmented: the step after one flagged in `done` starts
+ * from a zero state.  Rows of several sequences of different lengths are packed
+ * the same way.  g_t below -104 (exp(g_t) is 0 in float32), -inf included, also
+ * starts afresh.
+ * In:  q [E,T,H,K], k [E,T,Hkv,K], v [E,T,Hkv,V] in fmt, H a multiple of Hkv
+ *      (query head h reads key/value head h / (H/Hkv));
+ *      log_decay, float32: g [E,T,H] in the layout if per_step, else [H];
+ *      done [E,T] in the layout (optional);
+ *      init_state [E,H,K,V] (optional), S_{-1}.
+ * Out: out [E,T,H,V] in fmt, rounded once from float32;
+ *      final_state [E,H,K,V] (optional): the state that the next window takes
+ *      as init_state, zero where the row's last step is flagged.
+ * Products run in bfloat16 matrix instructions on operands split into as many
+ * bfloat16 terms as fmt needs, with float32 sums; states stay in float32.
+ * 1 <= K, V <= RLSCAN_MAX_HEAD_DIM.  With T = 0 the state is passed through. */
+int64_t rlscan_linear_attention_workspace(rlscan_format fmt, int64_t E, int64_t T, int64_t H, int64_t Hkv, int64_t K,
+                                          int64_t V, int backward, int per_step);
+
+rlscan_status rlscan_linear_attention(rlscan_format fmt, rlscan_layout layout, const rlscan_heads *q,
+                                      const rlscan_heads *k, const rlscan_heads *v, const float *log_decay,
+                                      int per_step, const uint8_t *done, const float *init_state,
+                                      const rlscan_heads *out, float *final_state, void *workspace,
+                                      int64_t workspace_bytes, int64_t E, int64_t T, int64_t H, int64_t Hkv,
+                                      int64_t K, int64_t V, float scale, hipStream_t stream);
+
+/* Gradients of rlscan_linear_attention.
+ * In:  d_out [E,T,H,V], the gradient of out; the forward call's inputs;
+ *      d_final_state [E,H,K,V] (optional), the gradient of final_state.
+ * Out: dq, dk, dv like q, k, v (dk and dv summed over the heads of a group);
+ *      d_log_decay like log_decay; d_init_state [E,H,K,V] (optional).
+ * A decay that starts afresh has gradient 0.  Every sum has a fixed order:
+ * results do not vary from run to run. */
+rlscan_status rlscan_linear_attention_backward(
+    rlscan_format fmt, rlscan_layout layout, const rlscan_heads *d_out, const rlscan_heads *q, const rlscan_heads *k,
+    const rlscan_heads *v, const float *log_decay, int per_step, const uint8_t *done, const float *init_state,
+    const float *d_final_state, const rlscan_heads *dq, const rlscan_heads *dk, const rlscan_heads *dv,
+    float *d_log_decay, float *d_init_state, void *workspace, int64_t workspace_bytes, int64_t E, int64_t T, int64_t H,
+    int64_t Hkv, int64_t K, int64_t V, float scale, hipStream_t stream);
+
+/* The same recurrence for one step of E rows, on states kept from call to call
+ * and updated in place.
+ * In:  q [E,H,K], k [E,Hkv,K], v [E,Hkv,V] (rlscan_heads with step unused);
+ *      log_decay [E,H] if per_row, else [H];
+ *      reset [E] (optional): rows whose previous step ended an episode; their
+ *      state is dropped unread, so it may hold anything;
+ *      slots [E] int32 (optional): row e's state is state[slots[e]], else
+ *      state[e].  A row whose slot is outside [0, S) has no state: its output is
+ *      0 and nothing is written.  Two rows of one call must not share a slot.
+ * In/out: state [S,H,K,V] float32.
+ * Out: out [E,H,V]. */
+rlscan_status rlscan_linear_attention_step(rlscan_format fmt, const rlscan_heads *q, const rlscan_heads *k,
+                                           const rlscan_heads *v, const float *log_decay, int per_row,
+                                           const uint8_t *reset, const int32_t *slots, float *state,
+                                           const rlscan_heads *out, int64_t E, int64_t S, int64_t H, int64_t Hkv,
+                                           int64_t K, int64_t V, float scale, hipStream_t stream);
+
+/* One action for each row of logits, from given uniform numbers.
+ * Logits whose mask byte is 0, and those that are -inf or NaN, are not legal.  In
+ * the order of falling logits (equal ones: lower index first), with weights
+ * w_i = exp((x_i - max) / temperature), a row keeps its first top_k, of those
+ * the shortest prefix whose weight is at least top_p of theirs, and of those the
+ * ones with w_i >= min_p.  The action is the first kept index, in the order of
+ * the indices, at which the running weight passes uniforms[r] * (kept weight).
+ * Weights are whole multiples of 2^-43 (float64, rounded once), so an action does not
+ * depend on the order of any sum.
+ * In:  logits [R,N] in fmt, rows `stride` elements apart; mask [R,N]
+ *      contiguous (optional); uniforms [R] in [0,1);
+ *      temperatures, top_ks, top_ps, min_ps [R]: a row's own settings, or NULL
+ *      for the value given for all rows.  temperature 0 takes the largest logit
+ *      (as does a row whose own one is negative or NaN); top_k 0 (or N or more,
+ *      in rows also negative), top_p >= 1 and min_p 0 are off; at least the
+ *      largest logit is always kept.
+ * Out: actions [R] int64, -1 for a row without a legal action;
+ *      log_probs [R] (optional): log-probability under the kept weights, 0 for a
+ *      row without one.
+ * 1 <= N <= 2^20, R < 2^22. */
+rlscan_status rlscan_sample_actions(rlscan_format fmt, const void *logits, int64_t stride, const uint8_t *mask,
+                                    const float *uniforms, const float *temperatures, const int32_t *top_ks,
+                                    const float *top_ps, const float *min_ps, float temperature, int32_t top_k,
+                                    float top_p, float min_p, int64_t *actions, float *log_probs, int64_t R, int64_t N,
+                                    hipStream_t stream);
+
+/* Log-probability of the taken action and entropy of softmax(logits /
+ * temperature) over the legal actions of each row.
+ * In:  logits, mask as above; actions [R] int64: one outside [0,N) (a padded
+ *      step) has log-probability 0 and no gradient, an illegal one -inf;
+ *      temperature > 0.
+ * Out: log_probs [R], entropies [R]; lse [R] float64: log of the sum of exp(x /
+ *      temperature), for the backward call.  A row without a legal action has 0, 0
+ *      and -inf.  A NaN among legal logits gives NaN. */
+int64_t rlscan_action_log_probs_workspace(int64_t R, int64_t N);
+
+rlscan_status rlscan_action_log_probs(rlscan_format fmt, const void *logits, int64_t stride, const uint8_t *mask,
+                                      const int64_t *actions, float temperature, float *log_probs, float *entropies,
+                                      double *lse, void *workspace, int64_t workspace_bytes, int64_t R, int64_t N,
+                                      hipStream_t stream);
+
+/* Gradient of the logits:
+ *   d_x_j = (d_lp (1[j = a] - p_j) - d_H p_j (log p_j + H)) / temperature,
+ * 0 where not legal.  d_log_probs, d_entropies [R] (optional: 0); lse and
+ * entropies from the forward call; d_logits [R,N] in fmt, rows d_stride apart. */
+rlscan_status rlscan_action_log_probs_backward(rlscan_format fmt, const float *d_log_probs, const float *d_entropies,
+                                               const void *logits, int64_t stride, const uint8_t *mask,
+                                               const int64_t *actions, float temperature, const double *lse,
+                                               const float *entropies, void *d_logits, int64_t d_stride, int64_t R,
+                                               int64_t N, hipStream_t stream);
 
 #ifdef __cplusplus
 } /* extern "C" */

@@ -28,6 +28,8 @@ __all__ = [
     "discounted_returns", "td_lambda", "returns_and_td_lambda", "gae", "vtrace", "retrace",
     "eligibility_traces", "eligibility_traces_vec", "episodic_prefix_sum", "linear_scan",
     "linear_scan_segmented",
+    "linear_attention", "linear_attention_backward", "linear_attention_step",
+    "sample_actions", "action_log_probs", "action_log_probs_backward",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -62,6 +64,21 @@ for _n in _EX + ("rlscan_linear_scan_segmented", "rlscan_eligibility_traces_vec"
     _SIGNATURES[_n + "_ex"] = [_int, _int] + _SIGNATURES[_n]
 del _n
 
+_SIGNATURES.update({
+    "rlscan_linear_attention": [_int, _int] + [_vp] * 4 + [_int] + [_vp] * 5 + [_i64] * 7 + [_f32, _vp],
+    "rlscan_linear_attention_backward": [_int, _int] + [_vp] * 5 + [_int] + [_vp] * 9 + [_i64] * 7 + [_f32, _vp],
+    "rlscan_linear_attention_step": [_int] + [_vp] * 4 + [_int] + [_vp] * 4 + [_i64] * 6 + [_f32, _vp],
+    "rlscan_sample_actions": [_int, _vp, _i64] + [_vp] * 6 + [_f32, _int, _f32, _f32, _vp, _vp, _i64, _i64, _vp],
+    "rlscan_action_log_probs": [_int, _vp, _i64, _vp, _vp, _f32] + [_vp] * 4 + [_i64] * 3 + [_vp],
+    "rlscan_action_log_probs_backward": [_int, _vp, _vp, _vp, _i64, _vp, _vp, _f32, _vp, _vp, _vp, _i64, _i64, _i64,
+                                         _vp],
+})
+# Workspace sizes in bytes (-1: refused).
+_SIZES = {
+    "rlscan_linear_attention_workspace": [_int] + [_i64] * 6 + [_int, _int],
+    "rlscan_action_log_probs_workspace": [_i64, _i64],
+}
+
 # rlscan_format codes by storage dtype name
 _FORMATS = {"float32": 0, "bfloat16": 1, "float16": 2}
 
@@ -93,6 +110,10 @@ def lib() -> ctypes.CDLL:
             fn = getattr(handle, name)
             fn.argtypes = args
             fn.restype = ctypes.c_int
+        for name, args in _SIZES.items():
+            fn = getattr(handle, name)
+            fn.argtypes = args
+            fn.restype = _i64
         handle.rlscan_status_string.argtypes = [ctypes.c_int]
         handle.rlscan_status_string.restype = ctypes.c_char_p
         handle.rlscan_version.argtypes = []
@@ -433,3 +454,17 @@ def eligibility_traces_vec(x, terminated=None, truncated=None, init=None, *, gam
             _stream(dev, stream))
     _entry("rlscan_eligibility_traces_vec", dt, time_major, *args)
     return out
+
+
+# ----------------------------------------------------------------- policy operators
+_POLICY = ("linear_attention", "linear_attention_backward", "linear_attention_step", "sample_actions",
+           "action_log_probs", "action_log_probs_backward")
+
+
+def __getattr__(name):
+    if name in _POLICY:  # loaded on first use: the module imports torch
+        from . import policy
+        for n in _POLICY:
+            globals()[n] = getattr(policy, n)
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))

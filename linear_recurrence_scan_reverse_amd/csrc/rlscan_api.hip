@@ -444,6 +444,7 @@ const char* rlscan_status_string(rlscan_status s) {
     case RLSCAN_ERR_HIP: return "HIP kernel launch failed";
     case RLSCAN_ERR_ALIGN: return "a value pointer is not aligned to its element size";
     case RLSCAN_ERR_ALIAS: return "an output overlaps an input or another output";
+    case RLSCAN_ERR_WORKSPACE: return "the workspace is smaller than the call needs";
   }
   return "unknown status";
 }
