@@ -403,7 +403,7 @@ typedef struct rlscan_heads {
  * bfloat16 terms as fmt needs, with float32 sums; states stay in float32.
  * 1 <= K, V <= RLSCAN_MAX_HEAD_DIM.  With T = 0 the state is passed through. */
 int64_t rlscan_linear_attention_workspace(rlscan_format fmt, int64_t E, int64_t T, int64_t H, int64_t Hkv, int64_t K,
-                                          int64_t V, int backward, int per_step);
+                                          int64_t V, int backward);
 
 rlscan_status rlscan_linear_attention(rlscan_format fmt, rlscan_layout layout, const rlscan_heads *q,
                                       const rlscan_heads *k, const rlscan_heads *v, const float *log_decay,

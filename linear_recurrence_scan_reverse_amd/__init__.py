@@ -75,7 +75,7 @@ _SIGNATURES.update({
 })
 # Workspace sizes in bytes (-1: refused).
 _SIZES = {
-    "rlscan_linear_attention_workspace": [_int] + [_i64] * 6 + [_int, _int],
+    "rlscan_linear_attention_workspace": [_int] + [_i64] * 6 + [_int],
     "rlscan_action_log_probs_workspace": [_i64, _i64],
 }
 

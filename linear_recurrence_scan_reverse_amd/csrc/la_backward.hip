@@ -1,404 +1,266 @@
 // Gradients of linear attention (rlscan_linear_attention_backward).
 //
-// With dS the gradient of the state leaving a chunk and S the state entering it,
-// a chunk's gradients need nothing else from the rest of the row:
-//   dP_ij = scale exp(b_i - b_j) (do_i . v_j)
-//   dq_i  = sum_j dP_ij k_j + entry_i S do_i
-//   dk_j  = sum_i dP_ij q_i + leave_j dS v_j
-//   dv_j  = sum_i P_ij do_i + leave_j dS^T k_j
-// and for the log-decay of step t, every product of decays that holds a_t:
-//   dg_t  = sum_{j<t<=i} (q_i . k_j) dP_ij + sum_{i>=t} X_i + sum_{j<t} Y_j + across <S, dS>,
-//   X_i   = q_i . (entry_i S do_i),  Y_j = k_j . (leave_j dS v_j).
-// The textbook running sum of q.dq - k.dk over the rest of the row gives the same
-// number, but cancels over the row's length; this form only ever sums over one chunk.
-//
-// walk_kernel first leaves S and dS of every chunk in the workspace (both
-// directions), then every chunk runs by itself: one block per row, key/value head and chunk, which
-// adds up dk and dv over the heads of the group in registers, in a fixed order.
-#include "rlscan_la_walk.hpp"
+// dq, dk and dv are each a chunk walk of their own (rlscan_la_attend.hpp) with the state or
+// its gradient in registers; the three run side by side in one launch, the blocks of one
+// head next to each other on one XCD, whose L2 they share.  The log-decay's gradient follows from
+// b_t, the running sum of g up to t: every product of decays is exp(b_i - b_j), so
+//   dL/db_i = q_i . dq_i - k_i . dk_i  (without the i = j terms, which hold no decay),
+//   dg_t    = sum of dL/db_i over the i >= t of t's episode, plus <S, dS> behind the last one
+//             (of both, the part of k and v at T-1 holds no decay and is left out).
+// Both dot products are taken from the float32 sums before dq and dk are rounded, from
+// operands of float32 precision, in float64: their differences are small against them.
+// So that their rounding does not add up over a row, some boundaries between chunks are
+// marked: there the walks leave S and dS, and the sum starts anew from dg = <S, dS>.
+#include "rlscan_la_attend.hpp"
 #include "rlscan_la_launch.hpp"
+#include "rlscan_la_walk.hpp"
 
 namespace rlscan {
 namespace la {
 
-template <class F, int KP, int VP, int C>
+template <class F, int KP, int VP, int C, int NWV>
 struct BackwardLds {
-  Tile<F::NT, C, KP> q, k;
-  Tile<F::NT, C, VP> v, dout;
-  Tile<F::NP, C, C> p, dp;    // row i, column j
-  Decay<C> dec;
-  float row[C / 16][C];       // sum over the j of one tile of pair_ij, j < i
-  float column[C / 16][C];    // sum over the i of one tile of pair_ij
-  float x[kWaves][C];         // parts of X and Y
-  float y[kWaves][C];
-  float z[kWaves];            // parts of <S, dS>
+  union {
+    AttendLds<F, VP, KP, C, NWV, true> k;   // dq and dk
+    AttendLds<F, KP, VP, C, NWV, false> v;  // dv
+  };
 };
 
-__device__ __forceinline__ float sum_groups(float x) {  // over the 4 lane groups of a column
-  x += __shfl_xor(x, 16);
-  x += __shfl_xor(x, 32);
-  return x;
-}
-
-__device__ __forceinline__ float sum_columns(float x) {  // over the 16 lanes of a group
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) x += __shfl_xor(x, o);
-  return x;
-}
-
-// 8 consecutive floats.
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const f32x4 a = *reinterpret_cast<const f32x4*>(p);
-  const f32x4 b = *reinterpret_cast<const f32x4*>(p + 4);
-#pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    x[s] = a[s];
-    x[4 + s] = b[s];
+// FO: the format that dk and dv are left in (float32 scratch where heads share them).
+template <class F, class FO, int KP, int VP, int C, int NWV, int MINW, bool VEC>
+__global__ void __launch_bounds__(64 * NWV, MINW) backward_kernel(const Args a, const Attend q, const Attend k, const Attend v) {
+  __shared__ char lds[sizeof(BackwardLds<F, KP, VP, C, NWV>)] __attribute__((aligned(16)));
+  auto& s = *reinterpret_cast<BackwardLds<F, KP, VP, C, NWV>*>(lds);
+  const int64_t items = a.E * a.H * a.nseg;
+  const int64_t item = blockIdx.x / 24 * 8 + blockIdx.x % 8;
+  if (item >= items) return;
+  const int64_t eh = item % (a.E * a.H), seg = item / (a.E * a.H);
+  switch (blockIdx.x % 24 / 8) {
+    case 0: attend<F, F, VP, KP, C, NWV, false, true, F::NW, VEC>(s.k, a, q, eh, seg, 0); break;
+    case 1: attend<F, FO, VP, KP, C, NWV, true, true, F::NW, VEC>(s.k, a, k, eh, seg, 0); break;
+    default: attend<F, FO, KP, VP, C, NWV, true, false, F::NP, VEC>(s.v, a, v, eh, seg, 0); break;
   }
 }
 
-// Four consecutive columns of an LDS row, as floats.
-template <int N, int R, int D>
-__device__ __forceinline__ void get4(const Tile<N, R, D>& t, int row, int col, float (&x)[4]) {
-  const int o = row * Tile<N, R, D>::LD + col;
+// dg of one row and head: x_t = u_t - w_t summed from the end, afresh at each episode's last step.
+// A thread takes four steps; the sums of those behind it pass through the wave and the block.
+__global__ void __launch_bounds__(256) decay_grad_kernel(const Args a, const double* u, const double* w, const float* end,
+                                                         const double* mark_dots, int64_t nmarks, int64_t mark_steps,
+                                                         double* total) {
+  __shared__ double sum[4];
+  __shared__ int open[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t eh = blockIdx.x, e = eh / a.H, h = eh % a.H;
+  u += eh * a.T;
+  w += eh * a.T;
+  mark_dots += eh * nmarks;
+  double carry = (double)end[eh];  // what comes from behind the tile
+  double all = 0.0;
+  const int64_t tiles = (a.T + 1023) / 1024;
+  for (int64_t n = tiles - 1; n >= 0; --n) {
+    const int64_t t0 = n * 1024 + (int64_t)(255 - tid) * 4;  // later steps in earlier lanes
+    // this thread's steps from the last: R = x_t + (step t+1 starts afresh ? 0 : R)
+    double x[4];
+    bool cut[4];  // step t starts afresh: its own gradient is 0 and nothing passes to t-1
+    bool mark[4];
+    double anew[4];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) x[r] = 0.0f;
-#pragma unroll
-  for (int n = N - 1; n >= 0; --n) {
-    const bf16x4 w = *reinterpret_cast<const bf16x4*>(&t.p[n][o]);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) x[r] += (float)w[r];
-  }
-}
-
-template <class F, int KP, int VP, int C>
-__global__ void __launch_bounds__(kThreads) backward_kernel(const Args a) {
-  constexpr int NT = F::NT, NP = F::NP, NW = F::NW, CT = C / 16, CC = C / 32;
-  constexpr int KW = (KP / 16 + kWaves - 1) / kWaves, VW = (VP / 16 + kWaves - 1) / kWaves;
-  constexpr bool kWhole = C == 64;  // a wave has a whole row of P tiles, or one tile of four
-  __shared__ BackwardLds<F, KP, VP, C> s;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, col = lane & 15, grp = lane >> 4;
-  const int64_t Hkv = a.H / a.G;
-  const int64_t ehk = blockIdx.x / a.chunks, c = blockIdx.x % a.chunks;
-  const int64_t e = ehk / Hkv, hk = ehk % Hkv;
-  const int64_t t0 = c * C;
-  using El = typename F::E;
-
-  {
-    Piece<F> rk[Share<C, KP>::n], rv[Share<C, VP>::n];
-    fetch<F, C, KP>(a.k, e, hk, t0, a.T, 0, a.K, tid, rk);
-    fetch<F, C, VP>(a.v, e, hk, t0, a.T, 0, a.V, tid, rv);
-    stage<F, C, KP>(s.k, rk, tid);
-    stage<F, C, VP>(s.v, rv, tid);
-  }
-  f32x4 dk[KW][CT], dv[VW][CT];
-#pragma unroll
-  for (int n = 0; n < KW; ++n)
-#pragma unroll
-    for (int jt = 0; jt < CT; ++jt) dk[n][jt] = f32x4{0, 0, 0, 0};
-#pragma unroll
-  for (int n = 0; n < VW; ++n)
-#pragma unroll
-    for (int jt = 0; jt < CT; ++jt) dv[n][jt] = f32x4{0, 0, 0, 0};
-
-  for (int64_t u = 0; u < a.G; ++u) {
-    const int64_t h = hk * a.G + u, eh = e * a.H + h;
-    {
-      Piece<F> rq[Share<C, KP>::n], rd[Share<C, VP>::n];
-      fetch<F, C, KP>(a.q, e, h, t0, a.T, 0, a.K, tid, rq);
-      fetch<F, C, VP>(a.dout, e, h, t0, a.T, 0, a.V, tid, rd);
-      stage<F, C, KP>(s.q, rq, tid);
-      stage<F, C, VP>(s.dout, rd, tid);
+    for (int i = 0; i < 4; ++i) {
+      const int64_t t = t0 + i;
+      x[i] = t < a.T ? u[t] - (t < a.T - 1 ? w[t] : 0.0) : 0.0;
+      cut[i] = false;
+      mark[i] = t > 0 && t < a.T && t % mark_steps == 0;
+      anew[i] = mark[i] ? mark_dots[t / mark_steps - 1] : 0.0;
+      if (t < a.T)
+        cut[i] = a.g[e * a.g_se + t * a.g_st + h * a.g_sh] < kCutBelow ||
+                 (t > 0 && a.done && a.done[e * a.d_se + (t - 1) * a.d_st] != 0);
     }
-    if (w == 0) fill_decay<C>(s.dec, load_decay<C>(a, e, h, t0, lane), a.scale, lane);
-    __syncthreads();
-
-    // ---- P, dP and their part of dg, as transposed tiles (rows j, columns i)
-    {
-      const int it = kWhole ? w : w >> 1;
-      const int i = it * 16 + col;
-      const float hi_i = s.dec.hi[i], lo_i = s.dec.lo[i];
-      const int seg_i = s.dec.seg[i];
+    double own = 0.0;  // sum that leaves towards t0 - 1
+    bool passes = true;
 #pragma unroll
-      for (int m = 0; m < (kWhole ? CT : 1); ++m) {
-        const int jt = kWhole ? m : w & 1;
-        float p[4] = {0, 0, 0, 0}, dp[4] = {0, 0, 0, 0}, pair[4] = {0, 0, 0, 0};
-        if (jt <= it) {
-          f32x4 qk{0, 0, 0, 0}, dov{0, 0, 0, 0};
+    for (int i = 3; i >= 0; --i) {
+      own = mark[i] ? anew[i] : own + x[i];
+      if (cut[i]) own = 0.0;
+      passes &= !(cut[i] || mark[i]);
+    }
+    // inclusive over lanes: (own, passes) of this lane and those before it (later steps)
+    double run = own;
+    int through = passes;
 #pragma unroll
-          for (int kk = 0; kk < KP / 32; ++kk)
-            qk = mma(frag_row<NT, C, KP>(s.k, jt * 16, kk, lane), frag_row<NT, C, KP>(s.q, it * 16, kk, lane), qk);
-#pragma unroll
-          for (int vv = 0; vv < VP / 32; ++vv)
-            dov = mma(frag_row<NT, C, VP>(s.v, jt * 16, vv, lane), frag_row<NT, C, VP>(s.dout, it * 16, vv, lane), dov);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int j = jt * 16 + grp * 4 + r;
-            const float d = a.scale * between<C>(s.dec, hi_i, lo_i, seg_i, i, j);
-            p[r] = qk[r] * d;
-            dp[r] = dov[r] * d;
-            pair[r] = j < i ? qk[r] * dp[r] : 0.0f;
-          }
-        }
-        put4<NP, C, C>(s.p, i, jt * 16 + grp * 4, p);
-        put4<NP, C, C>(s.dp, i, jt * 16 + grp * 4, dp);
-        const float row = sum_groups((pair[0] + pair[1]) + (pair[2] + pair[3]));
-        if (grp == 0) s.row[jt][i] = row;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float column = sum_columns(pair[r]);
-          if (col == 0) s.column[it][jt * 16 + grp * 4 + r] = column;
-        }
+    for (int o = 1; o < 64; o <<= 1) {
+      const double b = __shfl_up(run, o);
+      const int p = __shfl_up(through, o);
+      if (lane >= o) {
+        run += through ? b : 0.0;
+        through &= p;
       }
+    }
+    if (lane == 63) {
+      sum[wave] = run;
+      open[wave] = through;
     }
     __syncthreads();
-
-    const float* S = a.states + (eh * a.chunks + c) * (int64_t)(KP * VP);
-    const float* dS = a.grads + (eh * a.chunks + c) * (int64_t)(KP * VP);
-
-    // ---- dq and dk: wave w has the tiles w, w + 4 of K.  Transposed: rows k, columns i or j
-    float xs[CT], ys[CT], z = 0.0f;
-#pragma unroll
-    for (int n = 0; n < CT; ++n) xs[n] = ys[n] = 0.0f;
-#pragma unroll
-    for (int n = 0; n < KW; ++n) {
-      const int kt = n * kWaves + w;
-      if (kt >= KP / 16) break;
-      f32x4 dq[CT], in[CT];
-#pragma unroll
-      for (int it = 0; it < CT; ++it) dq[it] = in[it] = f32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int vv = 0; vv < VP / 32; ++vv) {
-        float x[8], y[8];
-        load8(S + (kt * 16 + col) * VP + vv * 32 + grp * 8, x);
-        load8(dS + (kt * 16 + col) * VP + vv * 32 + grp * 8, y);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) z += x[i] * y[i];
-        const Frag<NW> fs = split<NW>(x), fd = split<NW>(y);
-#pragma unroll
-        for (int it = 0; it < CT; ++it) {
-          dq[it] = mma(fs, frag_row<NT, C, VP>(s.dout, it * 16, vv, lane), dq[it]);
-          in[it] = mma(fd, frag_row<NT, C, VP>(s.v, it * 16, vv, lane), in[it]);
-        }
-      }
-#pragma unroll
-      for (int it = 0; it < CT; ++it) {
-        const int row = it * 16 + col;
-        float q[4], k[4];
-        get4<NT, C, KP>(s.q, row, kt * 16 + grp * 4, q);
-        get4<NT, C, KP>(s.k, row, kt * 16 + grp * 4, k);
-        dq[it] *= s.dec.entry[row];
-        in[it] *= s.dec.leave[row];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          xs[it] += q[r] * dq[it][r];
-          ys[it] += k[r] * in[it][r];
-        }
-        dk[n][it] += in[it];
-      }
-#pragma unroll
-      for (int jj = 0; jj < CC; ++jj) {
-        const Frag<NT> fk = frag_col<NT, C, KP>(s.k, kt * 16, jj, lane);
-        const Frag<NT> fq = frag_col<NT, C, KP>(s.q, kt * 16, jj, lane);
-#pragma unroll
-        for (int it = 0; it < CT; ++it) {
-          if (jj <= it / 2) dq[it] = mma(fk, frag_row<NP, C, C>(s.dp, it * 16, jj, lane), dq[it]);
-          if (jj >= it / 2) dk[n][it] = mma(fq, frag_col<NP, C, C>(s.dp, it * 16, jj, lane), dk[n][it]);
-        }
-      }
-#pragma unroll
-      for (int it = 0; it < CT; ++it) {
-        const int64_t t = t0 + it * 16 + col;
-        if (t < a.T) {
-          const float x[4] = {dq[it][0], dq[it][1], dq[it][2], dq[it][3]};
-          store4<F>(static_cast<El*>(const_cast<void*>(a.dq.p)) + e * a.dq.se + h * a.dq.sh + t * a.dq.st,
-                    kt * 16 + grp * 4, a.K, a.dq.vec, x);
-        }
-      }
-    }
-#pragma unroll
-    for (int it = 0; it < CT; ++it) {
-      xs[it] = sum_groups(xs[it]);
-      ys[it] = sum_groups(ys[it]);
-      if (grp == 0) {
-        s.x[w][it * 16 + col] = xs[it];
-        s.y[w][it * 16 + col] = ys[it];
-      }
-    }
-    z = sum_columns(sum_groups(z));
-    if (lane == 0) s.z[w] = z;
-
-    // ---- dv: wave w has the tiles w, w + 4 of V.  Transposed: rows v, columns j
-#pragma unroll
-    for (int n = 0; n < VW; ++n) {
-      const int vt = n * kWaves + w;
-      if (vt >= VP / 16) break;
-      f32x4 in[CT];
-#pragma unroll
-      for (int jt = 0; jt < CT; ++jt) in[jt] = f32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int kk = 0; kk < KP / 32; ++kk) {
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = dS[(kk * 32 + grp * 8 + i) * VP + vt * 16 + col];
-        const Frag<NP> fd = split<NP>(y);  // feeds dv alone: that output's precision
-#pragma unroll
-        for (int jt = 0; jt < CT; ++jt) in[jt] = mma(fd, frag_row<NT, C, KP>(s.k, jt * 16, kk, lane), in[jt]);
-      }
-#pragma unroll
-      for (int jt = 0; jt < CT; ++jt) {
-        const float leave = s.dec.leave[jt * 16 + col];
-        dv[n][jt] += in[jt] * leave;
-      }
-#pragma unroll
-      for (int ii = 0; ii < CC; ++ii) {
-        const Frag<NT> fo = frag_col<NT, C, VP>(s.dout, vt * 16, ii, lane);
-#pragma unroll
-        for (int jt = 0; jt < CT; ++jt)
-          if (ii >= jt / 2) dv[n][jt] = mma(fo, frag_col<NP, C, C>(s.p, jt * 16, ii, lane), dv[n][jt]);
-      }
-    }
+    double in = carry;
+    for (int i = 0; i < wave; ++i) in = sum[i] + (open[i] ? in : 0.0);
+    const double before = __shfl_up(run, 1);
+    const int before_through = __shfl_up(through, 1);
+    double r = lane == 0 ? in : before + (before_through ? in : 0.0);
+    for (int i = wave; i < 4; ++i) in = sum[i] + (open[i] ? in : 0.0);
+    carry = in;
     __syncthreads();
-
-    // ---- dg: the first wave adds up the chunk's parts, in float64
-    if (w == 0) {
-      double back = 0.0, y = 0.0;  // summed over i >= t, and over j < t
-      if (lane < C) {
 #pragma unroll
-        for (int n = 0; n < CT; ++n) back += (double)s.row[n][lane] - (double)s.column[n][lane];
-#pragma unroll
-        for (int n = 0; n < kWaves; ++n) {
-          if (n < KP / 16) {
-            back += (double)s.x[n][lane];
-            y += (double)s.y[n][lane];
-          }
-        }
+    for (int i = 3; i >= 0; --i) {
+      r = mark[i] ? anew[i] : r + x[i];
+      const double g = cut[i] ? 0.0 : r;
+      if (cut[i]) r = 0.0;
+      const int64_t t = t0 + i;
+      if (t < a.T) {
+        all += g;
+        if (!total) a.dg[e * a.dg_se + t * a.dg_st + h * a.dg_sh] = (float)g;
       }
-      const double own = y;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const double b = __shfl_down(back, o), f = __shfl_up(y, o);
-        if (lane + o < 64) back += b;
-        if (lane >= o) y += f;
-      }
-      double zz = 0.0;
-#pragma unroll
-      for (int n = 0; n < kWaves; ++n) zz += (double)s.z[n];
-      const double g = back + (y - own) + (double)s.dec.across * zz;
-      const int64_t t = t0 + lane;
-      if (lane < C && t < a.T)
-        a.dg[e * a.dg_se + t * a.dg_st + h * a.dg_sh] = (s.dec.cuts >> lane & 1) ? 0.0f : (float)g;
-    }
-    __syncthreads();
-  }
-
-#pragma unroll
-  for (int n = 0; n < KW; ++n) {
-    const int kt = n * kWaves + w;
-    if (kt >= KP / 16) break;
-#pragma unroll
-    for (int jt = 0; jt < CT; ++jt) {
-      const int64_t t = t0 + jt * 16 + col;
-      if (t >= a.T) continue;
-      const float x[4] = {dk[n][jt][0], dk[n][jt][1], dk[n][jt][2], dk[n][jt][3]};
-      store4<F>(static_cast<El*>(const_cast<void*>(a.dk.p)) + e * a.dk.se + hk * a.dk.sh + t * a.dk.st,
-                kt * 16 + grp * 4, a.K, a.dk.vec, x);
     }
   }
+  if (!total) return;
 #pragma unroll
-  for (int n = 0; n < VW; ++n) {
-    const int vt = n * kWaves + w;
-    if (vt >= VP / 16) break;
-#pragma unroll
-    for (int jt = 0; jt < CT; ++jt) {
-      const int64_t t = t0 + jt * 16 + col;
-      if (t >= a.T) continue;
-      const float x[4] = {dv[n][jt][0], dv[n][jt][1], dv[n][jt][2], dv[n][jt][3]};
-      store4<F>(static_cast<El*>(const_cast<void*>(a.dv.p)) + e * a.dv.se + hk * a.dv.sh + t * a.dv.st,
-                vt * 16 + grp * 4, a.V, a.dv.vec, x);
-    }
-  }
-}
-
-// The gradient of one log-decay for each head: the sum over rows and steps, in
-// float64 and in a fixed order.
-__global__ void __launch_bounds__(256) head_sum_kernel(const float* dg, float* out, int64_t rows, int64_t H) {
-  __shared__ double part[256];
-  const int64_t h = blockIdx.x;
-  double x = 0.0;
-  for (int64_t i = threadIdx.x; i < rows; i += 256) x += (double)dg[i * H + h];
-  part[threadIdx.x] = x;
+  for (int o = 1; o < 64; o <<= 1) all += __shfl_xor(all, o);
+  if (lane == 0) sum[wave] = all;
   __syncthreads();
-  for (int o = 128; o > 0; o >>= 1) {
-    if ((int)threadIdx.x < o) part[threadIdx.x] += part[threadIdx.x + o];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) out[h] = (float)part[0];
+  if (tid == 0) total[eh] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
 
-template <class F, int KP, int C, bool REV>
-void walk(const Args& a, const Plan& pl, hipStream_t st) {
-  const int64_t heads = a.E * a.H * (pl.VP / 64);
-  if (heads == 0) return;
-  WalkArgs w{};
-  w.a = a;
-  w.VP = pl.VP;
-  float* seg = REV ? a.seg_grad : a.seg_state;
-  float* decay = REV ? a.seg_gdecay : a.seg_decay;
-  const float* given = REV ? a.d_final : a.init;
-  if (pl.nseg > 1) {
-    w.seg_end = seg;
-    w.seg_decay = decay;
-    walk_kernel<F, KP, C, REV><<<dim3((unsigned)(heads * pl.nseg)), kThreads, 0, st>>>(w);
-    CombineArgs c{};
-    c.seg = seg;
-    c.decay = decay;
-    c.given = given;
-    c.done = a.done;
-    c.d_se = a.d_se;
-    c.d_st = a.d_st;
-    c.H = a.H;
-    c.T = a.T;
-    c.nseg = pl.nseg;
-    c.KP = KP;
-    c.VP = pl.VP;
-    c.K = a.K;
-    c.V = a.V;
-    c.closed = REV;
-    combine_kernel<<<dim3((unsigned)(a.E * a.H * ((KP * pl.VP + 255) / 256))), 256, 0, st>>>(c);
-    w.seg_end = nullptr;
-    w.seg_decay = nullptr;
-    w.enter = seg;
+// <S, dS> at one marked boundary, in float64 and in a fixed order.
+__global__ void __launch_bounds__(256) mark_dot_kernel(const float* s, const float* ds, double* out, int64_t n) {
+  __shared__ double part[4];
+  const int64_t base = (int64_t)blockIdx.x * n;
+  double x = 0.0;
+  for (int64_t i = threadIdx.x * 4; i < n; i += 1024) {
+    const f32x4 p = *reinterpret_cast<const f32x4*>(s + base + i), q = *reinterpret_cast<const f32x4*>(ds + base + i);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x += (double)p[k] * (double)q[k];
   }
-  w.given = given;
-  w.each = REV ? a.grads : a.states;
-  w.end = REV ? a.d_init : nullptr;
-  walk_kernel<F, KP, C, REV><<<dim3((unsigned)(heads * pl.nseg)), kThreads, 0, st>>>(w);
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
+  __syncthreads();
+  if (threadIdx.x == 0) out[blockIdx.x] = (part[0] + part[1]) + (part[2] + part[3]);
 }
 
-template <class F, int KP, int C>
-hipError_t launch_backward_as(Args a, const Plan& pl, float* dg_head, hipStream_t st) {
-  walk<F, KP, C, false>(a, pl, st);
-  walk<F, KP, C, true>(a, pl, st);
-  const int64_t blocks = a.E * (a.H / a.G) * a.chunks;
-  if (blocks > 0) {
-    if (pl.VP == 64) backward_kernel<F, KP, 64, C><<<dim3((unsigned)blocks), kThreads, 0, st>>>(a);
-    else backward_kernel<F, KP, 128, C><<<dim3((unsigned)blocks), kThreads, 0, st>>>(a);
+// One log-decay for each head: its gradient is the sum over the rows.
+__global__ void __launch_bounds__(64) head_sum_kernel(const double* total, float* out, int64_t E, int64_t H) {
+  double x = 0.0;
+  for (int64_t e = threadIdx.x; e < E; e += 64) x += total[e * H + blockIdx.x];
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o);
+  if (threadIdx.x == 0) out[blockIdx.x] = (float)x;
+}
+
+// Adds up the heads of a group, in order: from [E, T, H, D] float32 to out's [E, T, H / G, D].
+template <class F>
+__global__ void __launch_bounds__(256) group_sum_kernel(const Args a, const float* from, const View out, int D) {
+  const int64_t Hkv = a.H / a.G;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t d = i % D, hk = i / D % Hkv, et = i / D / Hkv;
+  if (et >= a.E * a.T) return;
+  const float* p = from + (et * a.H + hk * a.G) * D + d;
+  float x = p[0];
+  for (int64_t n = 1; n < a.G; ++n) x += p[n * D];
+  const int64_t e = et / a.T, t = et % a.T;
+  auto* to = static_cast<typename F::E*>(const_cast<void*>(out.p)) + e * out.se + t * out.st + hk * out.sh + d;
+  if constexpr (sizeof(*to) == 4) *to = x;
+  else if constexpr (F::NT == 1) *to = __builtin_bit_cast(uint16_t, (__bf16)x);
+  else *to = __builtin_bit_cast(uint16_t, (_Float16)x);
+}
+
+template <class F, class FO, int KP, int VP, int C, int NWV, int MINW, bool VEC>
+void launch_walks(const Args& a, const Backward& b, const Plan& pl, hipStream_t st) {
+  enter_segments<F, KP, C, false, VEC>(a, VP, a.init, b.seg_state, b.seg_decay, st);
+  enter_segments<F, KP, C, true, VEC>(a, VP, b.d_final, b.seg_grad, b.seg_gdecay, st);
+  const int64_t kv = (int64_t)a.K * a.V, pad = KP * VP;
+  // states as [K][V] in memory, and as the walks with v first take them
+  auto rows_k = [&](const float* p) { return StateView{const_cast<float*>(p), kv, 0, a.V, 1}; };
+  auto rows_v = [&](const float* p) { return StateView{const_cast<float*>(p), kv, 0, 1, a.V}; };
+  Attend q{}, k{}, v{};
+  q.a = a.dout;
+  q.b = a.v;
+  q.c = a.k;
+  q.out = a.dq;
+  q.ga = 1;
+  q.gb = q.gc = a.G;
+  q.A = a.V;
+  q.D = a.K;
+  q.m = a.q;
+  q.gm = 1;
+  q.dot = b.u;
+  q.enter = pl.nseg > 1 ? StateView{b.seg_state, pl.nseg * pad, pad, 1, VP} : rows_v(a.init);
+  q.end = rows_v(b.d_final);
+  q.end_dot = b.end;
+  q.marks = b.marks;
+  q.nmarks = k.nmarks = b.nmarks;
+  k.marks = b.mark_grads;
+  k.a = a.v;
+  k.b = a.dout;
+  k.c = a.q;
+  k.out = b.dk;
+  k.ga = a.G;
+  k.gb = k.gc = 1;
+  k.A = a.V;
+  k.D = a.K;
+  k.m = a.k;
+  k.gm = a.G;
+  k.dot = b.w;
+  k.enter = pl.nseg > 1 ? StateView{b.seg_grad, pl.nseg * pad, pad, 1, VP} : rows_v(b.d_final);
+  k.enter_closed = pl.nseg == 1;  // segments have it from combine_kernel
+  k.leave = rows_v(b.d_init);
+  v.a = a.k;
+  v.b = a.q;
+  v.c = a.dout;
+  v.out = b.dv;
+  v.ga = a.G;
+  v.gb = v.gc = 1;
+  v.A = a.K;
+  v.D = a.V;
+  v.enter = pl.nseg > 1 ? StateView{b.seg_grad, pl.nseg * pad, pad, VP, 1} : rows_k(b.d_final);
+  v.enter_closed = pl.nseg == 1;
+  const int64_t items = a.E * a.H * pl.nseg;
+  backward_kernel<F, FO, KP, VP, C, NWV, MINW, VEC><<<dim3((unsigned)((items + 7) / 8 * 24)), 64 * NWV, 0, st>>>(a, q, k, v);
+}
+
+template <class F, class FO, bool VEC>
+void launch_sizes(const Args& a, const Backward& b, const Plan& pl, hipStream_t st) {
+  if (pl.KP == 64) launch_walks<F, FO, 64, 64, 32, 4, 2, VEC>(a, b, pl, st);
+  else launch_walks<F, FO, 128, 128, F::NT == 1 ? 64 : 32, 8, 2, VEC>(a, b, pl, st);
+}
+
+template <class F>
+hipError_t launch_backward_fmt(const Args& a, const Backward& b, const Plan& pl, hipStream_t st) {
+  if (a.E * a.H > 0) {
+    const bool vec = a.q.vec && a.k.vec && a.v.vec && a.dout.vec && a.dq.vec && b.dk.vec && b.dv.vec;
+    if (a.G > 1) {
+      if (vec) launch_sizes<F, TF32, true>(a, b, pl, st);
+      else launch_sizes<F, TF32, false>(a, b, pl, st);
+    } else {
+      if (vec) launch_sizes<F, F, true>(a, b, pl, st);
+      else launch_sizes<F, F, false>(a, b, pl, st);
+    }
+    if (b.nmarks > 0)
+      mark_dot_kernel<<<dim3((unsigned)(a.E * a.H * b.nmarks)), 256, 0, st>>>(b.marks, b.mark_grads, b.mark_dots, pl.KP * pl.VP);
+    decay_grad_kernel<<<dim3((unsigned)(a.E * a.H)), 256, 0, st>>>(a, b.u, b.w, b.end, b.mark_dots, b.nmarks,
+                                                                   a.mark_chunks * pl.C, b.dg_head ? b.total : nullptr);
+    if (a.G > 1 && a.T > 0) {
+      const int64_t rows = a.E * a.T * (a.H / a.G);
+      group_sum_kernel<F><<<dim3((unsigned)((rows * a.K + 255) / 256)), 256, 0, st>>>(a, static_cast<const float*>(b.dk.p), a.dk, a.K);
+      group_sum_kernel<F><<<dim3((unsigned)((rows * a.V + 255) / 256)), 256, 0, st>>>(a, static_cast<const float*>(b.dv.p), a.dv, a.V);
+    }
   }
-  if (dg_head && a.H > 0) head_sum_kernel<<<dim3((unsigned)a.H), 256, 0, st>>>(a.dg, dg_head, a.E * a.T, a.H);
+  if (b.dg_head) head_sum_kernel<<<dim3((unsigned)a.H), 64, 0, st>>>(b.total, b.dg_head, a.E, a.H);
   return hipGetLastError();
 }
 
-template <class F, int C>
-hipError_t launch_backward_fmt(const Args& a, const Plan& pl, float* dg_head, hipStream_t st) {
-  return pl.KP == 64 ? launch_backward_as<F, 64, C>(a, pl, dg_head, st) : launch_backward_as<F, 128, C>(a, pl, dg_head, st);
-}
-
-hipError_t launch_backward(rlscan_format f, const Args& a, const Plan& pl, float* dg_head, hipStream_t st) {
+hipError_t launch_backward(rlscan_format f, const Args& a, const Backward& b, const Plan& pl, hipStream_t st) {
   switch (f) {
-    case RLSCAN_FORMAT_BF16: return launch_backward_fmt<TBf16, 64>(a, pl, dg_head, st);
-    case RLSCAN_FORMAT_F16: return launch_backward_fmt<TF16, 32>(a, pl, dg_head, st);
-    default: return launch_backward_fmt<TF32, 32>(a, pl, dg_head, st);
+    case RLSCAN_FORMAT_BF16: return launch_backward_fmt<TBf16>(a, b, pl, st);
+    case RLSCAN_FORMAT_F16: return launch_backward_fmt<TF16>(a, b, pl, st);
+    default: return launch_backward_fmt<TF32>(a, b, pl, st);
   }
 }
 

@@ -28,10 +28,10 @@ __global__ void __launch_bounds__(256) step_kernel(const StepArgs a, int64_t nvs
   const int64_t e = eh / a.H, h = eh % a.H, hk = h / a.G;
   const int64_t slot = a.slots ? (int64_t)a.slots[e] : e;
   const int v = (int)vs * VB + cg * 4;
-  typename F::E* out = static_cast<typename F::E*>(a.out) + e * a.o_se + h * a.o_sh;
+  const TileRows<F> out(View{a.out, a.o_se, 0, a.o_sh, 0}, e, h, 0, 1, 1);  // one row
   if (slot < 0 || slot >= a.S) {  // no state: the whole block leaves with a zero output
     const float zero[4] = {0, 0, 0, 0};
-    if (rg == 0) store4<F>(out, v, a.V, 0, zero);
+    if (rg == 0) store4<F, false>(out, 0, v, a.V, zero);
     return;
   }
   float decay = 0.0f;
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(256) step_kernel(const StepArgs a, int64_t nvs
 #pragma unroll
     for (int n = 1; n < RG; ++n) o += part[n][cg];
     const float y[4] = {o[0], o[1], o[2], o[3]};
-    store4<F>(out, v, a.V, 0, y);
+    store4<F, false>(out, 0, v, a.V, y);
   }
 }
 

@@ -124,10 +124,11 @@ struct HeadsCheck {
     }
     v.p = x->data;
     v.se = E > 1 ? s[0] : 0;
-    v.st = T > 1 ? s[1] : 0;
+    v.st = T > 1 ? s[1] : D;  // D: one step's end is the next one's start
     v.sh = heads > 1 ? s[2] : 0;
     const int64_t unit = 16 / es;
-    v.vec = D % 8 == 0 && aligned(x->data, 16) && v.se % unit == 0 && v.st % unit == 0 && v.sh % unit == 0;
+    v.vec = D % 8 == 0 && aligned(x->data, 16) && v.se % unit == 0 && v.st % unit == 0 && v.sh % unit == 0 &&
+            v.st >= D && v.st * es <= ((int64_t)1 << 25);
     Span sp = plain(x->data, extent * es);
     sp.row = (D + (heads - 1) * s[2]) * es;
     const int64_t period = T > 1 ? s[1] : (E > 1 ? s[0] : 0);  // 0: one step, a plain range
@@ -150,15 +151,17 @@ rlscan_status check_sizes(rlscan_format f, int64_t E, int64_t T, int64_t H, int6
   return RLSCAN_OK;
 }
 
-// Blocks of the largest launch.
-bool grid_ok(const Plan& p, int64_t E, int64_t H, bool backward) {
+// Whether every launch stays below the block limit.
+bool grid_ok(const Plan& p, int64_t E, int64_t T, int64_t H, int64_t Hkv, int64_t K, int64_t V, bool backward) {
   const int64_t most = rlscan::la::kMaxBlocks;
   const int64_t heads = E * H;
   if (heads > most / 64) return false;  // combine: up to 64 blocks a head
-  const int64_t per = (p.VP / 64) * p.nseg;
-  const int64_t chunks = backward ? p.chunks : 0;
-  const int64_t each = per > chunks ? per : chunks;
-  return each == 0 || heads <= most / each;
+  const int64_t per = (p.VP / 64 > 3 || !backward ? p.VP / 64 : 3) * p.nseg;
+  if (heads > (most - 24) / per) return false;
+  if (backward && p.nmarks > 0 && heads > most / p.nmarks) return false;
+  // group sums: one block for 256 elements
+  if (backward && Hkv != H && E * T * Hkv > (most - 1) * 256 / (K > V ? K : V)) return false;
+  return true;
 }
 
 rlscan_status fill_common(Args& a, rlscan_layout l, const float* log_decay, int per_step, const uint8_t* done,
@@ -194,11 +197,11 @@ void fill_plan(Args& a, const Plan& p) {
 extern "C" {
 
 int64_t rlscan_linear_attention_workspace(rlscan_format fmt, int64_t E, int64_t T, int64_t H, int64_t Hkv, int64_t K,
-                                          int64_t V, int backward, int per_step) {
+                                          int64_t V, int backward) {
   if (check_sizes(fmt, E, T, H, Hkv, K, V) != RLSCAN_OK) return -1;
   if (E * H == 0) return 0;
-  const Plan p = rlscan::la::make_plan(fmt, E, T, H, K, V, backward != 0, per_step == 0);
-  if (!grid_ok(p, E, H, backward != 0)) return -1;
+  const Plan p = rlscan::la::make_plan(fmt, E, T, H, H / Hkv, K, V, backward != 0);
+  if (!grid_ok(p, E, T, H, Hkv, K, V, backward != 0)) return -1;
   return p.floats * (int64_t)sizeof(float);
 }
 
@@ -212,8 +215,8 @@ rlscan_status rlscan_linear_attention(rlscan_format fmt, rlscan_layout layout, c
   if (st != RLSCAN_OK) return st;
   if (!layout_ok(layout) || !std::isfinite(scale)) return RLSCAN_ERR_PARAM;
   if (E * H == 0 || (T == 0 && !final_state)) return RLSCAN_OK;
-  const Plan p = rlscan::la::make_plan(fmt, E, T, H, K, V, false, false);
-  if (!grid_ok(p, E, H, false)) return RLSCAN_ERR_SHAPE;
+  const Plan p = rlscan::la::make_plan(fmt, E, T, H, H / Hkv, K, V, false);
+  if (!grid_ok(p, E, T, H, Hkv, K, V, false)) return RLSCAN_ERR_SHAPE;
   const int64_t need = p.floats * (int64_t)sizeof(float);
   Args a{};
   fill_common(a, layout, log_decay, per_step, done, E, T, H, Hkv, K, V, scale);
@@ -258,8 +261,8 @@ rlscan_status rlscan_linear_attention_backward(
   if (!layout_ok(layout) || !std::isfinite(scale)) return RLSCAN_ERR_PARAM;
   if (H == 0 || (E == 0 && per_step)) return RLSCAN_OK;
   if (!d_log_decay && (!per_step || T > 0)) return RLSCAN_ERR_NULL;
-  const Plan p = rlscan::la::make_plan(fmt, E, T, H, K, V, true, per_step == 0);
-  if (!grid_ok(p, E, H, true)) return RLSCAN_ERR_SHAPE;
+  const Plan p = rlscan::la::make_plan(fmt, E, T, H, H / Hkv, K, V, true);
+  if (!grid_ok(p, E, T, H, Hkv, K, V, true)) return RLSCAN_ERR_SHAPE;
   const int64_t need = p.floats * (int64_t)sizeof(float);
   Args a{};
   fill_common(a, layout, log_decay, per_step, done, E, T, H, Hkv, K, V, scale);
@@ -291,29 +294,46 @@ rlscan_status rlscan_linear_attention_backward(
   io.add_out(plain(workspace, need));
   if (io.clash()) return RLSCAN_ERR_ALIAS;
   a.init = init_state;
-  a.d_final = d_final_state;
-  a.d_init = d_init_state;
   fill_plan(a, p);
-  float* ws = static_cast<float*>(workspace);
-  a.seg_state = ws;
-  a.seg_decay = (ws += p.seg_state);
-  a.seg_grad = (ws += p.seg_decay);
-  a.seg_gdecay = (ws += p.seg_state);
-  a.states = (ws += p.seg_decay);
-  a.grads = (ws += p.states);
-  ws += p.states;
   if (per_step) {
     a.dg = d_log_decay;
     a.dg_se = a.g_se;
     a.dg_st = a.g_st;
     a.dg_sh = 1;
-  } else {  // steps' gradients to the workspace, then their sum
-    a.dg = ws;
-    a.dg_se = T * H;
-    a.dg_st = H;
-    a.dg_sh = 1;
   }
-  return launched(rlscan::la::launch_backward(fmt, a, p, per_step ? nullptr : d_log_decay, stream));
+  rlscan::la::Backward b{};
+  b.d_final = d_final_state;
+  b.d_init = d_init_state;
+  b.dg_head = per_step ? nullptr : d_log_decay;
+  float* ws = static_cast<float*>(workspace);
+  auto take = [&](int64_t floats) {
+    float* at = ws;
+    ws += floats;
+    return at;
+  };
+  b.total = reinterpret_cast<double*>(take(2 * p.heads));
+  b.end = take(p.heads);
+  b.seg_state = take(p.seg_state);
+  b.seg_decay = take(p.seg_decay);
+  b.seg_grad = take(p.seg_state);
+  b.seg_gdecay = take(p.seg_decay);
+  b.u = reinterpret_cast<double*>(take(p.dots));
+  b.w = reinterpret_cast<double*>(take(p.dots));
+  b.marks = take(p.marks);
+  b.mark_grads = take(p.marks);
+  b.mark_dots = reinterpret_cast<double*>(take((2 * E * H * p.nmarks + 3) / 4 * 4));
+  b.nmarks = p.nmarks;
+  a.mark_chunks = p.mark_chunks;
+  b.dk = a.dk;
+  b.dv = a.dv;
+  if (a.G > 1) {
+    auto scratch = [&](float* at, int64_t D) {
+      return View{at, T * H * D, H * D, D, D % 8 == 0 && H * D <= ((int64_t)1 << 23)};
+    };
+    b.dk = scratch(take(p.dk), K);
+    b.dv = scratch(take(p.dv), V);
+  }
+  return launched(rlscan::la::launch_backward(fmt, a, b, p, stream));
 }
 
 rlscan_status rlscan_linear_attention_step(rlscan_format fmt, const rlscan_heads* q, const rlscan_heads* k,

@@ -153,7 +153,7 @@ def linear_attention(q, k, v, log_decay, done=None, init_state=None, *, scale=No
             _plain(final_state, "final_state", (E, H, K, V), torch.float32, dev)
         elif with_state:
             final_state = torch.empty((E, H, K, V), dtype=torch.float32, device=dev)
-        need = _rl.lib().rlscan_linear_attention_workspace(fmt, E, T, H, Hkv, K, V, 0, per_step)
+        need = _rl.lib().rlscan_linear_attention_workspace(fmt, E, T, H, Hkv, K, V, 0)
         ws = _workspace(need, "rlscan_linear_attention", dev)
         _rl._call("rlscan_linear_attention", fmt, 1 if time_major else 0, _heads4(q, time_major),
                   _heads4(k, time_major), _heads4(v, time_major), log_decay.data_ptr(), per_step, _ptr(done),
@@ -189,7 +189,7 @@ def linear_attention_backward(d_out, q, k, v, log_decay, done=None, init_state=N
             _plain(d_init_state, "d_init_state", (E, H, K, V), torch.float32, dev)
         elif init_state is not None:
             d_init_state = torch.empty_like(init_state)
-        need = _rl.lib().rlscan_linear_attention_workspace(fmt, E, T, H, Hkv, K, V, 1, per_step)
+        need = _rl.lib().rlscan_linear_attention_workspace(fmt, E, T, H, Hkv, K, V, 1)
         ws = _workspace(need, "rlscan_linear_attention_backward", dev)
         h = [_heads4(x, time_major) for x in (d_out, q, k, v, dq, dk, dv)]
         _rl._call("rlscan_linear_attention_backward", fmt, 1 if time_major else 0, *h[:4], log_decay.data_ptr(),

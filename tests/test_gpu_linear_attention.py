@@ -191,7 +191,7 @@ def test_long_rows_are_cut_into_segments(dtype, T):
     """One row, one head: segments joined through the workspace, cuts anywhere."""
     H, G = (2, 2) if T == 1000 else (1, 1)
     fmt = {"f32": 0, "bf16": 1, "f16": 2}[dtype]
-    assert rl.lib().rlscan_linear_attention_workspace(fmt, 1, T, H, H // G, 32, 40, 0, 1) > 0
+    assert rl.lib().rlscan_linear_attention_workspace(fmt, 1, T, H, H // G, 32, 40, 0) > 0
     d = make(T, 1, T, H, G, 32, 40, dtype, p_done=0.002, decay=0.01)
     check_forward(d)
     if T < 3000:

@@ -42,7 +42,7 @@ def heads(i, E, T, H, D, offset=0, env=None, step=None, head=None):
 def forward(lib, E=2, T=100, H=4, Hkv=2, K=64, V=32, fmt=BF16, layout=0, per_step=1, scale=0.125, **kw):
     a = {"q": heads(0, E, T, H, K), "k": heads(1, E, T, Hkv, K), "v": heads(2, E, T, Hkv, V), "g": addr(3),
          "done": addr(4), "init": addr(5), "out": heads(6, E, T, H, V), "final": addr(7), "ws": addr(8)}
-    a["bytes"] = max(0, lib.rlscan_linear_attention_workspace(fmt, E, T, H, Hkv, K, V, 0, per_step))
+    a["bytes"] = max(0, lib.rlscan_linear_attention_workspace(fmt, E, T, H, Hkv, K, V, 0))
     a.update(kw)
     p = lambda x: ctypes.byref(x) if isinstance(x, _Heads) else x
     return lib.rlscan_linear_attention(fmt, layout, p(a["q"]), p(a["k"]), p(a["v"]), a["g"], per_step, a["done"],
@@ -55,7 +55,7 @@ def backward(lib, E=2, T=100, H=4, Hkv=2, K=64, V=32, fmt=BF16, layout=0, per_st
          "v": heads(2, E, T, Hkv, V), "g": addr(3), "done": addr(4), "init": addr(5), "d_final": addr(6),
          "dq": heads(10, E, T, H, K), "dk": heads(11, E, T, Hkv, K), "dv": heads(12, E, T, Hkv, V), "dg": addr(13),
          "d_init": addr(14), "ws": addr(15)}
-    a["bytes"] = max(0, lib.rlscan_linear_attention_workspace(fmt, E, T, H, Hkv, K, V, 1, per_step))
+    a["bytes"] = max(0, lib.rlscan_linear_attention_workspace(fmt, E, T, H, Hkv, K, V, 1))
     a.update(kw)
     p = lambda x: ctypes.byref(x) if isinstance(x, _Heads) else x
     return lib.rlscan_linear_attention_backward(
@@ -141,13 +141,13 @@ def test_attention_strides_and_overlap(lib):
 
 def test_workspace_sizes(lib):
     ws = lib.rlscan_linear_attention_workspace
-    assert ws(BF16, 64, 128, 16, 16, 64, 64, 0, 1) == 0  # enough heads: no segments
-    assert ws(BF16, 1, 32768, 1, 1, 64, 64, 0, 1) > 0
-    assert ws(BF16, 0, 128, 4, 4, 64, 64, 1, 1) == 0
-    assert ws(BF16, 2, 128, 4, 4, 64, 64, 1, 0) > ws(BF16, 2, 128, 4, 4, 64, 64, 1, 1) > 0
-    assert ws(BF16, 2, 128, 4, 4, 129, 64, 1, 1) == -1
-    assert ws(BF16, 2, 128, 4, 3, 64, 64, 1, 1) == -1
-    assert ws(7, 2, 128, 4, 4, 64, 64, 1, 1) == -1
+    assert ws(BF16, 64, 128, 16, 16, 64, 64, 0) == 0  # enough heads: no segments
+    assert ws(BF16, 1, 32768, 1, 1, 64, 64, 0) > 0
+    assert ws(BF16, 0, 128, 4, 4, 64, 64, 1) == 0
+    assert ws(BF16, 2, 128, 4, 2, 64, 64, 1) > ws(BF16, 2, 128, 4, 4, 64, 64, 1) > 0
+    assert ws(BF16, 2, 128, 4, 4, 129, 64, 1) == -1
+    assert ws(BF16, 2, 128, 4, 3, 64, 64, 1) == -1
+    assert ws(7, 2, 128, 4, 4, 64, 64, 1) == -1
     lp = lib.rlscan_action_log_probs_workspace
     assert lp(16384, 18) == 0 and lp(1, 131072) > 0
     assert lp(-1, 4) == -1 and lp(4, 0) == -1 and lp(2 ** 25, 4) == -1
