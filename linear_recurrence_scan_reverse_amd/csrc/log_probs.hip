@@ -63,18 +63,15 @@ __device__ __forceinline__ Sums join(Sums a, Sums b, float c) {
 // Adds logits; -inf stands for one that is not legal.  A NaN makes r and t NaN.
 template <int N>
 __device__ __forceinline__ void add(Sums& a, const float (&x)[N], float c) {
-  float top = a.m;
-  bool nan = false;
+  float top = a.m;  // fmaxf passes a NaN over; as a difference below it reaches r and t
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    top = fmaxf(top, x[i]);
-    nan |= x[i] != x[i];
-  }
-  if (nan) {
-    a = Sums{0.0f, 1.0f, __builtin_nanf(""), __builtin_nanf("")};
+  for (int i = 0; i < N; ++i) top = fmaxf(top, x[i]);
+  if (top == kNegInf) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (x[i] != x[i]) a = Sums{0.0f, 1.0f, x[i], x[i]};
     return;
   }
-  if (top == kNegInf) return;
   if (top > a.m) {
     if (a.n != 0.0f) raise(a, top, c);
     a.m = top;
@@ -113,7 +110,7 @@ __device__ __forceinline__ void finish(const LogProbArgs& p, int64_t r, const Su
   p.lse[r] = any ? minus(scaled(a.m, p.inv_t), -log_s) : (double)kNegInf;
 }
 
-// NTHR threads take one row (NTHR = 64: four rows a block), or with SPLIT a share of one.
+// NTHR threads take one row (below 256: several rows a block), or with SPLIT a share of one.
 template <class F, int NTHR, bool SPLIT>
 __global__ void __launch_bounds__(NTHR < 256 ? 256 : NTHR) log_probs_kernel(const LogProbArgs p) {
   constexpr int W = F::W, kRows = NTHR < 256 ? 256 / NTHR : 1;
@@ -122,7 +119,7 @@ __global__ void __launch_bounds__(NTHR < 256 ? 256 : NTHR) log_probs_kernel(cons
   const int64_t split = SPLIT ? p.split : 1;
   const int64_t r = SPLIT ? blockIdx.x / split : (int64_t)blockIdx.x * kRows + threadIdx.x / NTHR;
   const int64_t piece = SPLIT ? blockIdx.x % split : 0;
-  if (kRows > 1 && r >= p.R) return;  // a whole wave: rows below 256 threads meet no barrier
+  if (kRows > 1 && r >= p.R) return;  // whole groups of lanes: such rows meet no barrier
   const auto* row = static_cast<const typename F::E*>(p.x) + r * p.stride;
   const uint8_t* mask = p.mask ? p.mask + r * p.N : nullptr;
   int64_t lo = 0, hi = p.N;
@@ -142,9 +139,7 @@ __global__ void __launch_bounds__(NTHR < 256 ? 256 : NTHR) log_probs_kernel(cons
     add<1>(a, x, c);
   };
   for (int64_t i = lo + tid; i < i0; i += NTHR) one(i);
-  for (int64_t i = i0 + (int64_t)tid * W; i < i1; i += (int64_t)NTHR * W) {
-    Vec<F> x;
-    x.w = *reinterpret_cast<const u32x4*>(row + i);
+  auto group = [&](const Vec<F>& x, int64_t i) __attribute__((always_inline)) {
     float y[W];
 #pragma unroll
     for (int k = 0; k < W; ++k) y[k] = F::get(x.e[k]);
@@ -154,10 +149,24 @@ __global__ void __launch_bounds__(NTHR < 256 ? 256 : NTHR) log_probs_kernel(cons
         if (mask[i + k] == 0) y[k] = kNegInf;
     }
     add<W>(a, y, c);
-  }
-  for (int64_t i = i1 + tid; i < hi; i += NTHR) one(i);
+  };
+  constexpr int64_t kStep = (int64_t)NTHR * W;
+  int64_t i = i0 + (int64_t)tid * W;
+  for (; i + 3 * kStep < i1; i += 4 * kStep) {  // four requests at a time
+    Vec<F> x[4];
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) a = join(a, shuffle(a, o), c);
+    for (int k = 0; k < 4; ++k) x[k].w = *reinterpret_cast<const u32x4*>(row + i + k * kStep);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) group(x[k], i + k * kStep);
+  }
+  for (; i < i1; i += kStep) {
+    Vec<F> x;
+    x.w = *reinterpret_cast<const u32x4*>(row + i);
+    group(x, i);
+  }
+  for (int64_t j = i1 + tid; j < hi; j += NTHR) one(j);
+#pragma unroll
+  for (int o = 1; o < (NTHR < 64 ? NTHR : 64); o <<= 1) a = join(a, shuffle(a, o), c);
   if constexpr (NTHR > 64) {
     if ((tid & 63) == 0) part[tid >> 6] = a;
     __syncthreads();
@@ -243,6 +252,8 @@ hipError_t forward_fmt(const LogProbArgs& a, hipStream_t st) {
   if (a.split > 1) {
     log_probs_kernel<F, 256, true><<<dim3((unsigned)(a.R * a.split)), 256, 0, st>>>(a);
     log_probs_join_kernel<F><<<dim3((unsigned)a.R), 64, 0, st>>>(a);
+  } else if (a.N <= 64) {  // 16384 rows of 18: 15.3 us with a wave for each, 5.5 with 8 lanes
+    log_probs_kernel<F, 8, false><<<dim3((unsigned)((a.R + 31) / 32)), 256, 0, st>>>(a);
   } else if (a.N <= 2048) {
     log_probs_kernel<F, 64, false><<<dim3((unsigned)((a.R + 3) / 4)), 256, 0, st>>>(a);
   } else {

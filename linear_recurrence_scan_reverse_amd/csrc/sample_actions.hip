@@ -15,18 +15,27 @@
 // a row is shared changes an action.
 //
 // A kept set is a prefix of the falling order: all logits above a threshold and
-// the first `quota` of those equal to it.  A block finds it for one row: a pass
-// for the maximum; for long rows a pass that sorts logits into coarse bins of
-// (max - x) with their counts and weights, which leaves one bin to look into; that
-// bin's logits, collected in LDS, are searched by 8-bit digits of their
-// order-preserving keys.  A last pass sums the kept weights of tiles of the row, and
-// one wave finds the tile and in it the action.
+// the first `quota` of those equal to it.  One block takes a row.  Long rows go by
+// bins of max - x, which spread the LDS atomics (bins of the keys' leading bits put
+// most logits into some fifty: twice the time).  A pass after the one for the
+// maximum counts each bin's logits, for top_k, which leaves a few hundred that it can
+// keep.  They are collected in LDS, ranked against each other, and the rest of the
+// work is on them alone.  Without top_k, or where it leaves more, the threshold is
+// searched instead: by the bins' weights, then in the one bin that it falls into by
+// 8-bit digits of the keys; a last pass sums the kept weights of tiles of the row,
+// and one wave finds the tile and in it the action.
+//
+// 256 rows of 64007 bfloat16 logits with top_k up to 100: 80 us, of which reading
+// them takes 6 and the few rows without a top_k, which compute the float64 exponential
+// of every logit, nearly all; one row of 131072 float32 logits with top_p alone: 134 us
+// on its one CU.
 #include "rlscan_logits.hpp"
 
 namespace rlscan {
 namespace logits {
 
-constexpr int kBins = 1024;     // coarse bins over 32 temperatures below the maximum
+constexpr int kBins = 4096;     // bins of long rows, over 32 temperatures below the maximum
+constexpr int kFew = 512;       // logits that are ranked against each other: work grows with the square
 constexpr int kSmall = 1024;    // rows up to here go to one wave
 constexpr int kMiddle = 4096;   // and up to here to four
 constexpr double kUnit = 8796093022208.0;  // 2^43
@@ -80,9 +89,17 @@ struct SampleLds {
   static constexpr int kTiles = (int)((kCoarse ? kMaxActions : kList) / 256) + 2;
   double table[64];
   uint64_t hist[256];
-  uint64_t coarse_w[kCoarse ? kBins : 1];
+  union {
+    uint64_t coarse_w[kCoarse ? kBins : 1];  // weight of each bin
+    float together[NTHR / 64][512];          // then, per wave, a tile's kept logits
+  };
   uint32_t coarse_n[kCoarse ? kBins : 1];
   uint32_t list[kList];
+  uint64_t few[kFew];    // key << 32 | ~index: falling order is that of these numbers
+  uint64_t sorted[kFew];
+  uint64_t kept[kFew];   // units, in falling order
+  uint32_t rank[kFew];
+  int last;              // how many are kept
   uint64_t tile_w[kTiles];
   uint32_t tile_n[kTiles];
   uint64_t red[NTHR / 64];
@@ -108,18 +125,85 @@ __device__ __forceinline__ uint64_t block_sum(uint64_t v, uint64_t* red) {
 }
 
 // The first of n bins whose running sum reaches `target` (at least one unit), by the
-// first wave; the last bin with anything in it if none does.  Results in s.bin,
-// s.before (sum before the bin, with `base`) and s.inside (its own).
-template <class S, class V>
-__device__ __forceinline__ void search_bins(S& s, const V* bins, int n, uint64_t base, double target, bool falling) {
+// whole block, n / PER threads with PER bins each; the last bin with anything in it if none
+// does.  Results in s.bin, s.before (sum before the bin, with `base`) and s.inside (its own).
+template <int NTHR, int PER, class V>
+__device__ __forceinline__ void search_bins(SampleLds<NTHR>& s, const V* bins, int n, uint64_t base, double target,
+                                            bool falling) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const bool has = tid * PER < n;
+  __syncthreads();  // the bins are filled
+  V v[PER];
+  uint64_t own = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int b = tid * PER + i;
+    v[i] = 0;
+    if (has) v[i] = bins[falling ? n - 1 - b : b];
+    own += v[i];
+  }
+  uint64_t upto = own;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint64_t up = __shfl_up(upto, o);
+    if (lane >= o) upto += up;
+  }
+  if (lane == 63) s.red[wave] = upto;
+  if (tid == 0) s.bin = -1;
   __syncthreads();
-  if (threadIdx.x < 64) {
-    const int lane = threadIdx.x;
-    const int per = n / 64;
+  uint64_t before = base, total = base;
+  int last_wave = 0;  // with anything in it
+#pragma unroll
+  for (int i = 0; i < NTHR / 64; ++i) {
+    if (i < wave) before += s.red[i];
+    total += s.red[i];
+    if (s.red[i] > 0) last_wave = i;
+  }
+  before += upto - own;
+  const uint64_t filled = __ballot(own > 0);
+  const bool reaches = (double)total >= target;
+  const bool here = reaches ? (double)before < target && (double)(before + own) >= target
+                            : wave == last_wave && filled && lane == 63 - __clzll((long long)filled);
+  if (here) {
+    uint64_t sum = before;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (v[i] == 0 || (s.bin >= 0 && (double)sum >= target)) continue;
+      s.bin = falling ? n - 1 - (tid * PER + i) : tid * PER + i;
+      s.before = sum;
+      s.inside = v[i];
+      sum += v[i];
+    }
+  }
+  __syncthreads();
+}
+
+// The rest of a row's work on the n <= kFew logits in s.few, by the whole block.
+template <class F, int NTHR>
+__device__ __forceinline__ void take_few(SampleLds<NTHR>& s, const SampleArgs& a, int64_t r, const Weigh& weigh, int n,
+                                         int top_k, float top_p, float min_p) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  // each logit's place in falling order: how many come before it.  `share` threads compare one.
+  int share = 1;
+  while (share * 2 * n <= NTHR && share < 64) share *= 2;
+  for (int i = tid; i < n; i += NTHR) s.rank[i] = 0;
+  __syncthreads();
+  for (int i = tid / share; i < n; i += NTHR / share) {
+    const uint64_t mine = s.few[i];
+    uint32_t before = 0;
+    for (int j = tid % share; j < n; j += share) before += s.few[j] > mine;
+    if (before) atomicAdd(&s.rank[i], before);
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += NTHR) s.sorted[s.rank[i]] = s.few[i];
+  __syncthreads();
+  if (tid < 64) {  // one wave: consecutive places per lane
+    const int per = (n + 63) / 64, i0 = lane * per < n ? lane * per : n, i1 = i0 + per < n ? i0 + per : n;
     uint64_t own = 0;
-    for (int i = 0; i < per; ++i) {
-      const int b = lane * per + i;
-      own += bins[falling ? n - 1 - b : b];
+    for (int i = i0; i < i1; ++i) {
+      const double w = i < top_k ? weigh.weight(value_of((uint32_t)(s.sorted[i] >> 32))) : 0.0;
+      s.kept[i] = Weigh::units(w);
+      own += s.kept[i];
     }
     uint64_t upto = own;
 #pragma unroll
@@ -127,30 +211,50 @@ __device__ __forceinline__ void search_bins(S& s, const V* bins, int n, uint64_t
       const uint64_t up = __shfl_up(upto, o);
       if (lane >= o) upto += up;
     }
-    const uint64_t reached = __ballot((double)(base + upto) >= target && own > 0);
-    const uint64_t filled = __ballot(own > 0);
-    // running sums grow, so the first lane that reaches the target holds the bin
-    const int who = reached ? __ffsll((unsigned long long)reached) - 1 : (filled ? 63 - __clzll((long long)filled) : 0);
-    if (lane == who) {
-      uint64_t sum = base + upto - own;
-      int found = 0;
-      uint64_t before = sum, inside = 0;
-      for (int i = 0; i < per; ++i) {
-        const int b = falling ? n - 1 - (lane * per + i) : lane * per + i;
-        const uint64_t v = bins[b];
-        if (v == 0) continue;
-        found = b;
-        before = sum;
-        inside = v;
-        sum += v;
-        if ((double)sum >= target) break;
-      }
-      s.bin = found;
-      s.before = before;
-      s.inside = inside;
+    const uint64_t total = __shfl(upto, 63);
+    double target = top_p < 1.0f ? (double)top_p * (double)total : (double)total;
+    if (!(target >= 1.0)) target = 1.0;  // the largest is always kept
+    uint64_t before = upto - own;
+    int last = 0;
+    for (int i = i0; i < i1; ++i) {
+      const uint64_t u = s.kept[i];
+      const bool keep = i < top_k && (double)before < target &&
+                        weigh.weight(value_of((uint32_t)(s.sorted[i] >> 32))) >= (double)min_p;
+      before += u;
+      if (keep) last = i + 1;  // what is kept is a prefix
     }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int other = __shfl_xor(last, o);
+      last = other > last ? other : last;
+    }
+    if (lane == 0) s.last = last;
   }
   __syncthreads();
+  // the running weight in the order of the indices, of each that is kept
+  const int m = s.last;
+  uint64_t total = 0;
+  for (int j = 0; j < m; ++j) total += s.kept[j];
+  const double goal = (double)a.u[r] * (double)total;
+  for (int i = tid; i < m; i += NTHR) {
+    const uint32_t mine = ~(uint32_t)s.sorted[i];
+    uint64_t before = 0;
+    bool none_after = true;
+    for (int j = 0; j < m; ++j) {
+      const uint32_t other = ~(uint32_t)s.sorted[j];
+      if (other < mine) before += s.kept[j];
+      none_after &= !(other > mine && s.kept[j] > 0);
+    }
+    const uint64_t own = s.kept[i];
+    // the first that passes the goal; the last with any weight if none does (u >= 1)
+    const bool reached = own > 0 && (double)(before + own) > goal;
+    const bool first = !((double)before > goal) || before == 0;
+    if ((reached && first) || (own > 0 && !reached && none_after)) {
+      a.action[r] = (int64_t)mine;
+      if (a.log_prob)
+        a.log_prob[r] = (float)(weigh.log_weight(value_of((uint32_t)(s.sorted[i] >> 32))) - log((double)total / kUnit));
+    }
+  }
 }
 
 template <class F, int NTHR>
@@ -196,6 +300,11 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
     }
   };
 
+  constexpr bool coarse = SampleLds<NTHR>::kCoarse;
+  constexpr int kList = SampleLds<NTHR>::kList;
+  bool need_k = top_k > 0 && top_k < N;
+  const bool need_p = top_p < 1.0f;
+
   // ---- maximum
   float top = kNegInf;
   for (int g = tid; g < groups; g += NTHR) {
@@ -221,20 +330,50 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
   const Weigh weigh{(double)top, 1.0 / (double)temperature, s.table};
 
   // ---- the threshold: keys above it, and `quota` of those equal to it, are kept
-  bool need_k = top_k > 0 && top_k < N;
-  const bool need_p = top_p < 1.0f;
   uint32_t thr = 0;
   uint64_t quota = ~0ull;
   if (need_k || need_p) {
-    constexpr bool coarse = SampleLds<NTHR>::kCoarse;
-    constexpr int kList = SampleLds<NTHR>::kList;
+    uint64_t before_k = 0;  // logits in the bins before the one that top_k cuts
+    int bin_k = kBins;
     const float per = fminf((float)kBins / (32.0f * temperature), 1e30f);
     auto bin_of = [&](float x) __attribute__((always_inline)) { return (int)fminf((top - x) * per, (float)(kBins - 1)); };
-    if (coarse) {
-      for (int i = tid; i < kBins; i += NTHR) {
-        s.coarse_n[i] = 0;
-        s.coarse_w[i] = 0;
+    if (coarse && need_k) {
+      for (int i = tid; i < kBins; i += NTHR) s.coarse_n[i] = 0;
+      __syncthreads();
+      for (int g = tid; g < groups; g += NTHR) {
+        float x[W];
+        group(g, x);
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+          if (x[k] != kNegInf) atomicAdd(&s.coarse_n[bin_of(x[k])], 1u);
       }
+      search_bins<NTHR, 4>(s, s.coarse_n, kBins, 0, (double)top_k, false);
+      before_k = s.before;
+      bin_k = s.bin;
+      need_k = s.before + s.inside >= (uint64_t)top_k;
+    }
+    const uint64_t candidates = coarse ? (need_k ? before_k + s.inside : (uint64_t)N) : (uint64_t)N;
+    if (candidates <= (uint64_t)kFew) {
+      __syncthreads();
+      if (tid == 0) s.count = 0;
+      __syncthreads();
+      for (int g = tid; g < groups; g += NTHR) {
+        float x[W];
+        group(g, x);
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+          if (x[k] == kNegInf || (coarse && need_k && bin_of(x[k]) > bin_k)) continue;
+          const uint32_t at = atomicAdd(&s.count, 1u);  // at most kFew: the bins were counted
+          if (at < (uint32_t)kFew) s.few[at] = (uint64_t)key_of(x[k]) << 32 | (uint32_t)~(g * W - shift + k);
+        }
+      }
+      __syncthreads();
+      const int n = (int)s.count < kFew ? (int)s.count : kFew;
+      take_few<F, NTHR>(s, a, r, weigh, n, need_k ? top_k : n, top_p, min_p);
+      return;
+    }
+    if (coarse && need_p) {
+      for (int i = tid; i < kBins; i += NTHR) s.coarse_w[i] = 0;
       __syncthreads();
       for (int g = tid; g < groups; g += NTHR) {
         float x[W];
@@ -242,12 +381,8 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
 #pragma unroll
         for (int k = 0; k < W; ++k) {
           if (x[k] == kNegInf) continue;
-          const int b = bin_of(x[k]);
-          if (need_k) atomicAdd(&s.coarse_n[b], 1u);
-          if (need_p) {
-            const uint64_t u = Weigh::units(weigh.weight(x[k]));
-            if (u) atomicAdd((unsigned long long*)&s.coarse_w[b], (unsigned long long)u);
-          }
+          const uint64_t u = Weigh::units(weigh.weight(x[k]));
+          if (u) atomicAdd((unsigned long long*)&s.coarse_w[bin_of(x[k])], (unsigned long long)u);
         }
       }
       __syncthreads();
@@ -303,7 +438,7 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
           const uint64_t v = weights ? Weigh::units(weigh.weight(value_of(key))) : 1;
           if (v) atomicAdd((unsigned long long*)&s.hist[key >> d & 255], (unsigned long long)v);
         });
-        search_bins(s, s.hist, 256, base, target, true);
+        search_bins<NTHR, NTHR < 256 ? 256 / NTHR : 1>(s, s.hist, 256, base, target, true);
         prefix |= (uint32_t)s.bin << d;
         known |= 255u << d;
         base = s.before;
@@ -315,22 +450,11 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
 
     uint64_t kept_before = 0;  // weight of whole bins before the one that top_k cuts
     uint64_t kept = 0;         // weight that top_k keeps
-    int bin_k = kBins;         // the bin that top_k cuts
     if (need_k) {
-      uint64_t before = 0;
-      int bin = -1;
-      if (coarse) {
-        search_bins(s, s.coarse_n, kBins, 0, (double)top_k, false);
-        before = s.before;
-        bin = bin_k = s.bin;
-        need_k = s.before + s.inside >= (uint64_t)top_k;
-      }
+      collect(coarse ? bin_k : -1);
+      if (!coarse) need_k = s.count > (uint32_t)top_k;
       if (need_k) {
-        collect(bin);
-        if (!coarse) need_k = s.count > (uint32_t)top_k;
-      }
-      if (need_k) {
-        thr = descend(false, before, (double)top_k);
+        thr = descend(false, before_k, (double)top_k);
         quota = (uint64_t)top_k - s.before;
         if (need_p) {
           uint64_t mine = 0;
@@ -367,7 +491,7 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
           bin = bin_k;
           base = kept_before;
         } else {
-          search_bins(s, s.coarse_w, kBins, 0, target, false);
+          search_bins<NTHR, 4>(s, s.coarse_w, kBins, 0, target, false);
           bin = s.bin;
           base = s.before;
         }
@@ -415,27 +539,46 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
       }
     }
   };
+  // A tile's kept logits are first moved together, so that weights are computed for
+  // them alone: where top_p keeps a sixth of a row, a sixth of the exponentials.
+  float* together = s.together[wave];
   for (int t = wave; t < tiles; t += NTHR / 64) {
-    uint64_t u[W], sum = 0;
-    bool tie[W];
-    uint32_t n = 0;
-    lane_part(t, u, tie);
+    const int g = t * 64 + lane;
+    float x[W];
+    if (g < groups) {
+      group(g, x);
+    } else {
+#pragma unroll
+      for (int k = 0; k < W; ++k) x[k] = kNegInf;
+    }
+    int many = 0;
+    uint32_t ties = 0;
 #pragma unroll
     for (int k = 0; k < W; ++k) {
-      sum += u[k];
-      n += tie[k];
+      const uint32_t key = key_of(x[k]);
+      const bool legal = x[k] != kNegInf, above = legal && key > thr;
+      const uint64_t who = __ballot(above);
+      if (above) together[many + __popcll(who & ~(~0ull << lane))] = x[k];
+      many += __popcll(who);
+      ties += __popcll(__ballot(legal && key == thr));
     }
-    if (__ballot(sum != 0 || n != 0)) {
+    uint64_t sum = 0;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // written and read by this wave alone
+    __builtin_amdgcn_wave_barrier();
+    for (int i = lane; i < many; i += 64) {
+      const double w = weigh.weight(together[i]);
+      if (w >= (double)min_p) sum += Weigh::units(w);
+    }
+    if (many) {
 #pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        sum += __shfl_xor(sum, o);
-        n += __shfl_xor(n, o);
-      }
+      for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o);
     }
     if (lane == 0) {
       s.tile_w[t] = sum;
-      s.tile_n[t] = n;
+      s.tile_n[t] = ties;
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
   }
   __syncthreads();
   if (wave != 0) return;

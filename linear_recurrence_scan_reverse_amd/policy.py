@@ -26,6 +26,49 @@ class _Heads(ctypes.Structure):
                 ("head", ctypes.c_int64)]
 
 
+_HEADS_BYTES = ctypes.sizeof(_Heads)
+_ARRAYS = {n: ctypes.c_int64 * (4 * n) for n in (4, 7)}  # n rlscan_heads in a row
+_raw_stream_of = torch._C._cuda_getCurrentRawStream
+
+
+def _refuse(x, name, shape, dtype, device):
+    """Raises for a tensor that _strided does not take."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if x.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, str(dtype).replace("torch.", ""), x.dtype))
+    if x.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(x.shape)))
+    if x.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, x.device, device))
+    raise ValueError("%s must be contiguous in its last dimension" % name)
+
+
+def _strided(x, name, shape, dtype, device):
+    """A value tensor of any strides with a contiguous last dimension."""
+    if not (isinstance(x, torch.Tensor) and x.dtype is dtype and x.shape == shape and x.device == device
+            and (x.stride(-1) == 1 if shape else True) or _single(x, shape, dtype, device)):
+        _refuse(x, name, shape, dtype, device)
+    return x
+
+
+def _single(x, shape, dtype, device):
+    """Whether only the stride of a last dimension of one element was in the way."""
+    return (isinstance(x, torch.Tensor) and x.dtype is dtype and x.shape == shape and x.device == device
+            and shape[-1] <= 1)
+
+
+def _plain(x, name, shape, dtype, device):
+    """A contiguous tensor of the given dtype, or None."""
+    if x is None:
+        return None
+    if not (isinstance(x, torch.Tensor) and x.dtype is dtype and x.shape == shape and x.device == device
+            and x.is_contiguous()):
+        _strided(x, name, shape, dtype, device)
+        raise ValueError("%s must be contiguous" % name)
+    return x
+
+
 def _values(x, name, dims):
     if not isinstance(x, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
@@ -36,37 +79,12 @@ def _values(x, name, dims):
     return x
 
 
-def _strided(x, name, shape, dtype, device):
-    """A value tensor of any strides with a contiguous last dimension."""
-    if not isinstance(x, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if x.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, str(dtype).replace("torch.", ""), x.dtype))
-    if x.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(x.shape)))
-    if x.device != device:
-        raise ValueError("%s is on %s, expected %s" % (name, x.device, device))
-    if x.dim() and x.shape[-1] > 1 and x.stride(-1) != 1:
-        raise ValueError("%s must be contiguous in its last dimension" % name)
-    return x
-
-
-def _plain(x, name, shape, dtype, device):
-    """A contiguous tensor of the given dtype, or None."""
-    if x is None:
-        return None
-    _strided(x, name, shape, dtype, device)
-    if not x.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return x
-
-
 def _flags(x, name, shape, device):
     return None if x is None else _rl._check_flags(x, name, shape, device)
 
 
 def _on_gpu(x, name):
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError("%s must be on a GPU device, got %s" % (name, x.device))
     return x.device
 
@@ -78,34 +96,50 @@ def _on(stream, device):
     """Allocations and launches go to the caller's stream, on the tensors' device."""
     if stream is not None:
         return torch.cuda.stream(stream)
-    if device.index is not None and device.index != torch.cuda.current_device():
+    if device.index != torch._C._cuda_getDevice():
         return torch.cuda.device(device)
     return _HERE
 
 
 def _raw_stream(stream, device):
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+    return _raw_stream_of(device.index) if stream is None else stream.cuda_stream
 
 
-def _heads4(x, time_major):
-    s = x.stride()
-    return ctypes.byref(_Heads(x.data_ptr(), s[1], s[0], s[2]) if time_major
-                        else _Heads(x.data_ptr(), s[0], s[1], s[2]))
-
-
-def _heads3(x):
-    s = x.stride()
-    return ctypes.byref(_Heads(x.data_ptr(), s[0], 0, s[1]))
+def _heads(tensors, time_major):
+    """(array to keep alive, address) of the [E, T, heads, D] views of the tensors, one after the other."""
+    v = []
+    for x in tensors:
+        s0, s1, s2, _ = x.stride()
+        v += (x.data_ptr(), s1, s0, s2) if time_major else (x.data_ptr(), s0, s1, s2)
+    a = _ARRAYS[len(tensors)](*v)
+    return a, ctypes.addressof(a)
 
 
 def _ptr(x):
     return None if x is None else x.data_ptr()
 
 
-def _workspace(bytes_, fname, device):
-    if bytes_ < 0:
+_functions = {}
+
+
+def _call(fname, *args):
+    fn = _functions.get(fname)
+    if fn is None:
+        fn = _functions[fname] = getattr(_rl.lib(), fname)
+    st = fn(*args)
+    if st != 0:
+        raise _rl.RlscanError(st, fname)
+
+
+def _workspace(fname, device, *sizes):
+    """(tensor or None, bytes) of scratch memory that an entry asks for."""
+    fn = _functions.get(fname)
+    if fn is None:
+        fn = _functions[fname] = getattr(_rl.lib(), fname)
+    need = fn(*sizes)
+    if need < 0:
         raise _rl.RlscanError(2, fname)
-    return torch.empty(bytes_, dtype=torch.uint8, device=device) if bytes_ else None
+    return (torch.empty(need, dtype=torch.uint8, device=device) if need else None), need
 
 
 def _attention_inputs(q, k, v, log_decay, done, init_state, time_major):
@@ -153,12 +187,12 @@ def linear_attention(q, k, v, log_decay, done=None, init_state=None, *, scale=No
             _plain(final_state, "final_state", (E, H, K, V), torch.float32, dev)
         elif with_state:
             final_state = torch.empty((E, H, K, V), dtype=torch.float32, device=dev)
-        need = _rl.lib().rlscan_linear_attention_workspace(fmt, E, T, H, Hkv, K, V, 0)
-        ws = _workspace(need, "rlscan_linear_attention", dev)
-        _rl._call("rlscan_linear_attention", fmt, 1 if time_major else 0, _heads4(q, time_major),
-                  _heads4(k, time_major), _heads4(v, time_major), log_decay.data_ptr(), per_step, _ptr(done),
-                  _ptr(init_state), _heads4(out, time_major), _ptr(final_state), _ptr(ws), need, E, T, H, Hkv, K, V,
-                  scale, _raw_stream(stream, dev))
+        ws, need = _workspace("rlscan_linear_attention_workspace", dev, fmt, E, T, H, Hkv, K, V, 0)
+        keep, h = _heads((q, k, v, out), time_major)
+        n = _HEADS_BYTES
+        _call("rlscan_linear_attention", fmt, 1 if time_major else 0, h, h + n, h + 2 * n, log_decay.data_ptr(),
+              per_step, _ptr(done), _ptr(init_state), h + 3 * n, _ptr(final_state), _ptr(ws), need, E, T, H, Hkv, K, V,
+              scale, _raw_stream(stream, dev))
     return out if final_state is None else (out, final_state)
 
 
@@ -189,12 +223,12 @@ def linear_attention_backward(d_out, q, k, v, log_decay, done=None, init_state=N
             _plain(d_init_state, "d_init_state", (E, H, K, V), torch.float32, dev)
         elif init_state is not None:
             d_init_state = torch.empty_like(init_state)
-        need = _rl.lib().rlscan_linear_attention_workspace(fmt, E, T, H, Hkv, K, V, 1)
-        ws = _workspace(need, "rlscan_linear_attention_backward", dev)
-        h = [_heads4(x, time_major) for x in (d_out, q, k, v, dq, dk, dv)]
-        _rl._call("rlscan_linear_attention_backward", fmt, 1 if time_major else 0, *h[:4], log_decay.data_ptr(),
-                  per_step, _ptr(done), _ptr(init_state), _ptr(d_final_state), *h[4:], d_log_decay.data_ptr(),
-                  _ptr(d_init_state), _ptr(ws), need, E, T, H, Hkv, K, V, scale, _raw_stream(stream, dev))
+        ws, need = _workspace("rlscan_linear_attention_workspace", dev, fmt, E, T, H, Hkv, K, V, 1)
+        keep, h = _heads((d_out, q, k, v, dq, dk, dv), time_major)
+        h = [h + i * _HEADS_BYTES for i in range(7)]
+        _call("rlscan_linear_attention_backward", fmt, 1 if time_major else 0, *h[:4], log_decay.data_ptr(), per_step,
+              _ptr(done), _ptr(init_state), _ptr(d_final_state), *h[4:], d_log_decay.data_ptr(), _ptr(d_init_state),
+              _ptr(ws), need, E, T, H, Hkv, K, V, scale, _raw_stream(stream, dev))
     return dq, dk, dv, d_log_decay, d_init_state
 
 
@@ -232,9 +266,15 @@ def linear_attention_step(q, k, v, log_decay, state, reset=None, slots=None, *, 
     scale = K ** -0.5 if scale is None else float(scale)
     with _on(stream, dev):
         out = torch.empty((E, H, V), dtype=dt, device=dev) if out is None else _strided(out, "out", (E, H, V), dt, dev)
-        _rl._call("rlscan_linear_attention_step", _DTYPES[dt], _heads3(q), _heads3(k), _heads3(v),
-                  log_decay.data_ptr(), per_row, _ptr(reset), _ptr(slots), state.data_ptr(), _heads3(out), E, S, H, Hkv,
-                  K, V, scale, _raw_stream(stream, dev))
+        v_ = []
+        for x in (q, k, v, out):
+            s0, s1, _ = x.stride()
+            v_ += (x.data_ptr(), s0, 0, s1)
+        keep = _ARRAYS[4](*v_)
+        h, n = ctypes.addressof(keep), _HEADS_BYTES
+        _call("rlscan_linear_attention_step", _DTYPES[dt], h, h + n, h + 2 * n, log_decay.data_ptr(), per_row,
+              _ptr(reset), _ptr(slots), state.data_ptr(), h + 3 * n, E, S, H, Hkv, K, V, scale,
+              _raw_stream(stream, dev))
     return out
 
 
@@ -304,10 +344,10 @@ def sample_actions(logits, uniforms, *, temperature=1.0, top_k=None, top_p=None,
         else:
             _plain(actions, "actions", lead, torch.int64, dev)
         if log_probs is None:
-            log_probs = torch.empty(lead, dtype=torch.float32, device=dev)
+            log_probs = torch.empty_like(uniforms)
         else:
             _plain(log_probs, "log_probs", lead, torch.float32, dev)
-        _rl._call("rlscan_sample_actions", _DTYPES[logits.dtype], logits.data_ptr(), stride, _ptr(mask),
+        _call("rlscan_sample_actions", _DTYPES[logits.dtype], logits.data_ptr(), stride, _ptr(mask),
                   uniforms.data_ptr(), _ptr(temps), _ptr(ks), _ptr(ps), _ptr(ms), float(t1), min(int(k1), 2 ** 31 - 1),
                   float(p1), float(m1), actions.data_ptr(), log_probs.data_ptr(), R, N, _raw_stream(stream, dev))
     return actions, log_probs
@@ -331,9 +371,8 @@ def action_log_probs(logits, actions, *, temperature=1.0, mask=None, log_probs=N
         outs = [torch.empty(lead, dtype=dt, device=dev) if x is None else _plain(x, name, lead, dt, dev)
                 for x, name, dt in ((log_probs, "log_probs", torch.float32), (entropies, "entropies", torch.float32),
                                     (lse, "lse", torch.float64))]
-        need = _rl.lib().rlscan_action_log_probs_workspace(R, N)
-        ws = _workspace(need, "rlscan_action_log_probs", dev)
-        _rl._call("rlscan_action_log_probs", _DTYPES[logits.dtype], logits.data_ptr(), stride, _ptr(mask),
+        ws, need = _workspace("rlscan_action_log_probs_workspace", dev, R, N)
+        _call("rlscan_action_log_probs", _DTYPES[logits.dtype], logits.data_ptr(), stride, _ptr(mask),
                   actions.data_ptr(), float(temperature), outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(),
                   _ptr(ws), need, R, N, _raw_stream(stream, dev))
     return tuple(outs)
@@ -361,7 +400,7 @@ def action_log_probs_backward(d_log_probs, d_entropies, logits, actions, lse, en
             d_logits = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
         else:
             _strided(d_logits, "d_logits", logits.shape, logits.dtype, dev)
-        _rl._call("rlscan_action_log_probs_backward", _DTYPES[logits.dtype], _ptr(d_log_probs), _ptr(d_entropies),
+        _call("rlscan_action_log_probs_backward", _DTYPES[logits.dtype], _ptr(d_log_probs), _ptr(d_entropies),
                   logits.data_ptr(), stride, _ptr(mask), actions.data_ptr(), float(temperature), lse.data_ptr(),
                   entropies.data_ptr(), d_logits.data_ptr(), _row_stride(d_logits, "d_logits"), R, N,
                   _raw_stream(stream, dev))
