@@ -25,10 +25,10 @@
 // 8-bit digits of the keys; a last pass sums the kept weights of tiles of the row,
 // and one wave finds the tile and in it the action.
 //
-// 256 rows of 64007 bfloat16 logits with top_k up to 100: 80 us, of which reading
-// them takes 6 and the few rows without a top_k, which compute the float64 exponential
-// of every logit, nearly all; one row of 131072 float32 logits with top_p alone: 134 us
-// on its one CU.
+// 256 rows of 64007 bfloat16 logits with top_k up to 100: 79 us, of which reading them
+// takes 6 and the few rows without a top_k nearly all; one row of 131072 float32 logits
+// with top_p alone: 122 us on its one CU.  Both are bound by the instructions of the
+// float64 exponentials, some 40 for each logit, in two passes.
 #include "rlscan_logits.hpp"
 
 namespace rlscan {
@@ -50,10 +50,13 @@ __device__ __forceinline__ float value_of(uint32_t k) {
   return __builtin_bit_cast(float, k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
-// e^y for y <= 0, to about 2e-16: 2^(n/64) from a table, and the Taylor series of
-// the rest, |r| <= ln 2 / 128, to the fifth power.
+// e^y for -31 <= y <= 0, to about 2e-16: 2^(n/64) from a table, and the Taylor series
+// of the rest, |r| <= ln 2 / 128, to the fifth power.  The whole number n is read from
+// a sum's low bits and 2^(n/64)'s exponent added to as an integer.
 __device__ __forceinline__ double exp_table(double y, const double* table) {
-  const double n = __builtin_rint(y * (64.0 / 0.693147180559945309417));
+  constexpr double kWhole = 6755399441055744.0;  // 1.5 * 2^52: sums with it are whole numbers
+  const double t = __builtin_fma(y, 64.0 / 0.693147180559945309417, kWhole);
+  const double n = t - kWhole;
   double r = __builtin_fma(n, -0x1.62e42fefap-7, y);  // the leading 37 bits of ln 2 / 64: n * it is exact
   r = __builtin_fma(n, -(0x1.62e42fefa39efp-7 - 0x1.62e42fefap-7) - 0x1.abc9e3b39803fp-62, r);
   double p = __builtin_fma(r, 1.0 / 120.0, 1.0 / 24.0);
@@ -61,18 +64,26 @@ __device__ __forceinline__ double exp_table(double y, const double* table) {
   p = __builtin_fma(p, r, 0.5);
   p = __builtin_fma(p, r, 1.0);
   p = __builtin_fma(p, r, 1.0);
-  const int i = (int)n;
-  return __builtin_ldexp(p * table[i & 63], i >> 6);
+  const int i = (int)(uint32_t)__builtin_bit_cast(uint64_t, t);
+  const uint64_t scale = __builtin_bit_cast(uint64_t, table[i & 63]) + ((uint64_t)(uint32_t)(i >> 6) << 52);
+  return p * __builtin_bit_cast(double, scale);
 }
 
 struct Weigh {
   double max, inv_t;
   const double* table;
   __device__ __forceinline__ double log_weight(float x) const { return ((double)x - max) * inv_t; }
-  // A weight as a float64, 0 where it rounds to no unit.
+  // A weight as a float64, 0 where it rounds to no unit.  No branch: the weights of a
+  // group are computed side by side (131072 of them by one CU with their sums by bins:
+  // 84 thousand clocks; 92 with a branch around each).
   __device__ __forceinline__ double weight(float x) const {
     const double y = log_weight(x);
-    return y < -31.0 ? 0.0 : exp_table(y, table);
+    const double w = exp_table(fmax(y, -31.0), table);
+    return y < -31.0 ? 0.0 : w;
+  }
+  // in units
+  static __device__ __forceinline__ double whole(double w) {
+    return __builtin_fma(w, kUnit, 4503599627370496.0) - 4503599627370496.0;
   }
   static __device__ __forceinline__ uint64_t units(double w) {
     const double m = __builtin_fma(w, kUnit, 4503599627370496.0);  // + 2^52: rounds to a whole number
@@ -89,10 +100,7 @@ struct SampleLds {
   static constexpr int kTiles = (int)((kCoarse ? kMaxActions : kList) / 256) + 2;
   double table[64];
   uint64_t hist[256];
-  union {
-    uint64_t coarse_w[kCoarse ? kBins : 1];  // weight of each bin
-    float together[NTHR / 64][512];          // then, per wave, a tile's kept logits
-  };
+  uint64_t coarse_w[kCoarse ? kBins : 1];
   uint32_t coarse_n[kCoarse ? kBins : 1];
   uint32_t list[kList];
   uint64_t few[kFew];    // key << 32 | ~index: falling order is that of these numbers
@@ -110,6 +118,23 @@ struct SampleLds {
   uint64_t before;
   uint64_t inside;
 };
+
+// The wave's sum, in lane 63.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double add_from(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xf, false);
+  return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_sum_last(double v) {
+  v = add_from<0x111, 0xf>(v);  // row_shr:1
+  v = add_from<0x112, 0xf>(v);
+  v = add_from<0x114, 0xf>(v);
+  v = add_from<0x118, 0xf>(v);
+  v = add_from<0x142, 0xa>(v);  // row_bcast:15
+  return add_from<0x143, 0xc>(v);  // row_bcast:31
+}
 
 template <int NTHR>
 __device__ __forceinline__ uint64_t block_sum(uint64_t v, uint64_t* red) {
@@ -280,7 +305,9 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
   }
   min_p = min_p > 0.0f ? fminf(min_p, 1.0f) : 0.0f;
 
-  // fn(x) for each legal logit of group g
+  // NaN is not legal; +inf counts as the largest float
+  auto legal = [](float x) __attribute__((always_inline)) { return x > kNegInf ? fminf(x, kMaxFloat) : kNegInf; };
+  // the logits of group g, -inf where not legal
   auto group = [&](int g, float (&x)[W]) __attribute__((always_inline)) {
     const int i = g * W - shift;
     if (i >= 0 && i + W <= N) {
@@ -294,9 +321,40 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
     }
 #pragma unroll
     for (int k = 0; k < W; ++k) {
-      // NaN is not legal; +inf counts as the largest float
       if (mask && i + k >= 0 && i + k < N && mask[i + k] == 0) x[k] = kNegInf;
-      x[k] = x[k] > kNegInf ? fminf(x[k], kMaxFloat) : kNegInf;
+      x[k] = legal(x[k]);
+    }
+  };
+  // Calls fn(g, x) for each of the thread's groups.  Unmasked long rows ask for 64 bytes
+  // at a time (one row of 131072 float32 logits: 121 us; 134 with 16 bytes).
+  auto each_group = [&](auto fn) __attribute__((always_inline)) {
+    constexpr int kAhead = 16 / W;
+    int g = tid;
+    if (NTHR == 1024 && !mask) {
+      if (g == 0) {  // it may begin before the row
+        float x[W];
+        group(g, x);
+        fn(g, x);
+        g += NTHR;
+      }
+      const int inside = (N + shift) / W;  // groups that end within the row
+      for (; g + (kAhead - 1) * NTHR < inside; g += kAhead * NTHR) {
+        Vec<F> v[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) v[j].w = *reinterpret_cast<const u32x4*>(row + ((g + j * NTHR) * W - shift));
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          float x[W];
+#pragma unroll
+          for (int k = 0; k < W; ++k) x[k] = legal(F::get(v[j].e[k]));
+          fn(g + j * NTHR, x);
+        }
+      }
+    }
+    for (; g < groups; g += NTHR) {
+      float x[W];
+      group(g, x);
+      fn(g, x);
     }
   };
 
@@ -307,12 +365,10 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
 
   // ---- maximum
   float top = kNegInf;
-  for (int g = tid; g < groups; g += NTHR) {
-    float x[W];
-    group(g, x);
+  each_group([&](int , float (&x)[W]) __attribute__((always_inline)) {
 #pragma unroll
     for (int k = 0; k < W; ++k) top = fmaxf(top, x[k]);
-  }
+  });
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
   if (lane == 0) s.redf[wave] = top;
@@ -340,13 +396,11 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
     if (coarse && need_k) {
       for (int i = tid; i < kBins; i += NTHR) s.coarse_n[i] = 0;
       __syncthreads();
-      for (int g = tid; g < groups; g += NTHR) {
-        float x[W];
-        group(g, x);
+      each_group([&](int , float (&x)[W]) __attribute__((always_inline)) {
 #pragma unroll
         for (int k = 0; k < W; ++k)
           if (x[k] != kNegInf) atomicAdd(&s.coarse_n[bin_of(x[k])], 1u);
-      }
+      });
       search_bins<NTHR, 4>(s, s.coarse_n, kBins, 0, (double)top_k, false);
       before_k = s.before;
       bin_k = s.bin;
@@ -357,16 +411,14 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
       __syncthreads();
       if (tid == 0) s.count = 0;
       __syncthreads();
-      for (int g = tid; g < groups; g += NTHR) {
-        float x[W];
-        group(g, x);
+      each_group([&](int g, float (&x)[W]) __attribute__((always_inline)) {
 #pragma unroll
         for (int k = 0; k < W; ++k) {
           if (x[k] == kNegInf || (coarse && need_k && bin_of(x[k]) > bin_k)) continue;
           const uint32_t at = atomicAdd(&s.count, 1u);  // at most kFew: the bins were counted
           if (at < (uint32_t)kFew) s.few[at] = (uint64_t)key_of(x[k]) << 32 | (uint32_t)~(g * W - shift + k);
         }
-      }
+      });
       __syncthreads();
       const int n = (int)s.count < kFew ? (int)s.count : kFew;
       take_few<F, NTHR>(s, a, r, weigh, n, need_k ? top_k : n, top_p, min_p);
@@ -375,16 +427,15 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
     if (coarse && need_p) {
       for (int i = tid; i < kBins; i += NTHR) s.coarse_w[i] = 0;
       __syncthreads();
-      for (int g = tid; g < groups; g += NTHR) {
-        float x[W];
-        group(g, x);
+      each_group([&](int , float (&x)[W]) __attribute__((always_inline)) {
+        uint64_t u[W];
+#pragma unroll
+        for (int k = 0; k < W; ++k) u[k] = Weigh::units(weigh.weight(x[k]));
 #pragma unroll
         for (int k = 0; k < W; ++k) {
-          if (x[k] == kNegInf) continue;
-          const uint64_t u = Weigh::units(weigh.weight(x[k]));
-          if (u) atomicAdd((unsigned long long*)&s.coarse_w[bin_of(x[k])], (unsigned long long)u);
+          if (u[k]) atomicAdd((unsigned long long*)&s.coarse_w[bin_of(x[k])], (unsigned long long)u[k]);
         }
-      }
+      });
       __syncthreads();
     }
 
@@ -396,16 +447,14 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
       __syncthreads();
       if (tid == 0) s.count = 0;
       __syncthreads();
-      for (int g = tid; g < groups; g += NTHR) {
-        float x[W];
-        group(g, x);
+      each_group([&](int , float (&x)[W]) __attribute__((always_inline)) {
 #pragma unroll
         for (int k = 0; k < W; ++k) {
           if (x[k] == kNegInf || (bin >= 0 && bin_of(x[k]) != bin)) continue;
           const uint32_t at = atomicAdd(&s.count, 1u);
           if (at < (uint32_t)kList) s.list[at] = key_of(x[k]);
         }
-      }
+      });
       __syncthreads();
       held = bin;
       in_list = s.count <= (uint32_t)kList;
@@ -415,13 +464,11 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
         const int n = (int)s.count;
         for (int i = tid; i < n; i += NTHR) fn(s.list[i]);
       } else {
-        for (int g = tid; g < groups; g += NTHR) {
-          float x[W];
-          group(g, x);
+        each_group([&](int , float (&x)[W]) __attribute__((always_inline)) {
 #pragma unroll
           for (int k = 0; k < W; ++k)
             if (x[k] != kNegInf && (held < 0 || bin_of(x[k]) == held)) fn(key_of(x[k]));
-        }
+        });
       }
     };
     // Within the held bin: the key at which the running sum (of 1 for each logit, or
@@ -530,55 +577,55 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
     for (int k = 0; k < W; ++k) {
       u[k] = 0;
       tie[k] = false;
-      if (x[k] == kNegInf) continue;
+      const bool valid = x[k] != kNegInf;
       const uint32_t key = key_of(x[k]);
-      tie[k] = key == thr;
-      if (key > thr) {
-        const double w = weigh.weight(x[k]);
-        if (w >= (double)min_p) u[k] = Weigh::units(w);
-      }
+      tie[k] = valid && key == thr;
+      const double w = weigh.weight(x[k]);
+      if (valid && key > thr && w >= (double)min_p) u[k] = Weigh::units(w);
     }
   };
-  // A tile's kept logits are first moved together, so that weights are computed for
-  // them alone: where top_p keeps a sixth of a row, a sixth of the exponentials.
-  float* together = s.together[wave];
+  Vec<F> ahead;  // of the next tile, where it lies within an unmasked row
+  auto inside = [&](int t) __attribute__((always_inline)) { return !mask && t > 0 && (t + 1) * 64 * W - shift <= N; };
+  auto ask = [&](int t) __attribute__((always_inline)) {
+    if (inside(t)) ahead.w = *reinterpret_cast<const u32x4*>(row + ((t * 64 + lane) * W - shift));
+  };
+  ask(wave);
   for (int t = wave; t < tiles; t += NTHR / 64) {
     const int g = t * 64 + lane;
     float x[W];
-    if (g < groups) {
+    if (inside(t)) {
+#pragma unroll
+      for (int k = 0; k < W; ++k) x[k] = legal(F::get(ahead.e[k]));
+    } else if (g < groups) {
       group(g, x);
     } else {
 #pragma unroll
       for (int k = 0; k < W; ++k) x[k] = kNegInf;
     }
-    int many = 0;
+    ask(t + NTHR / 64);
     uint32_t ties = 0;
+    bool above[W], some = false;
 #pragma unroll
     for (int k = 0; k < W; ++k) {
       const uint32_t key = key_of(x[k]);
-      const bool legal = x[k] != kNegInf, above = legal && key > thr;
-      const uint64_t who = __ballot(above);
-      if (above) together[many + __popcll(who & ~(~0ull << lane))] = x[k];
-      many += __popcll(who);
-      ties += __popcll(__ballot(legal && key == thr));
+      const bool valid = x[k] != kNegInf;
+      above[k] = valid && key > thr;
+      some |= above[k];
+      ties += __popcll(__ballot(valid && key == thr));
     }
-    uint64_t sum = 0;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // written and read by this wave alone
-    __builtin_amdgcn_wave_barrier();
-    for (int i = lane; i < many; i += 64) {
-      const double w = weigh.weight(together[i]);
-      if (w >= (double)min_p) sum += Weigh::units(w);
-    }
-    if (many) {
+    double sum = 0.0;  // in units, below 2^53 for a tile: a whole number
+    if (__ballot(some)) {
 #pragma unroll
-      for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o);
+      for (int k = 0; k < W; ++k) {
+        const double w = weigh.weight(x[k]);
+        sum += above[k] && w >= (double)min_p ? Weigh::whole(w) : 0.0;
+      }
+      sum = wave_sum_last(sum);
     }
-    if (lane == 0) {
-      s.tile_w[t] = sum;
+    if (lane == 63) {
+      s.tile_w[t] = (uint64_t)sum;
       s.tile_n[t] = ties;
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
   }
   __syncthreads();
   if (wave != 0) return;
