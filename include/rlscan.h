@@ -469,6 +469,17 @@ rlscan_status rlscan_sample_actions(rlscan_format fmt, const void *logits, int64
                                     float top_p, float min_p, int64_t *actions, float *log_probs, int64_t R, int64_t N,
                                     hipStream_t stream);
 
+/* The same, with scratch memory through which blocks share rows where these are few and
+ * long: workspace of rlscan_sample_actions_workspace(R, N) bytes (-1: sizes out of
+ * range; 0: not used), or NULL for one block a row.  The results are the same. */
+int64_t rlscan_sample_actions_workspace(int64_t R, int64_t N);
+rlscan_status rlscan_sample_actions_shared(rlscan_format fmt, const void *logits, int64_t stride, const uint8_t *mask,
+                                           const float *uniforms, const float *temperatures, const int32_t *top_ks,
+                                           const float *top_ps, const float *min_ps, float temperature, int32_t top_k,
+                                           float top_p, float min_p, int64_t *actions, float *log_probs,
+                                           void *workspace, int64_t workspace_bytes, int64_t R, int64_t N,
+                                           hipStream_t stream);
+
 /* Log-probability of the taken action and entropy of softmax(logits /
  * temperature) over the legal actions of each row.
  * In:  logits, mask as above; actions [R] int64: one outside [0,N) (a padded

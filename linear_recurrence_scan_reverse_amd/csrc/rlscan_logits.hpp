@@ -34,7 +34,11 @@ struct SampleArgs {
   int64_t* action;        // [R]
   float* log_prob;        // [R] or NULL
   int64_t R, N;
+  void* shared;           // workspace where blocks share a row, or NULL
+  int64_t shared_words;   // of 8 bytes, for one row
+  int slices, tiles, slice_tiles;
 };
+int64_t sample_workspace(int64_t R, int64_t N);  // bytes; 0: rows are not shared
 hipError_t launch_sample(rlscan_format f, const SampleArgs& a, hipStream_t st);
 
 struct LogProbArgs {

@@ -15,20 +15,23 @@
 // a row is shared changes an action.
 //
 // A kept set is a prefix of the falling order: all logits above a threshold and
-// the first `quota` of those equal to it.  One block takes a row.  Long rows go by
-// bins of max - x, which spread the LDS atomics (bins of the keys' leading bits put
-// most logits into some fifty: twice the time).  A pass after the one for the
-// maximum counts each bin's logits, for top_k, which leaves a few hundred that it can
-// keep.  They are collected in LDS, ranked against each other, and the rest of the
-// work is on them alone.  Without top_k, or where it leaves more, the threshold is
-// searched instead: by the bins' weights, then in the one bin that it falls into by
-// 8-bit digits of the keys; a last pass sums the kept weights of tiles of the row,
-// and one wave finds the tile and in it the action.
+// the first `quota` of those equal to it.  Long rows go by bins of max - x, which
+// spread the LDS atomics (bins of the keys' leading bits put most logits into some fifty:
+// twice the time).  A pass after the one for the maximum counts each bin's logits, for
+// top_k, which leaves a few hundred that it can keep.  They are collected in LDS, ranked
+// against each other, and the rest of the work is on them alone.  Without top_k, or where
+// it leaves more, the threshold is searched instead: by the bins' weights, then in the
+// one bin that it falls into, each logit against all or by 8-bit digits of the keys; a last
+// pass sums the kept weights of tiles of the row, and one wave finds the tile and in it
+// the action.  One block takes a row; where rows are few and long, blocks share the passes
+// (slice_kernel) and one block for each row makes the choice.
 //
 // 256 rows of 64007 bfloat16 logits with top_k up to 100: 79 us, of which reading them
-// takes 6 and the few rows without a top_k nearly all; one row of 131072 float32 logits
-// with top_p alone: 122 us on its one CU.  Both are bound by the instructions of the
-// float64 exponentials, some 40 for each logit, in two passes.
+// takes 6 and the few rows without a top_k nearly all: two passes with some 40 instructions
+// a logit for the float64 exponential, by one compute unit.  One row of 131072 float32
+// logits with top_p alone: 3.2, 7.3 and 10.7 us for the three shared passes and 10.6 for the
+// choice; a chain of four kernels that each wait for memory a few times (122 us on one
+// compute unit).
 #include "rlscan_logits.hpp"
 
 namespace rlscan {
@@ -203,6 +206,17 @@ __device__ __forceinline__ void search_bins(SampleLds<NTHR>& s, const V* bins, i
   __syncthreads();
 }
 
+// What a prefix must reach to have top_p of the weight.
+__device__ __forceinline__ double weight_target(uint64_t kept, float top_p) {
+  const double target = (double)top_p * (double)kept;
+  return target >= 1.0 ? target : 1.0;  // the largest is always kept
+}
+
+// Searches the bins' weights for the bin in which the target is reached.
+__device__ __forceinline__ void cut_weight(SampleLds<1024>& s, uint64_t kept, float top_p) {
+  search_bins<1024, 4>(s, s.coarse_w, kBins, 0, weight_target(kept, top_p), false);
+}
+
 // The rest of a row's work on the n <= kFew logits in s.few, by the whole block.
 template <class F, int NTHR>
 __device__ __forceinline__ void take_few(SampleLds<NTHR>& s, const SampleArgs& a, int64_t r, const Weigh& weigh, int n,
@@ -282,33 +296,35 @@ __device__ __forceinline__ void take_few(SampleLds<NTHR>& s, const SampleArgs& a
   }
 }
 
-template <class F, int NTHR>
-__global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
-  constexpr int W = F::W;
-  __shared__ SampleLds<NTHR> s;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t r = blockIdx.x;
-  const auto* row = static_cast<const typename F::E*>(a.x) + r * a.stride;
-  const uint8_t* mask = a.mask ? a.mask + r * a.N : nullptr;
-  const int N = (int)a.N;
-  // groups of W logits on the row's 16-byte boundaries; the row begins `shift` into the first
-  const int shift = (int)(((uintptr_t)row / sizeof(typename F::E)) % W);
-  const int groups = (N + shift + W - 1) / W;
-
-  float temperature = a.temperature ? a.temperature[r] : a.temperature1;
-  int top_k = a.top_k ? a.top_k[r] : a.top_k1;
-  const float top_p = a.top_p ? a.top_p[r] : a.top_p1;
-  float min_p = a.min_p ? a.min_p[r] : a.min_p1;
-  if (!(temperature > 0.0f)) {  // greedy: the largest logit, lowest index first
-    temperature = 1.0f;
-    top_k = 1;
+// A row of logits and its settings.
+template <class F>
+struct Row {
+  static constexpr int W = F::W;
+  const typename F::E* row;
+  const uint8_t* mask;
+  int N, shift, groups;  // groups of W logits on 16-byte boundaries; the row begins `shift` into the first
+  float temperature, top_p, min_p;
+  int top_k;
+  __device__ __forceinline__ Row(const SampleArgs& a, int64_t r) {
+    row = static_cast<const typename F::E*>(a.x) + r * a.stride;
+    mask = a.mask ? a.mask + r * a.N : nullptr;
+    N = (int)a.N;
+    shift = (int)(((uintptr_t)row / sizeof(typename F::E)) % W);
+    groups = (N + shift + W - 1) / W;
+    temperature = a.temperature ? a.temperature[r] : a.temperature1;
+    top_k = a.top_k ? a.top_k[r] : a.top_k1;
+    top_p = a.top_p ? a.top_p[r] : a.top_p1;
+    min_p = a.min_p ? a.min_p[r] : a.min_p1;
+    if (!(temperature > 0.0f)) {  // greedy: the largest logit, lowest index first
+      temperature = 1.0f;
+      top_k = 1;
+    }
+    min_p = min_p > 0.0f ? fminf(min_p, 1.0f) : 0.0f;
   }
-  min_p = min_p > 0.0f ? fminf(min_p, 1.0f) : 0.0f;
-
   // NaN is not legal; +inf counts as the largest float
-  auto legal = [](float x) __attribute__((always_inline)) { return x > kNegInf ? fminf(x, kMaxFloat) : kNegInf; };
-  // the logits of group g, -inf where not legal
-  auto group = [&](int g, float (&x)[W]) __attribute__((always_inline)) {
+  static __device__ __forceinline__ float legal(float x) { return x > kNegInf ? fminf(x, kMaxFloat) : kNegInf; }
+  // the logits of group g, -inf where not legal or outside the row
+  __device__ __forceinline__ void group(int g, float (&x)[W]) const {
     const int i = g * W - shift;
     if (i >= 0 && i + W <= N) {
       Vec<F> v;
@@ -324,7 +340,182 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
       if (mask && i + k >= 0 && i + k < N && mask[i + k] == 0) x[k] = kNegInf;
       x[k] = legal(x[k]);
     }
-  };
+  }
+  // bins of 32 temperatures below the maximum; lower logits share the last
+  __device__ __forceinline__ float per_bin() const { return fminf((float)kBins / (32.0f * temperature), 1e30f); }
+  static __device__ __forceinline__ int bin(float top, float per, float x) {
+    return (int)fminf((top - x) * per, (float)(kBins - 1));
+  }
+};
+
+// What the blocks of a shared row leave in the workspace for each other.
+struct Shared {
+  uint64_t* w;       // [kBins] the bins' weight, where top_p is on and top_k is not
+  uint64_t* list;    // [kMiddle] key << 32 | ~index
+  uint32_t* n;       // [kBins] logits in each bin, where top_k is on
+  uint64_t* tile;    // [tiles] kept weight, without what is in the list
+  float* top;        // [slices] largest logit
+  uint32_t* listed;  // [1] logits that belong in the list
+  uint64_t* cut;     // [3] top_k: candidates, 0 if the list does not hold them; else the bin that
+                     // top_p cuts, the weight before it and the row's
+  static int64_t words(int64_t tiles, int64_t slices) {  // of 8 bytes, for one row
+    return kBins + kMiddle + kBins / 2 + 3 + tiles + (slices + 2) / 2;
+  }
+  __device__ __forceinline__ Shared(const SampleArgs& a, int64_t r) {
+    w = static_cast<uint64_t*>(a.shared) + r * a.shared_words;
+    list = w + kBins;
+    n = reinterpret_cast<uint32_t*>(list + kMiddle);
+    cut = reinterpret_cast<uint64_t*>(n + kBins);
+    tile = cut + 3;
+    top = reinterpret_cast<float*>(tile + a.tiles);
+    listed = reinterpret_cast<uint32_t*>(top + a.slices);
+  }
+};
+
+// The passes over a shared row, `slices` blocks a row, each over a.slice_tiles tiles:
+// 0, the maximum; 1, the bins; 2, the kept weight of tiles and the logits of the bin
+// that is cut (with a top_k, the logits down to that bin).
+template <class F, int STAGE>
+__global__ void __launch_bounds__(1024) slice_kernel(const SampleArgs a) {
+  constexpr int W = F::W, NTHR = 1024;
+  __shared__ SampleLds<NTHR> s;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t r = blockIdx.x / a.slices;
+  const int slice = (int)(blockIdx.x % a.slices);
+  const Row<F> in(a, r);
+  const Shared sh(a, r);
+  const int tiles = (in.groups + 63) / 64, t0 = slice * a.slice_tiles;
+  const int t1 = t0 + a.slice_tiles < tiles ? t0 + a.slice_tiles : tiles;
+  float top = kNegInf;
+  if constexpr (STAGE == 0) {
+    for (int i = slice * NTHR + tid; i < kBins; i += a.slices * NTHR) {
+      sh.w[i] = 0;
+      sh.n[i] = 0;
+    }
+    if (slice == 0 && tid == 0) *sh.listed = 0;
+    for (int t = t0 + wave; t < t1; t += NTHR / 64) {
+      const int g = t * 64 + lane;
+      if (g >= in.groups) break;
+      float x[W];
+      in.group(g, x);
+#pragma unroll
+      for (int k = 0; k < W; ++k) top = fmaxf(top, x[k]);
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+    if (lane == 0) s.redf[wave] = top;
+    __syncthreads();
+    for (int n = 0; n < NTHR / 64; ++n) top = fmaxf(top, s.redf[n]);
+    if (tid == 0) sh.top[slice] = top;
+  } else {
+    for (int i = 0; i < a.slices; ++i) top = fmaxf(top, sh.top[i]);
+    if (top == kNegInf) return;  // no legal action: the whole block leaves
+    const bool need_k = in.top_k > 0 && in.top_k < in.N, need_p = in.top_p < 1.0f;
+    if (tid < 64) s.table[tid] = exp2((double)tid / 64.0);
+    const Weigh weigh{(double)top, 1.0 / (double)in.temperature, s.table};
+    const float per = in.per_bin();
+    if constexpr (STAGE == 1) {
+      if (!need_k && !need_p) return;
+      for (int i = tid; i < kBins; i += NTHR) {
+        s.coarse_n[i] = 0;
+        s.coarse_w[i] = 0;
+      }
+      __syncthreads();
+      for (int t = t0 + wave; t < t1; t += NTHR / 64) {
+        const int g = t * 64 + lane;
+        if (g >= in.groups) break;
+        float x[W];
+        in.group(g, x);
+        if (need_k) {
+#pragma unroll
+          for (int k = 0; k < W; ++k)
+            if (x[k] != kNegInf) atomicAdd(&s.coarse_n[Row<F>::bin(top, per, x[k])], 1u);
+        } else {
+          uint64_t u[W];
+#pragma unroll
+          for (int k = 0; k < W; ++k) u[k] = Weigh::units(weigh.weight(x[k]));
+#pragma unroll
+          for (int k = 0; k < W; ++k)
+            if (u[k]) atomicAdd((unsigned long long*)&s.coarse_w[Row<F>::bin(top, per, x[k])], (unsigned long long)u[k]);
+        }
+      }
+      __syncthreads();
+      for (int i = tid; i < kBins; i += NTHR) {
+        if (s.coarse_n[i]) atomicAdd(&sh.n[i], s.coarse_n[i]);
+        if (s.coarse_w[i]) atomicAdd((unsigned long long*)&sh.w[i], (unsigned long long)s.coarse_w[i]);
+      }
+    } else {
+      int cut = kBins;
+      if (need_k) {
+        for (int i = tid; i < kBins; i += NTHR) s.coarse_n[i] = sh.n[i];
+        search_bins<NTHR, 4>(s, s.coarse_n, kBins, 0, (double)in.top_k, false);
+        const uint64_t candidates = s.before + s.inside;
+        const bool listed = candidates >= (uint64_t)in.top_k && candidates <= (uint64_t)kFew;
+        if (slice == 0 && tid == 0) sh.cut[0] = listed ? candidates : 0;
+        if (!listed) return;  // passed over again
+        cut = s.bin;
+      } else if (need_p) {
+        uint64_t w = 0;
+        for (int i = tid; i < kBins; i += NTHR) w += s.coarse_w[i] = sh.w[i];
+        const uint64_t kept = block_sum<NTHR>(w, s.red);
+        cut_weight(s, kept, in.top_p);
+        cut = s.bin;
+        if (slice == 0 && tid == 0) {
+          sh.cut[0] = (uint64_t)cut;
+          sh.cut[1] = s.before;
+          sh.cut[2] = kept;
+        }
+      }
+      __syncthreads();
+      for (int t = t0 + wave; t < t1; t += NTHR / 64) {
+        const int g = t * 64 + lane;
+        float x[W];
+        if (g < in.groups) {
+          in.group(g, x);
+        } else {
+#pragma unroll
+          for (int k = 0; k < W; ++k) x[k] = kNegInf;
+        }
+        double sum = 0.0;  // in units, below 2^53 for a tile: a whole number
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+          const int b = Row<F>::bin(top, per, x[k]);
+          const bool valid = x[k] != kNegInf;
+          if (need_k || need_p) {
+            if (valid && (need_k ? b <= cut : b == cut)) {
+              const uint32_t at = atomicAdd(sh.listed, 1u);
+              if (at < (uint32_t)kMiddle) sh.list[at] = (uint64_t)key_of(x[k]) << 32 | (uint32_t)~(g * W - in.shift + k);
+            }
+          }
+          const double w = weigh.weight(x[k]);
+          sum += valid && b < cut && w >= (double)in.min_p ? Weigh::whole(w) : 0.0;
+        }
+        if (!need_k) {
+          sum = wave_sum_last(sum);
+          if (lane == 63) sh.tile[t] = (uint64_t)sum;
+        }
+      }
+    }
+  }
+}
+
+// SHARED: slice_kernel has passed over the row, and what it left in the workspace is
+// taken; where that is not enough (a list that does not hold a bin, more than kFew
+// candidates of a top_k) the row is passed over again as without.
+template <class F, int NTHR, bool SHARED>
+__global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
+  constexpr int W = F::W;
+  __shared__ SampleLds<NTHR> s;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t r = blockIdx.x;
+  const Row<F> in(a, r);
+  const auto* row = in.row;
+  const bool mask = in.mask != nullptr;
+  const int N = in.N, shift = in.shift, groups = in.groups;
+  const float temperature = in.temperature, top_p = in.top_p, min_p = in.min_p;
+  const int top_k = in.top_k;
+  auto legal = [](float x) __attribute__((always_inline)) { return Row<F>::legal(x); };
+  auto group = [&](int g, float (&x)[W]) __attribute__((always_inline)) { in.group(g, x); };
   // Calls fn(g, x) for each of the thread's groups.  Unmasked long rows ask for 64 bytes
   // at a time (one row of 131072 float32 logits: 121 us; 134 with 16 bytes).
   auto each_group = [&](auto fn) __attribute__((always_inline)) {
@@ -365,10 +556,16 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
 
   // ---- maximum
   float top = kNegInf;
-  each_group([&](int , float (&x)[W]) __attribute__((always_inline)) {
+  const Shared sh(a, r);
+  bool taken = SHARED && !need_k;  // the tiles' weights, and the list, are in the workspace
+  if (SHARED) {
+    for (int i = tid; i < a.slices; i += NTHR) top = fmaxf(top, sh.top[i]);
+  } else {
+    each_group([&](int, float (&x)[W]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int k = 0; k < W; ++k) top = fmaxf(top, x[k]);
-  });
+      for (int k = 0; k < W; ++k) top = fmaxf(top, x[k]);
+    });
+  }
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
   if (lane == 0) s.redf[wave] = top;
@@ -391,43 +588,51 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
   if (need_k || need_p) {
     uint64_t before_k = 0;  // logits in the bins before the one that top_k cuts
     int bin_k = kBins;
-    const float per = fminf((float)kBins / (32.0f * temperature), 1e30f);
-    auto bin_of = [&](float x) __attribute__((always_inline)) { return (int)fminf((top - x) * per, (float)(kBins - 1)); };
-    if (coarse && need_k) {
-      for (int i = tid; i < kBins; i += NTHR) s.coarse_n[i] = 0;
+    const float per = in.per_bin();
+    auto bin_of = [&](float x) __attribute__((always_inline)) { return Row<F>::bin(top, per, x); };
+    const uint64_t shared_few = SHARED && need_k ? sh.cut[0] : 0;
+    if (coarse && need_k && shared_few == 0) {
+      for (int i = tid; i < kBins; i += NTHR) s.coarse_n[i] = SHARED ? sh.n[i] : 0;
       __syncthreads();
-      each_group([&](int , float (&x)[W]) __attribute__((always_inline)) {
+      if (!SHARED) {
+        each_group([&](int, float (&x)[W]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int k = 0; k < W; ++k)
-          if (x[k] != kNegInf) atomicAdd(&s.coarse_n[bin_of(x[k])], 1u);
-      });
+          for (int k = 0; k < W; ++k)
+            if (x[k] != kNegInf) atomicAdd(&s.coarse_n[bin_of(x[k])], 1u);
+        });
+      }
       search_bins<NTHR, 4>(s, s.coarse_n, kBins, 0, (double)top_k, false);
       before_k = s.before;
       bin_k = s.bin;
       need_k = s.before + s.inside >= (uint64_t)top_k;
     }
-    const uint64_t candidates = coarse ? (need_k ? before_k + s.inside : (uint64_t)N) : (uint64_t)N;
+    const uint64_t candidates = shared_few ? shared_few : coarse && need_k ? before_k + s.inside : (uint64_t)N;
     if (candidates <= (uint64_t)kFew) {
       __syncthreads();
       if (tid == 0) s.count = 0;
       __syncthreads();
-      each_group([&](int g, float (&x)[W]) __attribute__((always_inline)) {
+      if (SHARED) {
+        if (tid == 0) s.count = (uint32_t)candidates;
+        for (int i = tid; i < (int)candidates; i += NTHR) s.few[i] = sh.list[i];
+      } else {
+        each_group([&](int g, float (&x)[W]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int k = 0; k < W; ++k) {
-          if (x[k] == kNegInf || (coarse && need_k && bin_of(x[k]) > bin_k)) continue;
-          const uint32_t at = atomicAdd(&s.count, 1u);  // at most kFew: the bins were counted
-          if (at < (uint32_t)kFew) s.few[at] = (uint64_t)key_of(x[k]) << 32 | (uint32_t)~(g * W - shift + k);
-        }
-      });
+          for (int k = 0; k < W; ++k) {
+            if (x[k] == kNegInf || (coarse && need_k && bin_of(x[k]) > bin_k)) continue;
+            const uint32_t at = atomicAdd(&s.count, 1u);  // at most kFew: the bins were counted
+            if (at < (uint32_t)kFew) s.few[at] = (uint64_t)key_of(x[k]) << 32 | (uint32_t)~(g * W - shift + k);
+          }
+        });
+      }
       __syncthreads();
       const int n = (int)s.count < kFew ? (int)s.count : kFew;
       take_few<F, NTHR>(s, a, r, weigh, n, need_k ? top_k : n, top_p, min_p);
       return;
     }
-    if (coarse && need_p) {
+    if (coarse && need_p && !taken) {
       for (int i = tid; i < kBins; i += NTHR) s.coarse_w[i] = 0;
       __syncthreads();
-      each_group([&](int , float (&x)[W]) __attribute__((always_inline)) {
+      each_group([&](int, float (&x)[W]) __attribute__((always_inline)) {
         uint64_t u[W];
 #pragma unroll
         for (int k = 0; k < W; ++k) u[k] = Weigh::units(weigh.weight(x[k]));
@@ -445,9 +650,20 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
     auto collect = [&](int bin) __attribute__((always_inline)) {
       if (held == bin) return;
       __syncthreads();
+      if (SHARED && taken) {
+        taken = *sh.listed <= (uint32_t)kList;
+        if (taken) {
+          if (tid == 0) s.count = *sh.listed;
+          for (int i = tid; i < (int)*sh.listed; i += NTHR) s.list[i] = (uint32_t)(sh.list[i] >> 32);
+          __syncthreads();
+          held = bin;
+          in_list = true;
+          return;
+        }
+      }
       if (tid == 0) s.count = 0;
       __syncthreads();
-      each_group([&](int , float (&x)[W]) __attribute__((always_inline)) {
+      each_group([&](int, float (&x)[W]) __attribute__((always_inline)) {
 #pragma unroll
         for (int k = 0; k < W; ++k) {
           if (x[k] == kNegInf || (bin >= 0 && bin_of(x[k]) != bin)) continue;
@@ -464,7 +680,7 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
         const int n = (int)s.count;
         for (int i = tid; i < n; i += NTHR) fn(s.list[i]);
       } else {
-        each_group([&](int , float (&x)[W]) __attribute__((always_inline)) {
+        each_group([&](int, float (&x)[W]) __attribute__((always_inline)) {
 #pragma unroll
           for (int k = 0; k < W; ++k)
             if (x[k] != kNegInf && (held < 0 || bin_of(x[k]) == held)) fn(key_of(x[k]));
@@ -475,6 +691,31 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
     // of its weight) reaches target, from `base`; leaves the sum before that key in
     // s.before and that of all logits equal to it in s.inside.
     auto descend = [&](bool weights, uint64_t base, double target) __attribute__((always_inline)) {
+      if (in_list && s.count <= (uint32_t)kFew) {  // each against all, at once
+        const int n = (int)s.count;
+        for (int i = tid; i < n; i += NTHR) s.kept[i] = weights ? Weigh::units(weigh.weight(value_of(s.list[i]))) : 1;
+        __syncthreads();
+        for (int i = tid; i < n; i += NTHR) {
+          const uint32_t mine = s.list[i];
+          uint64_t above = base, same = 0, below = 0;
+          for (int j = 0; j < n; ++j) {
+            const uint32_t key = s.list[j];
+            const uint64_t v = s.kept[j];
+            above += key > mine ? v : 0;
+            same += key == mine ? v : 0;
+            below += key < mine ? v : 0;
+          }
+          // the last key with anything if none reaches it
+          const bool reaches = (double)above < target && (double)(above + same) >= target;
+          if (reaches || (same > 0 && below == 0 && (double)(above + same) < target)) {
+            s.rank[0] = mine;
+            s.before = above;
+            s.inside = same;
+          }
+        }
+        __syncthreads();
+        return s.rank[0];
+      }
       uint32_t prefix = 0, known = 0;
 #pragma unroll 1
       for (int d = 24; d + 8 > F::kLow; d -= 8) {
@@ -521,7 +762,9 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
     if (need_p) {
       int bin = -1;
       uint64_t base = 0;
-      if (!need_k) {
+      if (SHARED && taken) {
+        kept = sh.cut[2];
+      } else if (!need_k) {
         uint64_t w = 0;
         if (coarse) {
           for (int i = tid; i < kBins; i += NTHR) w += s.coarse_w[i];
@@ -531,14 +774,16 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
         }
         kept = block_sum<NTHR>(w, s.red);
       }
-      double target = (double)top_p * (double)kept;
-      if (!(target >= 1.0)) target = 1.0;  // the largest is always kept
-      if (coarse) {
-        if (need_k && (double)kept_before < target) {
+      const double target = weight_target(kept, top_p);
+      if constexpr (coarse) {
+        if (SHARED && taken) {
+          bin = (int)sh.cut[0];
+          base = sh.cut[1];
+        } else if (need_k && (double)kept_before < target) {
           bin = bin_k;
           base = kept_before;
         } else {
-          search_bins<NTHR, 4>(s, s.coarse_w, kBins, 0, target, false);
+          cut_weight(s, kept, top_p);
           bin = s.bin;
           base = s.before;
         }
@@ -584,47 +829,63 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
       if (valid && key > thr && w >= (double)min_p) u[k] = Weigh::units(w);
     }
   };
-  Vec<F> ahead;  // of the next tile, where it lies within an unmasked row
-  auto inside = [&](int t) __attribute__((always_inline)) { return !mask && t > 0 && (t + 1) * 64 * W - shift <= N; };
-  auto ask = [&](int t) __attribute__((always_inline)) {
-    if (inside(t)) ahead.w = *reinterpret_cast<const u32x4*>(row + ((t * 64 + lane) * W - shift));
-  };
-  ask(wave);
-  for (int t = wave; t < tiles; t += NTHR / 64) {
-    const int g = t * 64 + lane;
-    float x[W];
-    if (inside(t)) {
-#pragma unroll
-      for (int k = 0; k < W; ++k) x[k] = legal(F::get(ahead.e[k]));
-    } else if (g < groups) {
-      group(g, x);
-    } else {
-#pragma unroll
-      for (int k = 0; k < W; ++k) x[k] = kNegInf;
+  if (SHARED && taken) {
+    for (int t = tid; t < tiles; t += NTHR) {
+      s.tile_w[t] = sh.tile[t];
+      s.tile_n[t] = 0;
     }
-    ask(t + NTHR / 64);
-    uint32_t ties = 0;
-    bool above[W], some = false;
-#pragma unroll
-    for (int k = 0; k < W; ++k) {
-      const uint32_t key = key_of(x[k]);
-      const bool valid = x[k] != kNegInf;
-      above[k] = valid && key > thr;
-      some |= above[k];
-      ties += __popcll(__ballot(valid && key == thr));
+    __syncthreads();
+    const int listed = need_p ? (int)*sh.listed : 0;
+    for (int i = tid; i < listed; i += NTHR) {
+      const uint32_t key = (uint32_t)(sh.list[i] >> 32);
+      const int t = ((int)~(uint32_t)sh.list[i] + shift) / W / 64;
+      const double w = weigh.weight(value_of(key));
+      if (key > thr && w >= (double)min_p) atomicAdd((unsigned long long*)&s.tile_w[t], (unsigned long long)Weigh::units(w));
+      if (key == thr) atomicAdd(&s.tile_n[t], 1u);
     }
-    double sum = 0.0;  // in units, below 2^53 for a tile: a whole number
-    if (__ballot(some)) {
+  } else {
+    Vec<F> ahead;  // of the next tile, where it lies within an unmasked row
+    auto inside = [&](int t) __attribute__((always_inline)) { return !mask && t > 0 && (t + 1) * 64 * W - shift <= N; };
+    auto ask = [&](int t) __attribute__((always_inline)) {
+      if (inside(t)) ahead.w = *reinterpret_cast<const u32x4*>(row + ((t * 64 + lane) * W - shift));
+    };
+    ask(wave);
+    for (int t = wave; t < tiles; t += NTHR / 64) {
+      const int g = t * 64 + lane;
+      float x[W];
+      if (inside(t)) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) x[k] = legal(F::get(ahead.e[k]));
+      } else if (g < groups) {
+        group(g, x);
+      } else {
+#pragma unroll
+        for (int k = 0; k < W; ++k) x[k] = kNegInf;
+      }
+      ask(t + NTHR / 64);
+      uint32_t ties = 0;
+      bool above[W], some = false;
 #pragma unroll
       for (int k = 0; k < W; ++k) {
-        const double w = weigh.weight(x[k]);
-        sum += above[k] && w >= (double)min_p ? Weigh::whole(w) : 0.0;
+        const uint32_t key = key_of(x[k]);
+        const bool valid = x[k] != kNegInf;
+        above[k] = valid && key > thr;
+        some |= above[k];
+        ties += __popcll(__ballot(valid && key == thr));
       }
-      sum = wave_sum_last(sum);
-    }
-    if (lane == 63) {
-      s.tile_w[t] = (uint64_t)sum;
-      s.tile_n[t] = ties;
+      double sum = 0.0;  // in units, below 2^53 for a tile: a whole number
+      if (__ballot(some)) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+          const double w = weigh.weight(x[k]);
+          sum += above[k] && w >= (double)min_p ? Weigh::whole(w) : 0.0;
+        }
+        sum = wave_sum_last(sum);
+      }
+      if (lane == 63) {
+        s.tile_w[t] = (uint64_t)sum;
+        s.tile_n[t] = ties;
+      }
     }
   }
   __syncthreads();
@@ -735,11 +996,43 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
   }
 }
 
+// Blocks that share a row.  Where rows are few and long, the compute units that they leave
+// idle pay for three more launches.  One block a row against shared, us: one row of
+// 131072 float32, top_p 0.9: 122, 36.  Bfloat16, top_p 0.9, then top_k 50: 64 rows of
+// 64007: 74, 45 and 35, 35; 128 rows: 76, 99 and 36, 75; 64 rows of 32768: 43, 38 and
+// 24, 33 (which settings a row has is known on the device only); of 8192: 26, 40 and 19, 33.
+int64_t sample_slices(int64_t R, int64_t N) {
+  return R < 1 || R > 64 || N < 32768 ? 1 : 256 / R < N / 4096 ? 256 / R : N / 4096;
+}
+
+// Groups of a row that begins anywhere, in tiles of 64.
+static int64_t tiles_of(int64_t N, int W) { return (((N + 2 * (W - 1)) / W) + 63) / 64; }
+
+int64_t sample_workspace(int64_t R, int64_t N) {
+  const int64_t slices = sample_slices(R, N);
+  return slices > 1 ? R * Shared::words(tiles_of(N, 4), slices) * 8 : 0;
+}
+
 template <class F>
-hipError_t sample_fmt(const SampleArgs& a, hipStream_t st) {
-  if (a.N <= kSmall) sample_kernel<F, 64><<<dim3((unsigned)a.R), 64, 0, st>>>(a);
-  else if (a.N <= kMiddle) sample_kernel<F, 256><<<dim3((unsigned)a.R), 256, 0, st>>>(a);
-  else sample_kernel<F, 1024><<<dim3((unsigned)a.R), 1024, 0, st>>>(a);
+hipError_t sample_fmt(const SampleArgs& given, hipStream_t st) {
+  SampleArgs a = given;
+  a.slices = a.shared ? (int)sample_slices(a.R, a.N) : 1;
+  if (a.slices > 1) {
+    a.tiles = (int)tiles_of(a.N, F::W);
+    a.slice_tiles = (a.tiles + a.slices - 1) / a.slices;
+    a.shared_words = Shared::words(a.tiles, a.slices);
+    const dim3 grid((unsigned)(a.R * a.slices));
+    slice_kernel<F, 0><<<grid, 1024, 0, st>>>(a);
+    slice_kernel<F, 1><<<grid, 1024, 0, st>>>(a);
+    slice_kernel<F, 2><<<grid, 1024, 0, st>>>(a);
+    sample_kernel<F, 1024, true><<<dim3((unsigned)a.R), 1024, 0, st>>>(a);
+  } else if (a.N <= kSmall) {
+    sample_kernel<F, 64, false><<<dim3((unsigned)a.R), 64, 0, st>>>(a);
+  } else if (a.N <= kMiddle) {
+    sample_kernel<F, 256, false><<<dim3((unsigned)a.R), 256, 0, st>>>(a);
+  } else {
+    sample_kernel<F, 1024, false><<<dim3((unsigned)a.R), 1024, 0, st>>>(a);
+  }
   return hipGetLastError();
 }
 

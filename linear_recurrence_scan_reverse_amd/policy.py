@@ -347,9 +347,11 @@ def sample_actions(logits, uniforms, *, temperature=1.0, top_k=None, top_p=None,
             log_probs = torch.empty_like(uniforms)
         else:
             _plain(log_probs, "log_probs", lead, torch.float32, dev)
-        _call("rlscan_sample_actions", _DTYPES[logits.dtype], logits.data_ptr(), stride, _ptr(mask),
-                  uniforms.data_ptr(), _ptr(temps), _ptr(ks), _ptr(ps), _ptr(ms), float(t1), min(int(k1), 2 ** 31 - 1),
-                  float(p1), float(m1), actions.data_ptr(), log_probs.data_ptr(), R, N, _raw_stream(stream, dev))
+        ws, need = _workspace("rlscan_sample_actions_workspace", dev, R, N)
+        _call("rlscan_sample_actions_shared", _DTYPES[logits.dtype], logits.data_ptr(), stride, _ptr(mask),
+              uniforms.data_ptr(), _ptr(temps), _ptr(ks), _ptr(ps), _ptr(ms), float(t1), min(int(k1), 2 ** 31 - 1),
+              float(p1), float(m1), actions.data_ptr(), log_probs.data_ptr(), _ptr(ws), need, R, N,
+              _raw_stream(stream, dev))
     return actions, log_probs
 
 
