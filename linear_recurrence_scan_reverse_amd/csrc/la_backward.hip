@@ -13,7 +13,7 @@
 // marked: there the walks leave S and dS, and the sum starts anew from dg = <S, dS>.
 //
 // Measured: 8 rows of 4096 steps, 16 heads of 128 in bfloat16, gates for each step: 1006 us
-// for the three walks, 24 for the marked boundaries and 26 for the sums of dg; 944 MB and
+// for the three walks, 24 for the marked boundaries and 19 for the sums of dg; 944 MB and
 // 103 Gflop, 180 us of a copy.  128 heads times three walks leave one and a half blocks for
 // a compute unit, each bound by its own chain of products: dq and dk carry two terms for
 // intermediates and three for the float32 sums that dg needs, 3 to 6 matrix
@@ -53,11 +53,15 @@ __global__ void __launch_bounds__(64 * NWV, MINW) backward_kernel(const Args a, 
 
 // dg of one row and head: x_t = u_t - w_t summed from the end, afresh at each episode's last step.
 // A thread takes four steps; the sums of those behind it pass through the wave and the block.
-__global__ void __launch_bounds__(256) decay_grad_kernel(const Args a, const double* u, const double* w, const float* end,
-                                                         const double* mark_dots, int64_t nmarks, int64_t mark_steps,
-                                                         double* total) {
-  __shared__ double sum[4];
-  __shared__ int open[4];
+// Rows past 1024 steps take blocks of 1024 threads: a tile's chain of sums and trips to
+// memory is paid once for 4096 steps (8 rows of 4096, 16 heads: 27 us with 256 threads, 19).
+template <int NTHR>
+__global__ void __launch_bounds__(NTHR) decay_grad_kernel(const Args a, const double* u, const double* w,
+                                                          const float* end, const double* mark_dots, int64_t nmarks,
+                                                          int64_t mark_steps, double* total) {
+  constexpr int kWaves = NTHR / 64;
+  __shared__ double sum[kWaves];
+  __shared__ int open[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t eh = blockIdx.x, e = eh / a.H, h = eh % a.H;
   u += eh * a.T;
@@ -65,9 +69,9 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(const Args a, const dou
   mark_dots += eh * nmarks;
   double carry = (double)end[eh];  // what comes from behind the tile
   double all = 0.0;
-  const int64_t tiles = (a.T + 1023) / 1024;
+  const int64_t tiles = (a.T + NTHR * 4 - 1) / (NTHR * 4);
   for (int64_t n = tiles - 1; n >= 0; --n) {
-    const int64_t t0 = n * 1024 + (int64_t)(255 - tid) * 4;  // later steps in earlier lanes
+    const int64_t t0 = n * (NTHR * 4) + (int64_t)(NTHR - 1 - tid) * 4;  // later steps in earlier lanes
     // this thread's steps from the last: R = x_t + (step t+1 starts afresh ? 0 : R)
     double x[4];
     bool cut[4];  // step t starts afresh: its own gradient is 0 and nothing passes to t-1
@@ -114,7 +118,7 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(const Args a, const dou
     const double before = __shfl_up(run, 1);
     const int before_through = __shfl_up(through, 1);
     double r = lane == 0 ? in : before + (before_through ? in : 0.0);
-    for (int i = wave; i < 4; ++i) in = sum[i] + (open[i] ? in : 0.0);
+    for (int i = wave; i < kWaves; ++i) in = sum[i] + (open[i] ? in : 0.0);
     carry = in;
     __syncthreads();
 #pragma unroll
@@ -134,7 +138,10 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(const Args a, const dou
   for (int o = 1; o < 64; o <<= 1) all += __shfl_xor(all, o);
   if (lane == 0) sum[wave] = all;
   __syncthreads();
-  if (tid == 0) total[eh] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  if (tid == 0) {
+    for (int i = 1; i < kWaves; ++i) all += sum[i];
+    total[eh] = all;
+  }
 }
 
 // <S, dS> at one marked boundary, in float64 and in a fixed order.
@@ -253,8 +260,9 @@ hipError_t launch_backward_fmt(const Args& a, const Backward& b, const Plan& pl,
     }
     if (b.nmarks > 0)
       mark_dot_kernel<<<dim3((unsigned)(a.E * a.H * b.nmarks)), 256, 0, st>>>(b.marks, b.mark_grads, b.mark_dots, pl.KP * pl.VP);
-    decay_grad_kernel<<<dim3((unsigned)(a.E * a.H)), 256, 0, st>>>(a, b.u, b.w, b.end, b.mark_dots, b.nmarks,
-                                                                   a.mark_chunks * pl.C, b.dg_head ? b.total : nullptr);
+    auto decay_grad = a.T > 1024 ? decay_grad_kernel<1024> : decay_grad_kernel<256>;
+    decay_grad<<<dim3((unsigned)(a.E * a.H)), a.T > 1024 ? 1024 : 256, 0, st>>>(
+        a, b.u, b.w, b.end, b.mark_dots, b.nmarks, a.mark_chunks * pl.C, b.dg_head ? b.total : nullptr);
     if (a.G > 1 && a.T > 0) {
       const int64_t rows = a.E * a.T * (a.H / a.G);
       group_sum_kernel<F><<<dim3((unsigned)((rows * a.K + 255) / 256)), 256, 0, st>>>(a, static_cast<const float*>(b.dk.p), a.dk, a.K);
