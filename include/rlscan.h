@@ -444,7 +444,8 @@ rlscan_status rlscan_linear_attention_step(rlscan_format fmt, const rlscan_heads
                                            int64_t K, int64_t V, float scale, hipStream_t stream);
 
 /* One action for each row of logits, from given uniform numbers.
- * Logits whose mask byte is 0, and those that are -inf or NaN, are not legal.  In
+ * Logits whose mask byte is 0, and those that are -inf or NaN, are not legal; +inf
+ * counts as the largest float32 in every format.  In
  * the order of falling logits (equal ones: lower index first), with weights
  * w_i = exp((x_i - max) / temperature), a row keeps its first top_k, of those
  * the shortest prefix whose weight is at least top_p of theirs, and of those the

@@ -717,8 +717,10 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
         return s.rank[0];
       }
       uint32_t prefix = 0, known = 0;
+      // the bits below the format's own are equal in all keys, but for what +inf counts as
+      const uint32_t infinite = key_of(kMaxFloat);
 #pragma unroll 1
-      for (int d = 24; d + 8 > F::kLow; d -= 8) {
+      for (int d = 24; d >= 0 && (d + 8 > F::kLow || prefix == (infinite & known)); d -= 8) {
         for (int i = tid; i < 256; i += NTHR) s.hist[i] = 0;
         __syncthreads();
         each([&](uint32_t key) __attribute__((always_inline)) {
