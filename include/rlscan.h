@@ -401,6 +401,9 @@ typedef struct rlscan_heads {
  *      as init_state, zero where the row's last step is flagged.
  * Products run in bfloat16 matrix instructions on operands split into as many
  * bfloat16 terms as fmt needs, with float32 sums; states stay in float32.
+ * What is not finite (float32: from 3.396e38 on) stays within its episode and reaches
+ * what the recurrence takes it to, as inf or NaN: a cut or a later step is not
+ * multiplied by 0 but left out.  Rows that hold such values take longer.
  * 1 <= K, V <= RLSCAN_MAX_HEAD_DIM.  With T = 0 the state is passed through. */
 int64_t rlscan_linear_attention_workspace(rlscan_format fmt, int64_t E, int64_t T, int64_t H, int64_t Hkv, int64_t K,
                                           int64_t V, int backward);
@@ -417,7 +420,8 @@ rlscan_status rlscan_linear_attention(rlscan_format fmt, rlscan_layout layout, c
  *      d_final_state [E,H,K,V] (optional), the gradient of final_state.
  * Out: dq, dk, dv like q, k, v (dk and dv summed over the heads of a group);
  *      d_log_decay like log_decay; d_init_state [E,H,K,V] (optional).
- * A decay that starts afresh has gradient 0.  Every sum has a fixed order:
+ * A decay that starts afresh has gradient 0.  In an episode with a value that is not
+ * finite any d_log_decay may be inf or NaN.  Every sum has a fixed order:
  * results do not vary from run to run. */
 rlscan_status rlscan_linear_attention_backward(
     rlscan_format fmt, rlscan_layout layout, const rlscan_heads *d_out, const rlscan_heads *q, const rlscan_heads *k,

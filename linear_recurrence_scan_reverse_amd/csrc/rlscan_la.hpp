@@ -19,6 +19,13 @@
 // instructions (16 times slower on this card).  Decays are summed in float64 in units
 // of log2 and held as two floats, so differences far from the row's start keep
 // their bits.  States stay in float32 registers and are split only to be multiplied.
+//
+// What is not finite.  A cut or a mask is a weight of 0, and 0 times inf or NaN is NaN; a
+// matrix product mixes all rows of a chunk.  So one such element of the rows that reach
+// others (k and v, backward also q and do) spoils the state, which stays so to the walk's end.
+// There the state is looked at, once; if it is not finite the block walks again with care:
+// such elements are taken out of the tiles and of the state before the products, and what
+// the recurrence makes of them is written behind the products (Odd).
 #ifndef RLSCAN_LA_HPP
 #define RLSCAN_LA_HPP
 
@@ -259,6 +266,76 @@ __device__ __forceinline__ void get4(const MixTile<N, R, D>& t, int row, int col
   }
 }
 
+// x, unknown to the compiler: what a rare branch computes from it stays in the branch.
+__device__ __forceinline__ int rarely(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// Whether one of n values is not finite: 0 times them adds up to NaN.
+template <int N>
+__device__ __forceinline__ bool any_odd(const f32x4 (&x)[N]) {
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sum = __builtin_fmaf(0.0f, x[i][r], sum);
+  return sum != sum;
+}
+
+// Takes what is not finite out of a thread's part of the state; returns which it was.
+template <int N>
+__device__ __forceinline__ uint32_t take_odd(f32x4 (&x)[N]) {
+  static_assert(N <= 8, "a bit for each");
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float v = x[i][r];
+      if (0.0f * v == 0.0f) continue;
+      bits |= 1u << (i * 4 + r);
+      x[i][r] = 0.0f;
+    }
+  return bits;
+}
+
+// The elements of a chunk that are not finite, in a careful walk: bit y of a mask is row y of
+// the tiles.
+template <int C, int AD, int CD, int NTHR>
+struct Odd {
+  uint32_t wave[NTHR / 64];  // whether a wave's state is not finite at the end
+  uint32_t bits[CD / 16 / (NTHR / 64)][NTHR];  // take_odd of each thread's states
+  uint32_t state[CD];        // for each column, whether it has one in the state entering the chunk
+  uint64_t b[AD], c[CD];     // for each column of the tiles, the rows in which it has one
+  uint64_t before[C];        // for each row, those that reach it: at or before it, no cut between
+  uint64_t leaving;          // rows that reach the state behind the chunk
+};
+
+// Whether any thread of the block says so.
+template <int NTHR>
+__device__ __forceinline__ bool any_of_block(uint32_t (&wave)[NTHR / 64], bool mine, int tid) {
+  const bool any = __ballot(mine) != 0;
+  if ((tid & 63) == 0) wave[tid >> 6] = any;
+  __syncthreads();
+  return __ballot(wave[(tid & 63) % (NTHR / 64)] != 0) != 0;
+}
+
+// Sets every element of column `col` that is not finite to 0; returns their rows.
+template <int N, int R, int D>
+__device__ __forceinline__ uint64_t take_odd(MixTile<N, R, D>& t, int col) {
+  uint64_t rows = 0;
+#pragma unroll 1
+  for (int r = 0; r < R; ++r) {
+    const int o = MixTile<N, R, D>::at(r, col / 4) + col % 4;
+    if ((__builtin_bit_cast(uint16_t, t.p[0][o]) & 0x7f80) != 0x7f80) continue;
+    rows |= 1ull << r;
+#pragma unroll
+    for (int n = 0; n < N; ++n) t.p[n][o] = (__bf16)0.0f;
+  }
+  return rows;
+}
+
 // ------------------------------------------------------------------ global rows
 __device__ __forceinline__ float f16_bits(uint16_t b) {
   union {
@@ -274,6 +351,10 @@ template <class F>
 struct Piece {
   u32x4 w[sizeof(typename F::E) * 8 / 16];
 };
+
+// w x, and 0 where w is 0 whatever x is (the instruction v_mul_legacy_f32).
+extern "C" __device__ float rlscan_la_gated(float w, float x) __asm("llvm.amdgcn.fmul.legacy");
+__device__ __forceinline__ float gated(float w, float x) { return rlscan_la_gated(w, x); }
 
 // Nothing moves across in the compiler's schedule: keeps it from requesting the operands of
 // all products at once, which costs twice the registers and half the waves.
@@ -486,6 +567,22 @@ __device__ __forceinline__ void store4(const TileRows<F>& rows, int r, int col, 
   }
 }
 
+// A NaN to column col of row r.
+template <class F, bool VEC>
+__device__ __forceinline__ void store_nan(const TileRows<F>& rows, int r, int col, int D) {
+  constexpr auto bits = sizeof(typename F::E) == 4 ? 0x7fc00000u : F::NT == 1 ? 0x7fc0u : 0x7e00u;
+  if constexpr (VEC) {
+    const auto rs = rows.resource(D);
+    const uint32_t o = rows.offset(r, col, D);
+    if constexpr (sizeof(typename F::E) == 4) __builtin_amdgcn_raw_buffer_store_b32(bits, rs, o, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)bits, rs, o, 0, 0);
+  } else if (r < rows.left && col < D) {
+    auto* p = const_cast<typename F::E*>(rows.p) + r * rows.st + col;
+    if constexpr (sizeof(typename F::E) == 4) *p = __builtin_bit_cast(float, bits);
+    else *p = (uint16_t)bits;
+  }
+}
+
 // ------------------------------------------------------------------ decays of a chunk
 // Tile row r is step t0 + r, or with REV step t0 + C-1 - r: rows follow the walk.
 template <int C>
@@ -583,6 +680,28 @@ __device__ __forceinline__ void put_decay(Decay<C>& t, const LaneDecay& d, int l
     t.out[r] = d.out;
   }
   if (lane == 0) t.across = d.across;
+}
+
+// By the whole block, between barriers: takes what is not finite out of the tiles and says
+// which rows it reaches.
+template <int N, int C, int AD, int CD, int NTHR>
+__device__ __forceinline__ void sweep_odd(Odd<C, AD, CD, NTHR>& odd, MixTile<N, C, AD>& b, MixTile<N, C, CD>& c,
+                                          const Decay<C>& d, int tid) {
+  for (int i = tid; i < AD + CD; i += NTHR) {
+    if (i < AD) odd.b[i] = take_odd(b, i);
+    else odd.c[i - AD] = take_odd(c, i - AD);
+  }
+  if (tid < C) {
+    uint64_t rows = 0;
+    const int seg = d.seg[tid];
+#pragma unroll 1
+    for (int y = 0; y <= tid; ++y) rows |= (uint64_t)(d.seg[y] == seg) << y;
+    odd.before[tid] = rows;
+  }
+  if (tid < 64) {
+    const uint64_t rows = __ballot(tid < C && d.out[tid < C ? tid : 0] != 0.0f);
+    if (tid == 0) odd.leaving = rows;
+  }
 }
 
 // scale * decay between row x and the rows y ... y+3 of a chunk (0 unless y + r <= x with

@@ -82,6 +82,7 @@ struct AttendLds {
   MixTile<F::NT, C, CD> c;
   RowTile<NP, C, C> p;
   Decay<C> dec;
+  Odd<C, AD, CD, 64 * NWV> odd;
   float diag[DOT ? C : 1];
   double more[DOT ? (NWV - 2) * C : 1];
   // the waves' dot products: two in the place of decays that are no longer read
@@ -98,9 +99,13 @@ struct AttendLds {
 // the layout of an MFMA operand whose steps are in accumulator order (frag_row_acc),
 // so S^T a needs no exchange.  Outputs are formed transposed (rows: columns of c,
 // columns: x), which leaves four consecutive elements of one row in a lane.
-template <class F, class FO, int AD, int CD, int C, int NWV, bool REV, bool DOT, int UPD, bool VEC>
-__device__ __forceinline__ void attend(AttendLds<F, AD, CD, C, NWV, DOT>& s, const Args& g, const Attend& t, int64_t eh,
-                                       int64_t seg, int c0) {
+//
+// CARE: what is not finite reaches what the recurrence lets it reach and nothing else.
+// Without, the walk leaves before its last values and returns false if it met any; all
+// that it has written is written again.
+template <class F, class FO, int AD, int CD, int C, int NWV, bool REV, bool DOT, int UPD, bool VEC, bool CARE>
+__device__ __forceinline__ bool attend_as(AttendLds<F, AD, CD, C, NWV, DOT>& s, const Args& g, const Attend& t, int64_t eh,
+                                          int64_t seg, int c0) {
   constexpr int NT = F::NT, NTHR = 64 * NWV, CT = CD / 16 / NWV, AT = AD / 16, XT = C / 16, XX = C / 32;
   constexpr int NP = AttendLds<F, AD, CD, C, NWV, DOT>::NP;
   static_assert(CT * 16 * NWV == CD, "waves share the columns evenly");
@@ -111,13 +116,14 @@ __device__ __forceinline__ void attend(AttendLds<F, AD, CD, C, NWV, DOT>& s, con
 
   f32x4 S[CT][AT];
   const bool enters = t.enter.p && !(t.enter_closed && row_closed(g, e));
+  const int l = rarely(lane), x0 = (l >> 4) * 4, y0 = c0 + (l & 15);
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
     for (int at = 0; at < AT; ++at) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int x = at * 16 + grp * 4 + r, y = c0 + (w * CT + ct) * 16 + col;
+        const int x = at * 16 + x0 + r, y = (w * CT + ct) * 16 + y0;
         S[ct][at][r] = enters && x < t.A && y < t.D ? *t.enter.at(eh, seg, x, y) : 0.0f;
       }
       hold_schedule();
@@ -230,7 +236,7 @@ __device__ __forceinline__ void attend(AttendLds<F, AD, CD, C, NWV, DOT>& s, con
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) acc = mma<NT, NT, DOT && NT == 2 ? 2 : NT - 1>(fb[kk], fa[kk], acc);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] *= acc[r];
+        for (int r = 0; r < 4; ++r) v[r] = gated(v[r], acc[r]);
         if constexpr (DOT) {  // the y = x term has no decay: kept apart, in float32
           if (jt == it && grp == col >> 2) {
             s.diag[x] = col & 2 ? (col & 1 ? v[3] : v[2]) : (col & 1 ? v[1] : v[0]);
@@ -244,6 +250,17 @@ __device__ __forceinline__ void attend(AttendLds<F, AD, CD, C, NWV, DOT>& s, con
     }
     if (w == DW && n + 1 < p1) ld = scan(now, n + 1);
     __syncthreads();
+    if constexpr (CARE) {
+      sweep_odd(s.odd, s.b, s.c, d, rarely(tid));
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        const uint32_t bits = take_odd(S[ct]);
+        s.odd.bits[ct][rarely(tid)] = bits;
+        const uint64_t who = __ballot(bits != 0);
+        if (lane < 16) s.odd.state[(w * CT + ct) * 16 + lane] = (who >> lane & 0x0001000100010001ull) != 0;
+      }
+      __syncthreads();
+    }
 
     // ---- out and S.  Matrix instructions leave room for others between them, within one
     // wave too: each region below multiplies what the regions before it requested
@@ -371,6 +388,37 @@ __device__ __forceinline__ void attend(AttendLds<F, AD, CD, C, NWV, DOT>& s, con
         hold_schedule();
       }
     }
+    if constexpr (CARE) {  // what was taken out, in the output and the state
+      const float nan = __builtin_nanf("");
+      const int l = rarely(lane), x0 = l & 15, y0 = (l >> 4) * 4;
+      const uint64_t leaving = s.odd.leaving;
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        const int vt = (w * CT + ct) * 16;
+#pragma unroll
+        for (int it = 0; it < XT; ++it) {
+          const int x = it * 16 + x0;
+          const uint64_t before = s.odd.before[x];
+          const bool enters = d.in[x] != 0.0f;
+#pragma unroll 1
+          for (int r = 0; r < 4; ++r) {
+            const int y = vt + y0 + r;
+            if ((s.odd.c[y] & before) == 0 && !(enters && s.odd.state[y] != 0)) continue;
+            store_nan<FO, VEC>(out, REV ? C - 1 - x : x, c0 + y, t.D);
+            dot[it] = nan;
+          }
+        }
+        const uint64_t c = s.odd.c[vt + x0];
+        const uint32_t bits = across != 0.0f ? s.odd.bits[ct][w * 64 + l] : 0;
+#pragma unroll
+        for (int at = 0; at < AT; ++at)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if (((s.odd.b[at * 16 + y0 + r] | c) & leaving) != 0 || (bits >> (at * 4 + r) & 1) != 0) S[ct][at][r] = nan;
+            hold_schedule();
+          }
+      }
+    }
     out.p += step * C * out.st;
     if constexpr (DOT) {
 #pragma unroll
@@ -391,8 +439,14 @@ __device__ __forceinline__ void attend(AttendLds<F, AD, CD, C, NWV, DOT>& s, con
       }
     }
   }
+  if constexpr (!CARE) {
+    bool odd = false;
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) odd |= any_odd(S[ct]);
+    if (any_of_block<NTHR>(s.odd.wave, odd, tid)) return false;
+  }
 
-  if (seg != g.nseg - 1) return;
+  if (seg != g.nseg - 1) return true;
   if (t.leave.p) {
     const bool closed = t.leave_closed && row_closed(g, e);
 #pragma unroll
@@ -433,6 +487,14 @@ __device__ __forceinline__ void attend(AttendLds<F, AD, CD, C, NWV, DOT>& s, con
       }
     }
   }
+  return true;
+}
+
+template <class F, class FO, int AD, int CD, int C, int NWV, bool REV, bool DOT, int UPD, bool VEC>
+__device__ __forceinline__ void attend(AttendLds<F, AD, CD, C, NWV, DOT>& s, const Args& g, const Attend& t, int64_t eh,
+                                       int64_t seg, int c0) {
+  if (!attend_as<F, FO, AD, CD, C, NWV, REV, DOT, UPD, VEC, false>(s, g, t, eh, seg, c0))
+    attend_as<F, FO, AD, CD, C, NWV, REV, DOT, UPD, VEC, true>(s, g, t, eh, seg, c0);
 }
 
 }  // namespace la

@@ -17,12 +17,24 @@ namespace la {
 // order).  Wave w holds the 16 columns w*16 ... of the slice for all KP rows: accumulator
 // tile kt, lane l holds S[kt*16 + l%16][w*16 + (l/16)*4 + r].  What segment s adds goes
 // to slot s + 1 of seg_state [E, H, nseg, KP, VP], its decay to seg_decay [E, H, nseg].
-template <class F, int KP, int C, bool REV, bool VEC>
-__global__ void __launch_bounds__(kThreads) walk_kernel(const Args a, int64_t VP, float* seg_state, float* seg_decay) {
+// CARE as in rlscan_la_attend.hpp: without, it returns false before the segment's values if
+// they are not finite.
+template <class F, int KP, int C>
+struct WalkLds {
+  MixTile<F::NT, C, KP> xs;
+  MixTile<F::NT, C, 64> ys;
+  Decay<C> dec;
+  Odd<C, KP, 64, kThreads> odd;
+};
+
+template <class F, int KP, int C, bool REV, bool VEC, bool CARE>
+__device__ __forceinline__ bool walk_as(WalkLds<F, KP, C>& lds, const Args& a, int64_t VP, float* seg_state,
+                                        float* seg_decay) {
   constexpr int NT = F::NT, NW = F::NW, KT = KP / 16;
-  __shared__ MixTile<NT, C, KP> xs;
-  __shared__ MixTile<NT, C, 64> ys;
-  __shared__ Decay<C> dec;
+  auto& xs = lds.xs;
+  auto& ys = lds.ys;
+  auto& dec = lds.dec;
+  auto& odd = lds.odd;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, col = lane & 15, grp = lane >> 4;
   const int64_t EH = a.E * a.H, nvs = VP / 64;
   const int64_t eh = blockIdx.x % EH, rest = blockIdx.x / EH;
@@ -55,6 +67,12 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const Args a, int64_t VP
     stage<F, kThreads>(ys, ry[b], tid);
     if (w == 0) put_decay<C, REV>(dec, scan_decay<C, REV>(sd[b], a.scale, lane), lane);
     __syncthreads();
+    uint32_t bits = 0;
+    if constexpr (CARE) {
+      sweep_odd(odd, xs, ys, dec, tid);
+      bits = take_odd(S);
+      __syncthreads();
+    }
     if (n + 2 < p1) request(n + 2, b);
     const float across = dec.across;
     decay *= across;
@@ -71,18 +89,38 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const Args a, int64_t VP
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) S[kt] = mma(fy, frag_col(xs, kt, jj, lane), S[kt]);
     }
+    if constexpr (CARE) {  // what was taken out
+      if (across == 0.0f) bits = 0;
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (((odd.b[kt * 16 + col] | odd.c[w * 16 + grp * 4 + r]) & odd.leaving) != 0 ||
+              (bits >> (kt * 4 + r) & 1) != 0)
+            S[kt][r] = __builtin_nanf("");
+    }
     __syncthreads();
   };
   for (int64_t n = p0; n < p1; n += 2) {
     chunk(n, 0);
     if (n + 1 < p1) chunk(n + 1, 1);
   }
+  if (!CARE && any_of_block<kThreads>(odd.wave, any_odd(S), tid)) return false;
 
   float* to = seg_state + (eh * a.nseg + seg + 1) * KP * VP;
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt)
     *reinterpret_cast<f32x4*>(to + (kt * 16 + col) * VP + v0 + w * 16 + grp * 4) = S[kt];
   if (tid == 0 && vs == 0) seg_decay[eh * a.nseg + seg + 1] = decay;
+  return true;
+}
+
+// At least as many waves as the walk without care leaves room for.
+template <class F, int KP, int C, bool REV, bool VEC>
+__global__ void __launch_bounds__(kThreads, KP == 128 ? 2 : F::NT < 3 && VEC ? 4 : 3) walk_kernel(const Args a, int64_t VP, float* seg_state, float* seg_decay) {
+  __shared__ WalkLds<F, KP, C> lds;
+  if (!walk_as<F, KP, C, REV, VEC, false>(lds, a, VP, seg_state, seg_decay))
+    walk_as<F, KP, C, REV, VEC, true>(lds, a, VP, seg_state, seg_decay);
 }
 
 // In place: slot 0 gets the row's entering value, slot s + 1 becomes decay * slot s + slot s + 1.
@@ -111,7 +149,7 @@ static __global__ void __launch_bounds__(256) combine_kernel(const Args a, const
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       if (n0 + k < p.nseg) {
-        x = decay[n0 + k] * x + add[k];
+        x = gated(decay[n0 + k], x) + add[k];
         s[(n0 + k) * state] = x;
       }
   }
