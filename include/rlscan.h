@@ -487,8 +487,9 @@ rlscan_status rlscan_sample_actions_shared(rlscan_format fmt, const void *logits
 
 /* Log-probability of the taken action and entropy of softmax(logits /
  * temperature) over the legal actions of each row.
- * In:  logits, mask as above; actions [R] int64: one outside [0,N) (a padded
- *      step) has log-probability 0 and no gradient, an illegal one -inf;
+ * In:  logits, mask as above (mask byte 0 and -inf: not legal); actions [R] int64: one
+ *      outside [0,N) (a padded step) has log-probability 0 and no gradient, an
+ *      illegal one -inf, and gradients through the legal ones alone;
  *      temperature > 0.
  * Out: log_probs [R], entropies [R]; lse [R] float64: log of the sum of exp(x /
  *      temperature), for the backward call.  A row without a legal action has 0, 0

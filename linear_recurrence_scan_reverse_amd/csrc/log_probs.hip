@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(256) log_probs_backward_kernel(const LogProbAr
     l = l < -150.0f ? -150.0f : l;  // e^-150 is 0 in float32; keeps 0 * inf out
     const float pr = exp2_fast(l * kLog2E);
     const float d = (taken ? dlp : 0.0f) - pr * (base + dent * (l + ent));
-    return legal ? d * inv_t : 0.0f;
+    return legal && x != kNegInf ? d * inv_t : 0.0f;  // -inf is not legal either, if it was taken
   };
   const int64_t g1 = (blockIdx.x % pieces + 1) * per;
   for (int64_t g = blockIdx.x % pieces * per + threadIdx.x; g < g1; g += 256) {
