@@ -465,7 +465,7 @@ _POLICY = ("linear_attention", "linear_attention_backward", "linear_attention_st
 
 
 def __getattr__(name):
-    if name in _POLICY:  # loaded on first use: the module imports torch
+    if name in _POLICY:  # loaded on first use
         from . import policy
         for n in _POLICY:
             globals()[n] = getattr(policy, n)

@@ -13,11 +13,20 @@ from __future__ import annotations
 import contextlib
 import ctypes
 
-import torch
-
 import linear_recurrence_scan_reverse_amd as _rl
 
-_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+# Imported by the first call, like in the rest of the package, so that it loads without torch.
+torch = None
+_DTYPES = {}
+_raw_stream_of = None
+
+
+def _import_torch():
+    global torch, _raw_stream_of
+    import torch as module
+    _DTYPES.update({module.float32: 0, module.bfloat16: 1, module.float16: 2})
+    _raw_stream_of = module._C._cuda_getCurrentRawStream
+    torch = module
 
 
 class _Heads(ctypes.Structure):
@@ -28,7 +37,6 @@ class _Heads(ctypes.Structure):
 
 _HEADS_BYTES = ctypes.sizeof(_Heads)
 _ARRAYS = {n: ctypes.c_int64 * (4 * n) for n in (4, 7)}  # n rlscan_heads in a row
-_raw_stream_of = torch._C._cuda_getCurrentRawStream
 
 
 def _refuse(x, name, shape, dtype, device):
@@ -70,6 +78,8 @@ def _plain(x, name, shape, dtype, device):
 
 
 def _values(x, name, dims):
+    if torch is None:
+        _import_torch()
     if not isinstance(x, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if x.dim() != dims:
@@ -279,6 +289,8 @@ def linear_attention_step(q, k, v, log_decay, state, reset=None, slots=None, *, 
 
 
 def _logit_rows(logits, name="logits"):
+    if torch is None:
+        _import_torch()
     if not isinstance(logits, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if logits.dim() < 1 or logits.shape[-1] < 1:
