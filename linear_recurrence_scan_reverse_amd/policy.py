@@ -327,6 +327,11 @@ def _setting(x, name, shape, dtype, device, off):
     return None, off if x is None else x
 
 
+def _int32(x):
+    """The nearest int32 to a whole number, so that one past the range stays refused, or off."""
+    return max(-2 ** 31, min(int(x), 2 ** 31 - 1))
+
+
 def sample_actions(logits, uniforms, *, temperature=1.0, top_k=None, top_p=None, min_p=None, mask=None, actions=None,
                    log_probs=None, stream=None):
     """One action for each row of logits [..., N], from uniform numbers in [0, 1).
@@ -361,7 +366,7 @@ def sample_actions(logits, uniforms, *, temperature=1.0, top_k=None, top_p=None,
             _plain(log_probs, "log_probs", lead, torch.float32, dev)
         ws, need = _workspace("rlscan_sample_actions_workspace", dev, R, N)
         _call("rlscan_sample_actions_shared", _DTYPES[logits.dtype], logits.data_ptr(), stride, _ptr(mask),
-              uniforms.data_ptr(), _ptr(temps), _ptr(ks), _ptr(ps), _ptr(ms), float(t1), min(int(k1), 2 ** 31 - 1),
+              uniforms.data_ptr(), _ptr(temps), _ptr(ks), _ptr(ps), _ptr(ms), float(t1), _int32(k1),
               float(p1), float(m1), actions.data_ptr(), log_probs.data_ptr(), _ptr(ws), need, R, N,
               _raw_stream(stream, dev))
     return actions, log_probs
