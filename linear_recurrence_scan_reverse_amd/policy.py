@@ -152,6 +152,11 @@ def _workspace(fname, device, *sizes):
     return (torch.empty(need, dtype=torch.uint8, device=device) if need else None), need
 
 
+def _scale(scale, K):
+    """The given one or K^-0.5 (heads of no size are refused by the entry)."""
+    return max(K, 1) ** -0.5 if scale is None else float(scale)
+
+
 def _attention_inputs(q, k, v, log_decay, done, init_state, time_major):
     """Checks the inputs shared by the forward and the backward call."""
     _values(q, "q", 4)
@@ -189,7 +194,7 @@ def linear_attention(q, k, v, log_decay, done=None, init_state=None, *, scale=No
     ``final_state``; final_state is what the next window takes as init_state."""
     dev, dt, E, T, H, Hkv, K, V, per_step, done = _attention_inputs(q, k, v, log_decay, done, init_state, time_major)
     shape = (q.shape[0], q.shape[1], H, V)
-    scale = K ** -0.5 if scale is None else float(scale)
+    scale = _scale(scale, K)
     fmt = _DTYPES[dt]
     with _on(stream, dev):
         out = torch.empty(shape, dtype=dt, device=dev) if out is None else _strided(out, "out", shape, dt, dev)
@@ -218,7 +223,7 @@ def linear_attention_backward(d_out, q, k, v, log_decay, done=None, init_state=N
     dev, dt, E, T, H, Hkv, K, V, per_step, done = _attention_inputs(q, k, v, log_decay, done, init_state, time_major)
     _strided(d_out, "d_out", (q.shape[0], q.shape[1], H, V), dt, dev)
     _plain(d_final_state, "d_final_state", (E, H, K, V), torch.float32, dev)
-    scale = K ** -0.5 if scale is None else float(scale)
+    scale = _scale(scale, K)
     fmt = _DTYPES[dt]
     with _on(stream, dev):
         def grad(x, name, like):
@@ -273,7 +278,7 @@ def linear_attention_step(q, k, v, log_decay, state, reset=None, slots=None, *, 
     _plain(slots, "slots", (E,), torch.int32, dev)
     if slots is None and S < E:
         raise ValueError("state has %d slots for %d rows" % (S, E))
-    scale = K ** -0.5 if scale is None else float(scale)
+    scale = _scale(scale, K)
     with _on(stream, dev):
         out = torch.empty((E, H, V), dtype=dt, device=dev) if out is None else _strided(out, "out", (E, H, V), dt, dev)
         v_ = []

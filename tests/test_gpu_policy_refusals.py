@@ -19,3 +19,15 @@ def test_negative_top_k(k):
 def test_top_k_past_the_row_is_off(k):
     x, u = torch.randn(3, 40, device="cuda"), torch.rand(3, device="cuda")
     assert torch.equal(rl.sample_actions(x, u, top_k=k)[0], rl.sample_actions(x, u)[0])
+
+
+@pytest.mark.gpu
+def test_heads_of_no_size():
+    q, v = torch.zeros(2, 5, 4, 0, device="cuda"), torch.zeros(2, 5, 4, 8, device="cuda")
+    g = torch.zeros(4, device="cuda")
+    with pytest.raises(rl.RlscanError):
+        rl.linear_attention(q, q, v, g)
+    with pytest.raises(rl.RlscanError):
+        rl.linear_attention_backward(v, q, q, v, g)
+    with pytest.raises(rl.RlscanError):
+        rl.linear_attention_step(q[:, 0], q[:, 0], v[:, 0], g, torch.zeros(2, 4, 0, 8, device="cuda"))
