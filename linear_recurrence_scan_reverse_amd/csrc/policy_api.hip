@@ -155,7 +155,7 @@ rlscan_status check_sizes(rlscan_format f, int64_t E, int64_t T, int64_t H, int6
 bool grid_ok(const Plan& p, int64_t E, int64_t T, int64_t H, int64_t Hkv, int64_t K, int64_t V, bool backward) {
   const int64_t most = rlscan::la::kMaxBlocks;
   const int64_t heads = E * H;
-  if (heads > most / 64) return false;  // combine: up to 64 blocks a head
+  if (heads > most / 64 || H > most) return false;  // combine: up to 64 blocks a head; the sum over rows: one
   const int64_t per = (p.VP / 64 > 3 || !backward ? p.VP / 64 : 3) * p.nseg;
   if (heads > (most - 24) / per) return false;
   if (backward && p.nmarks > 0 && heads > most / p.nmarks) return false;
