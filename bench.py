@@ -38,6 +38,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import sys
 import threading
 import time
@@ -61,14 +62,26 @@ def log(*a):
     print(*a, file=sys.stderr, flush=True)
 
 
+def kernel_sources():
+    """The sources of the kernels that the bench times, each estimator's with the headers it
+    includes: what decides what they do and how they are launched."""
+    todo = [n for n in os.listdir(CSRC) if n.startswith("est_") and n.endswith(".hip")]
+    found = set()
+    while todo:
+        name = todo.pop()
+        if name in found or not os.path.exists(os.path.join(CSRC, name)):
+            continue  # a header of the library's interface or of the toolchain
+        found.add(name)
+        with open(os.path.join(CSRC, name)) as f:
+            todo += re.findall(r'^\s*#include "([^"]+)"', f.read(), re.M)
+    return sorted(found)
+
+
 def kernel_source_hash() -> str:
-    """Hash of the sources that decide what the kernels do and how they are launched
-    (the argument-checking C-ABI file is left out)."""
     h = hashlib.sha256()
-    for name in sorted(os.listdir(CSRC)):
-        if name.endswith((".hip", ".hpp", ".h")) and name != "rlscan_api.hip":
-            with open(os.path.join(CSRC, name), "rb") as f:
-                h.update(name.encode() + b"\0" + f.read())
+    for name in kernel_sources():
+        with open(os.path.join(CSRC, name), "rb") as f:
+            h.update(name.encode() + b"\0" + f.read())
     return h.hexdigest()[:16]
 
 
