@@ -12,14 +12,17 @@
 // So that their rounding does not add up over a row, some boundaries between chunks are
 // marked: there the walks leave S and dS, and the sum starts anew from dg = <S, dS>.
 //
-// Measured: 8 rows of 4096 steps, 16 heads of 128 in bfloat16, gates for each step: 1006 us
-// for the three walks, 24 for the marked boundaries and 19 for the sums of dg; 944 MB and
-// 103 Gflop, 180 us of a copy.  128 heads times three walks leave one and a half blocks for
-// a compute unit, each bound by its own chain of products: dq and dk carry two terms for
-// intermediates and three for the float32 sums that dg needs, 3 to 6 matrix
-// instructions where an output in bfloat16 alone would need one.  64 rows of 333 steps, 4
-// heads of 64 in float32, keys and values shared by two: 135 us for the walks, 26 to add up the
-// shared heads' gradients, 18 for dg.
+// Measured (kernels in a run of 300 calls): 8 rows of 4096 steps, 16 heads of 128 in bfloat16,
+// gates for each step: 989 us for the three walks, 24 for the marked boundaries and 18 for the
+// sums of dg; 944 MB and 103 Gflop, 180 us of a copy.  A block takes 87,872 bytes of LDS, so a
+// compute unit holds one: 128 heads times three walks are 384 blocks on 256 places, two rounds
+// of which the second is half empty.  Within a block the chain of products is what takes time:
+// dq and dk carry two terms for intermediates and three for the float32 sums that dg needs,
+// 3 to 6 matrix instructions where an output in bfloat16 alone would need one.  The 128-wide
+// walks without care need 203 (float16) to 253 registers and spill none, those with care 7 to 144;
+// where rows cannot be read 16 bytes at a time 0 to 45 and 5 to 262.  64 rows of 333 steps, 4 heads
+// of 64 in float32, keys and values shared by two: 125 us for the walks (230 registers, two blocks
+// on a compute unit: 768 blocks on 512 places), 24 to add up the shared heads' gradients, 19 for dg.
 #include "rlscan_la_attend.hpp"
 #include "rlscan_la_launch.hpp"
 #include "rlscan_la_walk.hpp"
@@ -54,7 +57,9 @@ __global__ void __launch_bounds__(64 * NWV, MINW) backward_kernel(const Args a, 
 // dg of one row and head: x_t = u_t - w_t summed from the end, afresh at each episode's last step.
 // A thread takes four steps; the sums of those behind it pass through the wave and the block.
 // Rows past 1024 steps take blocks of 1024 threads: a tile's chain of sums and trips to
-// memory is paid once for 4096 steps (8 rows of 4096, 16 heads: 27 us with 256 threads, 19).
+// memory is paid once for 4096 steps.  256 threads against 1024, us, rows of 1100, 2048, 4096 and 8192
+// steps: one head 7.7, 7.9, 14.2, 26.9 and 6.1, 6.6, 7.2, 13.1; 128 heads 10.6, 13.0, 22.7, 44.9
+// and 9.0, 11.2, 16.9, 32.2.  1024 heads fill the card by themselves: 29, 43, 96 (4096) and 34, 49, 90.
 template <int NTHR>
 __global__ void __launch_bounds__(NTHR) decay_grad_kernel(const Args a, const double* u, const double* w,
                                                           const float* end, const double* mark_dots, int64_t nmarks,

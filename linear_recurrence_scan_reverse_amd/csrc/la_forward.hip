@@ -5,11 +5,16 @@
 // each segment adds to the state, a second joins these along the row, and the segments are
 // walked side by side from the states so found; k and v are read twice.
 //
-// Measured (bfloat16): 256 rows of 256 steps, 8 heads of 64, gates for each step: 87 us,
-// 3.9 TB/s of its 338 MB; reading and writing them by a copy takes 64.  One row of 32768
-// steps, 16 heads of 128 in groups of 4: 84 us for the segments' states, 8 to join them,
-// 165 for the walk.  What bounds the walk is the chain within a chunk (products, decays and
-// masks on a C x C tile, products again) with two blocks on a compute unit, not memory.
+// Measured (bfloat16, kernels in a run of 300 calls; in the first dozen of a process they take
+// a tenth to a third longer): 256 rows of 256 steps, 8 heads of 64, gates for each step: 87
+// us, 3.9 TB/s of its 338 MB; reading and writing them by a copy takes 64.  One row of 32768
+// steps, 16 heads of 128 in groups of 4: 76 us for the segments' states, 8 to join them, 141
+// for the walk.  What bounds the walk is the chain within a chunk (products, decays and masks
+// on a C x C tile, products again), not memory.  At 128 a compute unit holds one block: eight
+// waves of 239 (float16) or 256 registers.  The walk without care needs 199 to 247 and spills
+// none; the one with care spills 20 or 21 in the other two formats, and 34 to 38 where rows cannot
+// be read 16 bytes at a time (the walk without care 1 to 3 there).  At 64 three blocks of bfloat16 fit: 2048 blocks are 2.67
+// rounds of the card.
 #include "rlscan_la_attend.hpp"
 #include "rlscan_la_launch.hpp"
 #include "rlscan_la_walk.hpp"

@@ -26,10 +26,10 @@
 // the action.  One block takes a row; where rows are few and long, blocks share the passes
 // (slice_kernel) and one block for each row makes the choice.
 //
-// 256 rows of 64007 bfloat16 logits with top_k up to 100: 79 us, of which reading them
+// 256 rows of 64007 bfloat16 logits with top_k up to 100: 78 us, of which reading them
 // takes 6 and the few rows without a top_k nearly all: two passes with some 40 instructions
 // a logit for the float64 exponential, by one compute unit.  One row of 131072 float32
-// logits with top_p alone: 3.2, 7.3 and 10.7 us for the three shared passes and 10.6 for the
+// logits with top_p alone: 3.4, 6.7 and 11.7 us for the three shared passes and 10.2 for the
 // choice; a chain of four kernels that each wait for memory a few times (122 us on one
 // compute unit).
 #include "rlscan_logits.hpp"
@@ -1003,6 +1003,8 @@ __global__ void __launch_bounds__(NTHR) sample_kernel(const SampleArgs a) {
 // 131072 float32, top_p 0.9: 122, 36.  Bfloat16, top_p 0.9, then top_k 50: 64 rows of
 // 64007: 74, 45 and 35, 35; 128 rows: 76, 99 and 36, 75; 64 rows of 32768: 43, 38 and
 // 24, 33 (which settings a row has is known on the device only); of 8192: 26, 40 and 19, 33.
+// Every pass holds the whole of SampleLds, 131,832 bytes, so one block to a compute unit,
+// and rows with a top_k are shared too.
 int64_t sample_slices(int64_t R, int64_t N) {
   return R < 1 || R > 64 || N < 32768 ? 1 : 256 / R < N / 4096 ? 256 / R : N / 4096;
 }

@@ -185,7 +185,8 @@ def linear_attention(q, k, v, log_decay, done=None, init_state=None, *, scale=No
     """Linear attention with a decay for each head, over whole rows.
 
     Per row and head S_t = exp(g_t) S_{t-1} + k_t v_t^T and o_t = scale * S_t^T q_t; the
-    step after one flagged in ``done`` starts from a zero state.
+    step after one flagged in ``done`` starts from a zero state, whatever the one before
+    it held: inf and NaN stay within their episode.
 
     q [E, T, H, K], k [E, T, Hkv, K], v [E, T, Hkv, V] (``time_major``: [T, E, ...]),
     H a multiple of Hkv, K and V up to 128; log_decay: g, float32, [H] or [E, T, H];
@@ -347,8 +348,9 @@ def sample_actions(logits, uniforms, *, temperature=1.0, top_k=None, top_p=None,
     the order of the indices.  temperature, top_k, top_p and min_p are numbers or tensors
     [...] (top_k int32, the others float32); None, top_k 0, top_p 1 and min_p 0 are
     off; temperature 0 takes the largest logit.  mask [..., N]: zero where an action is
-    not legal.  Returns (actions int64 [...], log_probs float32 [...]): -1 and 0
-    for a row without a legal action."""
+    not legal, nor are logits of -inf and NaN; +inf counts as the largest float32.
+    Returns (actions int64 [...], log_probs float32 [...]): -1 and 0 for a row without
+    a legal action."""
     lead, R, N = _logit_rows(logits)
     dev = _on_gpu(logits, "logits")
     stride = _row_stride(logits, "logits")
@@ -382,7 +384,8 @@ def action_log_probs(logits, actions, *, temperature=1.0, mask=None, log_probs=N
     """Log-probability of the taken action and entropy of softmax(logits / temperature).
 
     logits [..., N], actions [...] int64 (one outside [0, N), as for a padded step, has
-    log-probability 0 and no gradient), mask [..., N]: zero where an action is not legal.
+    log-probability 0 and no gradient), mask [..., N]: zero where an action is not legal,
+    as one with a logit of -inf (illegal taken ones: log-probability -inf).
     Returns (log_probs, entropies, lse) [...]: float32, and lse in float64 for the backward call."""
     lead, R, N = _logit_rows(logits)
     dev = _on_gpu(logits, "logits")
