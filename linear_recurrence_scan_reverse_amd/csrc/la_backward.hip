@@ -13,15 +13,15 @@
 // marked: there the walks leave S and dS, and the sum starts anew from dg = <S, dS>.
 //
 // Measured (kernels in a run of 300 calls): 8 rows of 4096 steps, 16 heads of 128 in bfloat16,
-// gates for each step: 989 us for the three walks, 24 for the marked boundaries and 18 for the
+// gates for each step: 981 us for the three walks, 24 for the marked boundaries and 18 for the
 // sums of dg; 944 MB and 103 Gflop, 180 us of a copy.  A block takes 87,872 bytes of LDS, so a
 // compute unit holds one: 128 heads times three walks are 384 blocks on 256 places, two rounds
 // of which the second is half empty.  Within a block the chain of products is what takes time:
 // dq and dk carry two terms for intermediates and three for the float32 sums that dg needs,
 // 3 to 6 matrix instructions where an output in bfloat16 alone would need one.  The 128-wide
-// walks without care need 203 (float16) to 253 registers and spill none, those with care 7 to 144;
-// where rows cannot be read 16 bytes at a time 0 to 45 and 5 to 262.  64 rows of 333 steps, 4 heads
-// of 64 in float32, keys and values shared by two: 125 us for the walks (230 registers, two blocks
+// walks without care need 203 (float16) to 253 registers and spill none, those with care 81 to 254;
+// where rows cannot be read 16 bytes at a time 0 to 45 and 91 to 388.  64 rows of 333 steps, 4 heads
+// of 64 in float32, keys and values shared by two: 120 us for the walks (245 registers, two blocks
 // on a compute unit: 768 blocks on 512 places), 24 to add up the shared heads' gradients, 19 for dg.
 #include "rlscan_la_attend.hpp"
 #include "rlscan_la_launch.hpp"
@@ -38,19 +38,25 @@ struct BackwardLds {
   };
 };
 
+struct BackwardArgs {
+  Args a;
+  Attend q, k, v;
+};
+
 // FO: the format that dk and dv are left in (float32 scratch where heads share them).
 template <class F, class FO, int KP, int VP, int C, int NWV, int MINW, bool VEC>
-__global__ void __launch_bounds__(64 * NWV, MINW) backward_kernel(const Args a, const Attend q, const Attend k, const Attend v) {
+__global__ void __launch_bounds__(64 * NWV, MINW) backward_kernel(const BackwardArgs p) {
   __shared__ char lds[sizeof(BackwardLds<F, KP, VP, C, NWV>)] __attribute__((aligned(16)));
   auto& s = *reinterpret_cast<BackwardLds<F, KP, VP, C, NWV>*>(lds);
+  const Args& a = p.a;
   const int64_t items = a.E * a.H * a.nseg;
   const int64_t item = blockIdx.x / 24 * 8 + blockIdx.x % 8;
   if (item >= items) return;
   const int64_t eh = item % (a.E * a.H), seg = item / (a.E * a.H);
   switch (blockIdx.x % 24 / 8) {
-    case 0: attend<F, F, VP, KP, C, NWV, false, true, F::NW, VEC>(s.k, a, q, eh, seg, 0); break;
-    case 1: attend<F, FO, VP, KP, C, NWV, true, true, F::NW, VEC>(s.k, a, k, eh, seg, 0); break;
-    default: attend<F, FO, KP, VP, C, NWV, true, false, F::NP, VEC>(s.v, a, v, eh, seg, 0); break;
+    case 0: attend<F, F, VP, KP, C, NWV, false, true, F::NW, VEC>(s.k, p, &BackwardArgs::q, eh, seg, 0); break;
+    case 1: attend<F, FO, VP, KP, C, NWV, true, true, F::NW, VEC>(s.k, p, &BackwardArgs::k, eh, seg, 0); break;
+    default: attend<F, FO, KP, VP, C, NWV, true, false, F::NP, VEC>(s.v, p, &BackwardArgs::v, eh, seg, 0); break;
   }
 }
 
@@ -243,7 +249,7 @@ void launch_walks(const Args& a, const Backward& b, const Plan& pl, hipStream_t 
   v.enter = pl.nseg > 1 ? StateView{b.seg_grad, pl.nseg * pad, pad, VP, 1} : rows_k(b.d_final);
   v.enter_closed = pl.nseg == 1;
   const int64_t items = a.E * a.H * pl.nseg;
-  backward_kernel<F, FO, KP, VP, C, NWV, MINW, VEC><<<dim3((unsigned)((items + 7) / 8 * 24)), 64 * NWV, 0, st>>>(a, q, k, v);
+  backward_kernel<F, FO, KP, VP, C, NWV, MINW, VEC><<<dim3((unsigned)((items + 7) / 8 * 24)), 64 * NWV, 0, st>>>(BackwardArgs{a, q, k, v});
 }
 
 template <class F, class FO, bool VEC>

@@ -8,12 +8,12 @@
 // Measured (bfloat16, kernels in a run of 300 calls; in the first dozen of a process they take
 // a tenth to a third longer): 256 rows of 256 steps, 8 heads of 64, gates for each step: 87
 // us, 3.9 TB/s of its 338 MB; reading and writing them by a copy takes 64.  One row of 32768
-// steps, 16 heads of 128 in groups of 4: 76 us for the segments' states, 8 to join them, 141
+// steps, 16 heads of 128 in groups of 4: 73 us for the segments' states, 8 to join them, 145
 // for the walk.  What bounds the walk is the chain within a chunk (products, decays and masks
 // on a C x C tile, products again), not memory.  At 128 a compute unit holds one block: eight
-// waves of 239 (float16) or 256 registers.  The walk without care needs 199 to 247 and spills
-// none; the one with care spills 20 or 21 in the other two formats, and 34 to 38 where rows cannot
-// be read 16 bytes at a time (the walk without care 1 to 3 there).  At 64 three blocks of bfloat16 fit: 2048 blocks are 2.67
+// waves of 255 or 256 registers.  The walk without care needs 199 to 247 and spills none; the
+// one with care spills up to 51, and up to 87 where rows cannot be read 16 bytes at a time (the
+// walk without care up to 3 there).  At 64 three blocks of bfloat16 fit: 2048 blocks are 2.67
 // rounds of the card.
 #include "rlscan_la_attend.hpp"
 #include "rlscan_la_launch.hpp"
@@ -22,13 +22,20 @@
 namespace rlscan {
 namespace la {
 
+struct ForwardArgs {
+  Args a;
+  Attend t;
+  int64_t nvs;
+};
+
 // A block: one head, CD columns of V, one segment.
 template <class F, int AD, int CD, int C, int NWV, int MINW, bool VEC>
-__global__ void __launch_bounds__(64 * NWV, MINW) forward_kernel(const Args a, const Attend t, int64_t nvs) {
+__global__ void __launch_bounds__(64 * NWV, MINW) forward_kernel(const ForwardArgs p) {
   __shared__ AttendLds<F, AD, CD, C, NWV, false> s;
-  const int64_t EH = a.E * a.H;
+  const int64_t EH = p.a.E * p.a.H;
   const int64_t eh = blockIdx.x % EH, rest = blockIdx.x / EH;
-  attend<F, F, AD, CD, C, NWV, false, false, F::NW, VEC>(s, a, t, eh, rest / nvs, (int)(rest % nvs) * CD);
+  attend<F, F, AD, CD, C, NWV, false, false, F::NW, VEC>(s, p, &ForwardArgs::t, eh, rest / p.nvs,
+                                                         (int)(rest % p.nvs) * CD);
 }
 
 template <class F, int KP, int CD, int C, int NWV, int MINW, bool VEC>
@@ -48,7 +55,7 @@ hipError_t launch_forward_as(const Args& a, const Plan& pl, hipStream_t st) {
   t.leave = StateView{a.final_state, (int64_t)a.K * a.V, 0, a.V, 1};
   t.leave_closed = 1;
   const int64_t nvs = pl.VP / CD;
-  forward_kernel<F, KP, CD, C, NWV, MINW, VEC><<<dim3((unsigned)(a.E * a.H * nvs * pl.nseg)), 64 * NWV, 0, st>>>(a, t, nvs);
+  forward_kernel<F, KP, CD, C, NWV, MINW, VEC><<<dim3((unsigned)(a.E * a.H * nvs * pl.nseg)), 64 * NWV, 0, st>>>(ForwardArgs{a, t, nvs});
   return hipGetLastError();
 }
 

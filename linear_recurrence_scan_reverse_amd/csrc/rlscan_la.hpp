@@ -272,6 +272,17 @@ __device__ __forceinline__ int rarely(int x) {
   return x;
 }
 
+// The kernel's argument, a struct of type T, read from memory once more: a rare branch that
+// takes it keeps no register of the ones before busy.
+template <class T>
+__device__ __forceinline__ T argument_again() {
+  auto* p = __builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  T t;
+  __builtin_memcpy(&t, (const void*)p, sizeof t);
+  return t;
+}
+
 // Whether one of n values is not finite: 0 times them adds up to NaN.
 template <int N>
 __device__ __forceinline__ bool any_odd(const f32x4 (&x)[N]) {

@@ -490,11 +490,14 @@ __device__ __forceinline__ bool attend_as(AttendLds<F, AD, CD, C, NWV, DOT>& s, 
   return true;
 }
 
-template <class F, class FO, int AD, int CD, int C, int NWV, bool REV, bool DOT, int UPD, bool VEC>
-__device__ __forceinline__ void attend(AttendLds<F, AD, CD, C, NWV, DOT>& s, const Args& g, const Attend& t, int64_t eh,
+// P: the kernel's argument, a struct with Args a and the Attend at T.
+template <class F, class FO, int AD, int CD, int C, int NWV, bool REV, bool DOT, int UPD, bool VEC, class P>
+__device__ __forceinline__ void attend(AttendLds<F, AD, CD, C, NWV, DOT>& s, const P& p, Attend P::*t, int64_t eh,
                                        int64_t seg, int c0) {
-  if (!attend_as<F, FO, AD, CD, C, NWV, REV, DOT, UPD, VEC, false>(s, g, t, eh, seg, c0))
-    attend_as<F, FO, AD, CD, C, NWV, REV, DOT, UPD, VEC, true>(s, g, t, eh, seg, c0);
+  if (attend_as<F, FO, AD, CD, C, NWV, REV, DOT, UPD, VEC, false>(s, p.a, p.*t, eh, seg, c0)) return;
+  const P again = argument_again<P>();
+  asm volatile("" : "+s"(eh), "+s"(seg), "+s"(c0));
+  attend_as<F, FO, AD, CD, C, NWV, REV, DOT, UPD, VEC, true>(s, again.a, again.*t, eh, seg, c0);
 }
 
 }  // namespace la

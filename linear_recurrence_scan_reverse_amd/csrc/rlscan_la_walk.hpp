@@ -27,17 +27,24 @@ struct WalkLds {
   Odd<C, KP, 64, kThreads> odd;
 };
 
+struct WalkArgs {
+  Args a;
+  int64_t VP;
+  float *seg_state, *seg_decay;
+};
+
 template <class F, int KP, int C, bool REV, bool VEC, bool CARE>
-__device__ __forceinline__ bool walk_as(WalkLds<F, KP, C>& lds, const Args& a, int64_t VP, float* seg_state,
-                                        float* seg_decay) {
+__device__ __forceinline__ bool walk_as(WalkLds<F, KP, C>& lds, const WalkArgs& p, int64_t block) {
   constexpr int NT = F::NT, NW = F::NW, KT = KP / 16;
+  const Args& a = p.a;
+  const int64_t VP = p.VP;
   auto& xs = lds.xs;
   auto& ys = lds.ys;
   auto& dec = lds.dec;
   auto& odd = lds.odd;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, col = lane & 15, grp = lane >> 4;
   const int64_t EH = a.E * a.H, nvs = VP / 64;
-  const int64_t eh = blockIdx.x % EH, rest = blockIdx.x / EH;
+  const int64_t eh = block % EH, rest = block / EH;
   const int64_t vs = rest % nvs, seg = rest / nvs;
   const int64_t e = eh / a.H, h = eh % a.H;
   const View& X = REV ? a.q : a.k;
@@ -107,20 +114,23 @@ __device__ __forceinline__ bool walk_as(WalkLds<F, KP, C>& lds, const Args& a, i
   }
   if (!CARE && any_of_block<kThreads>(odd.wave, any_odd(S), tid)) return false;
 
-  float* to = seg_state + (eh * a.nseg + seg + 1) * KP * VP;
+  float* to = p.seg_state + (eh * a.nseg + seg + 1) * KP * VP;
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt)
     *reinterpret_cast<f32x4*>(to + (kt * 16 + col) * VP + v0 + w * 16 + grp * 4) = S[kt];
-  if (tid == 0 && vs == 0) seg_decay[eh * a.nseg + seg + 1] = decay;
+  if (tid == 0 && vs == 0) p.seg_decay[eh * a.nseg + seg + 1] = decay;
   return true;
 }
 
 // At least as many waves as the walk without care leaves room for.
 template <class F, int KP, int C, bool REV, bool VEC>
-__global__ void __launch_bounds__(kThreads, KP == 128 ? 2 : F::NT < 3 && VEC ? 4 : 3) walk_kernel(const Args a, int64_t VP, float* seg_state, float* seg_decay) {
+__global__ void __launch_bounds__(kThreads, KP == 128 ? 2 : F::NT < 3 && VEC ? 4 : 3) walk_kernel(const WalkArgs p) {
   __shared__ WalkLds<F, KP, C> lds;
-  if (!walk_as<F, KP, C, REV, VEC, false>(lds, a, VP, seg_state, seg_decay))
-    walk_as<F, KP, C, REV, VEC, true>(lds, a, VP, seg_state, seg_decay);
+  int block = (int)blockIdx.x;
+  if (walk_as<F, KP, C, REV, VEC, false>(lds, p, block)) return;
+  const WalkArgs again = argument_again<WalkArgs>();
+  asm volatile("" : "+s"(block));
+  walk_as<F, KP, C, REV, VEC, true>(lds, again, block);
 }
 
 // In place: slot 0 gets the row's entering value, slot s + 1 becomes decay * slot s + slot s + 1.
@@ -161,7 +171,7 @@ void enter_segments(const Args& a, int64_t VP, const float* given, float* seg_st
   if (a.nseg < 2) return;
   const int64_t heads = a.E * a.H;
   walk_kernel<F, KP, C, REV, VEC>
-      <<<dim3((unsigned)(heads * (VP / 64) * (a.nseg - 1))), kThreads, 0, st>>>(a, VP, seg_state, seg_decay);
+      <<<dim3((unsigned)(heads * (VP / 64) * (a.nseg - 1))), kThreads, 0, st>>>(WalkArgs{a, VP, seg_state, seg_decay});
   CombineArgs c{seg_state, seg_decay, given, a.nseg, KP, VP, REV};
   combine_kernel<<<dim3((unsigned)(heads * (KP * VP / 256))), 256, 0, st>>>(a, c);
 }
