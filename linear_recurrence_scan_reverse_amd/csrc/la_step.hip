@@ -9,7 +9,7 @@
 //
 // Measured: 256 rows of 16 heads of 128 x 128 in float16, states in one of three pools in
 // turn: 109 to 117 us, 4.6 to 4.9 TB/s of its 539 MB (a copy: 5.25).  One pool of 315 MB called again and
-// again takes 87: the last-level cache keeps part of it.  One row: 5.5 us, a launch and
+// again takes 87: the last-level cache keeps part of it.  One row: 5.6 us, a launch and
 // two trips to memory.
 #include "rlscan_la_launch.hpp"
 

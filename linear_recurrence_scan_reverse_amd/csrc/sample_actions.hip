@@ -29,7 +29,7 @@
 // 256 rows of 64007 bfloat16 logits with top_k up to 100: 78 us, of which reading them
 // takes 6 and the few rows without a top_k nearly all: two passes with some 40 instructions
 // a logit for the float64 exponential, by one compute unit.  One row of 131072 float32
-// logits with top_p alone: 3.4, 6.7 and 11.7 us for the three shared passes and 10.2 for the
+// logits with top_p alone: 3.2, 6.6 and 11.3 us for the three shared passes and 10.7 for the
 // choice; a chain of four kernels that each wait for memory a few times (122 us on one
 // compute unit).
 #include "rlscan_logits.hpp"
