@@ -511,6 +511,67 @@ rlscan_status rlscan_action_log_probs_backward(rlscan_format fmt, const float *d
                                                const float *entropies, void *d_logits, int64_t d_stride, int64_t R,
                                                int64_t N, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Policies over token sequences: a memory of one number a channel, the heads
+ * that attention is fed with, and the table that tokens are looked up in.
+ * Formats, workspaces and errors as for the policy operators above.
+ */
+
+/* The gated recurrence, per row and channel:
+ *   s_t = rate sigmoid(r_t),  a_t = exp(-s_t),
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t,
+ * the generic recurrence x_t = a_t x_{t-1} + b_t with coefficients made from the
+ * two gates' logits i_t and r_t; a step after one flagged in `done` has a_t = 0,
+ * whatever r_t is, so that inf and NaN stay within their episode.
+ * In:  x, input_gate (i), decay_gate (r) [E,T,D] in fmt (rlscan_heads with head
+ *      unused); rate [D], >= 0 (below: NaN in the channel); done [E,T] in the
+ *      layout (optional); init_state [E,D] (optional), h_{-1}.
+ * Out: out [E,T,D] in fmt: h, rounded once from float32;
+ *      final_state [E,D] (optional): the state that the next window takes as
+ *      init_state, zero where the row's last step is flagged;
+ *      marks [E,ceil(T/RLSCAN_MARK_STEPS),D] float32 (optional): the state before
+ *      every RLSCAN_MARK_STEPS-th step, for the backward call.
+ * E*ceil(D/64) < 2^22.  With T = 0 the state is passed through. */
+#define RLSCAN_MARK_STEPS 16
+
+int64_t rlscan_gated_recurrence_workspace(rlscan_format fmt, int64_t E, int64_t T, int64_t D, int backward);
+
+rlscan_status rlscan_gated_recurrence(rlscan_format fmt, rlscan_layout layout, const rlscan_heads *x,
+                                      const rlscan_heads *input_gate, const rlscan_heads *decay_gate,
+                                      const float *rate, const uint8_t *done, const float *init_state,
+                                      const rlscan_heads *out, float *final_state, float *marks, void *workspace,
+                                      int64_t workspace_bytes, int64_t E, int64_t T, int64_t D, hipStream_t stream);
+
+/* Gradients of rlscan_gated_recurrence.
+ * In:  d_out [E,T,D], the gradient of out; the forward call's inputs and the
+ *      marks that it wrote; d_final_state [E,D] (optional).
+ * Out: dx, d_input_gate, d_decay_gate like x; d_rate [D]; d_init_state [E,D]
+ *      (optional).
+ * A step with a_t = 1 (sigmoid(r_t) = 0, or rate 0) holds the state: its
+ * gradients are the limits for sigmoid(r_t) towards 0, without the part through
+ * sqrt(1 - a_t^2).  Every sum has a fixed order: results do not vary from run to run. */
+rlscan_status rlscan_gated_recurrence_backward(
+    rlscan_format fmt, rlscan_layout layout, const rlscan_heads *d_out, const rlscan_heads *x,
+    const rlscan_heads *input_gate, const rlscan_heads *decay_gate, const float *rate, const float *marks,
+    const uint8_t *done, const float *d_final_state, const rlscan_heads *dx, const rlscan_heads *d_input_gate,
+    const rlscan_heads *d_decay_gate, float *d_rate, float *d_init_state, void *workspace, int64_t workspace_bytes,
+    int64_t E, int64_t T, int64_t D, hipStream_t stream);
+
+/* The same recurrence for one step of E rows, on states kept from call to call
+ * and updated in place.
+ * In:  x, input_gate, decay_gate [E,D] (rlscan_heads with step and head unused);
+ *      reset [E] (optional): rows whose previous step ended an episode; their
+ *      state is dropped unread; slots [E] int32 (optional): row e's state is
+ *      state[slots[e]], else state[e].  A row whose slot is outside [0, S) has
+ *      no state: its output is 0 and nothing is written.  Two rows of one call
+ *      must not share a slot.
+ * In/out: state [S,D] float32.
+ * Out: out [E,D]. */
+rlscan_status rlscan_gated_recurrence_step(rlscan_format fmt, const rlscan_heads *x, const rlscan_heads *input_gate,
+                                           const rlscan_heads *decay_gate, const float *rate, const uint8_t *reset,
+                                           const int32_t *slots, float *state, const rlscan_heads *out, int64_t E,
+                                           int64_t S, int64_t D, hipStream_t stream);
+
 #ifdef __cplusplus
 } /* extern "C" */
 #endif

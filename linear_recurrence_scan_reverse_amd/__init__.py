@@ -30,6 +30,7 @@ __all__ = [
     "linear_scan_segmented",
     "linear_attention", "linear_attention_backward", "linear_attention_step",
     "sample_actions", "action_log_probs", "action_log_probs_backward",
+    "gated_recurrence", "gated_recurrence_backward", "gated_recurrence_step",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -74,12 +75,16 @@ _SIGNATURES.update({
     "rlscan_action_log_probs": [_int, _vp, _i64, _vp, _vp, _f32] + [_vp] * 4 + [_i64] * 3 + [_vp],
     "rlscan_action_log_probs_backward": [_int, _vp, _vp, _vp, _i64, _vp, _vp, _f32, _vp, _vp, _vp, _i64, _i64, _i64,
                                          _vp],
+    "rlscan_gated_recurrence": [_int, _int] + [_vp] * 10 + [_i64] * 4 + [_vp],
+    "rlscan_gated_recurrence_backward": [_int, _int] + [_vp] * 14 + [_i64] * 4 + [_vp],
+    "rlscan_gated_recurrence_step": [_int] + [_vp] * 8 + [_i64] * 3 + [_vp],
 })
 # Workspace sizes in bytes (-1: refused).
 _SIZES = {
     "rlscan_linear_attention_workspace": [_int] + [_i64] * 6 + [_int],
     "rlscan_sample_actions_workspace": [_i64, _i64],
     "rlscan_action_log_probs_workspace": [_i64, _i64],
+    "rlscan_gated_recurrence_workspace": [_int] + [_i64] * 3 + [_int],
 }
 
 # rlscan_format codes by storage dtype name
@@ -460,14 +465,19 @@ def eligibility_traces_vec(x, terminated=None, truncated=None, init=None, *, gam
 
 
 # ----------------------------------------------------------------- policy operators
-_POLICY = ("linear_attention", "linear_attention_backward", "linear_attention_step", "sample_actions",
-           "action_log_probs", "action_log_probs_backward")
+_MODULES = {  # loaded on first use
+    "policy": ("linear_attention", "linear_attention_backward", "linear_attention_step", "sample_actions",
+               "action_log_probs", "action_log_probs_backward"),
+    "sequence": ("gated_recurrence", "gated_recurrence_backward", "gated_recurrence_step"),
+}
 
 
 def __getattr__(name):
-    if name in _POLICY:  # loaded on first use
-        from . import policy
-        for n in _POLICY:
-            globals()[n] = getattr(policy, n)
-        return globals()[name]
+    for module, names in _MODULES.items():
+        if name in names:
+            import importlib
+            loaded = importlib.import_module("." + module, __name__)
+            for n in names:
+                globals()[n] = getattr(loaded, n)
+            return globals()[name]
     raise AttributeError("module %r has no attribute %r" % (__name__, name))

@@ -1,0 +1,149 @@
+"""What a policy over token sequences has besides attention and sampling: checks and
+marshalling for librlscan's gated recurrence (declared in include/rlscan.h).
+
+Value tensors are float32, bfloat16 or float16, all of one dtype; states, rates and
+marks are float32.  Per-step tensors may be strided (time-major, slices of a fused
+projection) as long as their last dimension is contiguous.  Scratch memory and outputs that are
+not given are allocated on the call's stream.  The functions are not differentiated by
+autograd: each has its backward as a function of its own.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import policy as _p
+from .policy import _call, _flags, _on, _on_gpu, _plain, _ptr, _raw_stream, _strided, _values, _workspace
+
+_N = _p._HEADS_BYTES
+MARK_STEPS = 16  # RLSCAN_MARK_STEPS
+
+
+def _rows(tensors, time_major=False):
+    """(array to keep alive, addresses) of the [E, T, D] or [E, D] tensors as rlscan_heads."""
+    v = []
+    for x in tensors:
+        s = x.stride()
+        if len(s) == 2:
+            v += (x.data_ptr(), s[0], 0, 0)
+        else:
+            v += (x.data_ptr(), s[1], s[0], 0) if time_major else (x.data_ptr(), s[0], s[1], 0)
+    a = (ctypes.c_int64 * len(v))(*v)
+    h = ctypes.addressof(a)
+    return a, [h + i * _N for i in range(len(tensors))]
+
+
+def _recurrence_inputs(x, input_gate, decay_gate, rate, done, time_major):
+    _values(x, "x", 3)
+    dev, dt = _on_gpu(x, "x"), x.dtype
+    n0, n1, D = x.shape
+    E, T = (n1, n0) if time_major else (n0, n1)
+    _strided(x, "x", x.shape, dt, dev)
+    _strided(input_gate, "input_gate", x.shape, dt, dev)
+    _strided(decay_gate, "decay_gate", x.shape, dt, dev)
+    if not isinstance(rate, _p.torch.Tensor):
+        raise TypeError("rate must be a torch.Tensor")
+    _plain(rate, "rate", (D,), _p.torch.float32, dev)
+    return dev, dt, E, T, D, _flags(done, "done", (n0, n1), dev)
+
+
+def gated_recurrence(x, input_gate, decay_gate, rate, done=None, init_state=None, *, time_major=False,
+                     with_state=False, with_marks=False, out=None, final_state=None, marks=None, stream=None):
+    """A gated memory of one number a channel, over whole rows.
+
+    Per row and channel s_t = rate sigmoid(decay_gate_t), a_t = exp(-s_t) and
+    h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(input_gate_t) x_t; the step after one flagged in
+    ``done`` has a_t = 0, whatever the state was: inf and NaN stay within their episode.
+
+    x, input_gate, decay_gate [E, T, D] (``time_major``: [T, E, D]); rate [D] float32, not
+    negative; done [E, T]; init_state [E, D] float32.  Returns out, h in x's dtype, followed
+    by final_state [E, D] with ``with_state`` or ``final_state`` (what the next window takes as
+    init_state) and by marks [E, ceil(T / 16), D] float32 with ``with_marks`` or ``marks``
+    (states on the way, which the backward call takes)."""
+    dev, dt, E, T, D, done = _recurrence_inputs(x, input_gate, decay_gate, rate, done, time_major)
+    torch = _p.torch
+    _plain(init_state, "init_state", (E, D), torch.float32, dev)
+    fmt = _p._DTYPES[dt]
+    with _on(stream, dev):
+        out = torch.empty(x.shape, dtype=dt, device=dev) if out is None else _strided(out, "out", x.shape, dt, dev)
+        if final_state is not None:
+            _plain(final_state, "final_state", (E, D), torch.float32, dev)
+        elif with_state:
+            final_state = torch.empty((E, D), dtype=torch.float32, device=dev)
+        shape = (E, -(-T // MARK_STEPS), D)
+        if marks is not None:
+            _plain(marks, "marks", shape, torch.float32, dev)
+        elif with_marks:
+            marks = torch.empty(shape, dtype=torch.float32, device=dev)
+        ws, need = _workspace("rlscan_gated_recurrence_workspace", dev, fmt, E, T, D, 0)
+        keep, h = _rows((x, input_gate, decay_gate, out), time_major)
+        _call("rlscan_gated_recurrence", fmt, 1 if time_major else 0, h[0], h[1], h[2], rate.data_ptr(), _ptr(done),
+              _ptr(init_state), h[3], _ptr(final_state), _ptr(marks), _ptr(ws), need, E, T, D,
+              _raw_stream(stream, dev))
+    outs = (out,) + tuple(t for t in (final_state, marks) if t is not None)
+    return outs if len(outs) > 1 else out
+
+
+def gated_recurrence_backward(d_out, x, input_gate, decay_gate, rate, marks, done=None, d_final_state=None, *,
+                              time_major=False, dx=None, d_input_gate=None, d_decay_gate=None, d_rate=None,
+                              d_init_state=None, stream=None):
+    """Gradients of ``gated_recurrence``: (dx, d_input_gate, d_decay_gate, d_rate, d_init_state).
+
+    d_out like the output; marks are the forward call's, the other inputs as in it;
+    d_final_state [E, D], if the final state was used."""
+    dev, dt, E, T, D, done = _recurrence_inputs(x, input_gate, decay_gate, rate, done, time_major)
+    torch = _p.torch
+    _strided(d_out, "d_out", x.shape, dt, dev)
+    if not isinstance(marks, torch.Tensor):
+        raise TypeError("marks must be a torch.Tensor")
+    _plain(marks, "marks", (E, -(-T // MARK_STEPS), D), torch.float32, dev)
+    _plain(d_final_state, "d_final_state", (E, D), torch.float32, dev)
+    fmt = _p._DTYPES[dt]
+    with _on(stream, dev):
+        dx, di, dd = [torch.empty(x.shape, dtype=dt, device=dev) if g is None else _strided(g, name, x.shape, dt, dev)
+                      for g, name in ((dx, "dx"), (d_input_gate, "d_input_gate"), (d_decay_gate, "d_decay_gate"))]
+        dr = torch.empty_like(rate) if d_rate is None else _plain(d_rate, "d_rate", (D,), torch.float32, dev)
+        dh = d_init_state
+        if dh is None:
+            dh = torch.empty((E, D), dtype=torch.float32, device=dev)
+        else:
+            _plain(dh, "d_init_state", (E, D), torch.float32, dev)
+        ws, need = _workspace("rlscan_gated_recurrence_workspace", dev, fmt, E, T, D, 1)
+        keep, h = _rows((d_out, x, input_gate, decay_gate, dx, di, dd), time_major)
+        _call("rlscan_gated_recurrence_backward", fmt, 1 if time_major else 0, *h[:4], rate.data_ptr(),
+              marks.data_ptr(), _ptr(done), _ptr(d_final_state), *h[4:], dr.data_ptr(), dh.data_ptr(), _ptr(ws), need,
+              E, T, D, _raw_stream(stream, dev))
+    return dx, di, dd, dr, dh
+
+
+def gated_recurrence_step(x, input_gate, decay_gate, rate, state, reset=None, slots=None, *, out=None, stream=None):
+    """One step of ``gated_recurrence`` for E rows; ``state`` is updated in place.
+
+    x, input_gate, decay_gate [E, D]; rate [D] float32; state [S, D] float32; reset [E]: rows
+    that start a new episode (their state is dropped unread); slots [E] int32: row e's
+    state is state[slots[e]] (state[e] if not given).  A row whose slot is outside [0, S)
+    gets zeros and changes nothing; two rows of a call must not share a slot.  Returns
+    out [E, D]."""
+    _values(x, "x", 2)
+    dev, dt = _on_gpu(x, "x"), x.dtype
+    torch = _p.torch
+    E, D = x.shape
+    _strided(x, "x", (E, D), dt, dev)
+    _strided(input_gate, "input_gate", (E, D), dt, dev)
+    _strided(decay_gate, "decay_gate", (E, D), dt, dev)
+    if not isinstance(rate, torch.Tensor):
+        raise TypeError("rate must be a torch.Tensor")
+    _plain(rate, "rate", (D,), torch.float32, dev)
+    if not isinstance(state, torch.Tensor) or state.dim() != 2:
+        raise ValueError("state must be a [S, D] tensor")
+    S = state.shape[0]
+    _plain(state, "state", (S, D), torch.float32, dev)
+    reset = _flags(reset, "reset", (E,), dev)
+    _plain(slots, "slots", (E,), torch.int32, dev)
+    if slots is None and S < E:
+        raise ValueError("state has %d slots for %d rows" % (S, E))
+    with _on(stream, dev):
+        out = torch.empty((E, D), dtype=dt, device=dev) if out is None else _strided(out, "out", (E, D), dt, dev)
+        keep, h = _rows((x, input_gate, decay_gate, out))
+        _call("rlscan_gated_recurrence_step", _p._DTYPES[dt], h[0], h[1], h[2], rate.data_ptr(), _ptr(reset),
+              _ptr(slots), state.data_ptr(), h[3], E, S, D, _raw_stream(stream, dev))
+    return out
