@@ -572,6 +572,63 @@ rlscan_status rlscan_gated_recurrence_step(rlscan_format fmt, const rlscan_heads
                                            const int32_t *slots, float *state, const rlscan_heads *out, int64_t E,
                                            int64_t S, int64_t D, hipStream_t stream);
 
+/* Queries and keys of attention, each head normalised and rotated by its position:
+ *   n = x / sqrt(mean(x^2) + eps),  z = w n,
+ *   y_a = z_a cos - z_b sin,  y_b = z_b cos + z_a sin   for the pairs (a, b) of the
+ * first `rotate` elements, by the angle positions[e,t] base^(-2j / rotate) for pair j:
+ * (2j, 2j + 1) if interleaved, else (j, j + rotate / 2).  The rest of z is passed on.
+ * Angles are made in float64, sums and all else in float32 (mean(x^2) past its range: 0).
+ * In:  q [E,T,H,D], k [E,T,Hk,D] in fmt (H or Hk may be 0); q_weight, k_weight [D]
+ *      (optional: ones); positions [E,T] int32 in the layout, of either sign
+ *      (not read, and optional, if rotate is 0).
+ * Out: q_out, k_out like q, k, rounded once.
+ * 1 <= D <= RLSCAN_MAX_NORM_DIM, rotate even and at most D, base > 0, eps >= 0 (with
+ * eps 0 a row of zeros gives NaN). */
+#define RLSCAN_MAX_NORM_DIM 256
+
+rlscan_status rlscan_norm_rotate_heads(rlscan_format fmt, rlscan_layout layout, const rlscan_heads *q,
+                                       const rlscan_heads *k, const float *q_weight, const float *k_weight,
+                                       const int32_t *positions, const rlscan_heads *q_out, const rlscan_heads *k_out,
+                                       int64_t E, int64_t T, int64_t H, int64_t Hk, int64_t D, int64_t rotate,
+                                       float base, int interleaved, float eps, hipStream_t stream);
+
+/* Gradients of rlscan_norm_rotate_heads.
+ * In:  d_q_out, d_k_out, the gradients of the outputs; the forward call's inputs.
+ * Out: dq, dk like q, k; d_q_weight, d_k_weight [D] (optional, also where the weight is
+ *      not given).  Every sum has a fixed order: results do not vary from run to run.
+ * The workspace is of rlscan_norm_rotate_heads_workspace bytes. */
+int64_t rlscan_norm_rotate_heads_workspace(int64_t E, int64_t T, int64_t H, int64_t Hk, int64_t D);
+
+rlscan_status rlscan_norm_rotate_heads_backward(
+    rlscan_format fmt, rlscan_layout layout, const rlscan_heads *d_q_out, const rlscan_heads *d_k_out,
+    const rlscan_heads *q, const rlscan_heads *k, const float *q_weight, const float *k_weight,
+    const int32_t *positions, const rlscan_heads *dq, const rlscan_heads *dk, float *d_q_weight, float *d_k_weight,
+    void *workspace, int64_t workspace_bytes, int64_t E, int64_t T, int64_t H, int64_t Hk, int64_t D, int64_t rotate,
+    float base, int interleaved, float eps, hipStream_t stream);
+
+/* Rows of a table by token: out_r = scale table[tokens_r], zeros for a token outside
+ * [0,N) (padding).
+ * In:  table [N,D] in fmt, rows table_stride apart; tokens [R] int64 (as
+ *      rlscan_sample_actions gives them).
+ * Out: out [R,D] in fmt, rows out_stride apart, rounded once.
+ * 1 <= N <= 2^20, 1 <= D <= RLSCAN_MAX_TABLE_DIM, R <= 2^26 and R ceil(D/64) < 2^26. */
+#define RLSCAN_MAX_TABLE_DIM 32768
+
+rlscan_status rlscan_embed_tokens(rlscan_format fmt, const void *table, int64_t table_stride, const int64_t *tokens,
+                                  void *out, int64_t out_stride, int64_t R, int64_t N, int64_t D, float scale,
+                                  hipStream_t stream);
+
+/* Gradient of the table: d_table_n = scale * sum of d_out_r over the tokens n, in
+ * float32 and in the order of the tokens, rounded once; every row is written, rows without a
+ * token with zeros, and padding adds to none.  Results do not vary from run to run.
+ * The workspace is of rlscan_embed_tokens_workspace bytes. */
+int64_t rlscan_embed_tokens_workspace(int64_t R, int64_t N, int64_t D);
+
+rlscan_status rlscan_embed_tokens_backward(rlscan_format fmt, const void *d_out, int64_t out_stride,
+                                           const int64_t *tokens, void *d_table, int64_t table_stride, void *workspace,
+                                           int64_t workspace_bytes, int64_t R, int64_t N, int64_t D, float scale,
+                                           hipStream_t stream);
+
 #ifdef __cplusplus
 } /* extern "C" */
 #endif

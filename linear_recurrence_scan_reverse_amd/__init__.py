@@ -31,6 +31,7 @@ __all__ = [
     "linear_attention", "linear_attention_backward", "linear_attention_step",
     "sample_actions", "action_log_probs", "action_log_probs_backward",
     "gated_recurrence", "gated_recurrence_backward", "gated_recurrence_step",
+    "norm_rotate_heads", "norm_rotate_heads_backward", "embed_tokens", "embed_tokens_backward",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -78,6 +79,10 @@ _SIGNATURES.update({
     "rlscan_gated_recurrence": [_int, _int] + [_vp] * 10 + [_i64] * 4 + [_vp],
     "rlscan_gated_recurrence_backward": [_int, _int] + [_vp] * 14 + [_i64] * 4 + [_vp],
     "rlscan_gated_recurrence_step": [_int] + [_vp] * 8 + [_i64] * 3 + [_vp],
+    "rlscan_norm_rotate_heads": [_int, _int] + [_vp] * 7 + [_i64] * 6 + [_f32, _int, _f32, _vp],
+    "rlscan_norm_rotate_heads_backward": [_int, _int] + [_vp] * 12 + [_i64] * 7 + [_f32, _int, _f32, _vp],
+    "rlscan_embed_tokens": [_int, _vp, _i64, _vp, _vp] + [_i64] * 4 + [_f32, _vp],
+    "rlscan_embed_tokens_backward": [_int, _vp, _i64, _vp, _vp, _i64, _vp] + [_i64] * 4 + [_f32, _vp],
 })
 # Workspace sizes in bytes (-1: refused).
 _SIZES = {
@@ -85,6 +90,8 @@ _SIZES = {
     "rlscan_sample_actions_workspace": [_i64, _i64],
     "rlscan_action_log_probs_workspace": [_i64, _i64],
     "rlscan_gated_recurrence_workspace": [_int] + [_i64] * 3 + [_int],
+    "rlscan_norm_rotate_heads_workspace": [_i64] * 5,
+    "rlscan_embed_tokens_workspace": [_i64] * 3,
 }
 
 # rlscan_format codes by storage dtype name
@@ -468,7 +475,8 @@ def eligibility_traces_vec(x, terminated=None, truncated=None, init=None, *, gam
 _MODULES = {  # loaded on first use
     "policy": ("linear_attention", "linear_attention_backward", "linear_attention_step", "sample_actions",
                "action_log_probs", "action_log_probs_backward"),
-    "sequence": ("gated_recurrence", "gated_recurrence_backward", "gated_recurrence_step"),
+    "sequence": ("gated_recurrence", "gated_recurrence_backward", "gated_recurrence_step", "norm_rotate_heads",
+                 "norm_rotate_heads_backward", "embed_tokens", "embed_tokens_backward"),
 }
 
 

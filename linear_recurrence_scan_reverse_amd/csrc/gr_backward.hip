@@ -9,6 +9,7 @@
 // pairs of A and y.  The states h_{t-1} are computed again from the marks that the forward
 // call left every kMark steps.
 #include "rlscan_gr.hpp"
+#include "rlscan_sums.hpp"
 
 namespace rlscan {
 namespace gr {
@@ -163,23 +164,6 @@ __global__ void __launch_bounds__(64 * W) backward_kernel(const Args p, int64_t 
   }
 }
 
-// The rows of partial sums added up: 64 channels a block, each wave a share of the rows, in float64.
-__global__ void __launch_bounds__(1024) rate_kernel(const float* part, float* out, int64_t rows, int64_t D) {
-  __shared__ double s[16][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t d = (int64_t)blockIdx.x * 64 + lane;
-  double sum = 0.0;
-  if (d < D) {
-    for (int64_t r = w; r < rows; r += 16) sum += (double)part[r * D + d];
-  }
-  s[w][lane] = sum;
-  __syncthreads();
-  if (w == 0 && d < D) {
-    for (int u = 1; u < 16; ++u) sum += s[u][lane];
-    out[d] = (float)sum;
-  }
-}
-
 template <class F, int W>
 static hipError_t backward_waves(const Args& a, hipStream_t st) {
   const int64_t tiles = (a.D + 63) / 64;
@@ -192,8 +176,7 @@ static hipError_t backward_waves(const Args& a, hipStream_t st) {
   backward_kernel<F, W, false><<<dim3((unsigned)(a.groups * a.nseg * tiles)), 64 * W, 0, st>>>(a, tiles);
   e = hipGetLastError();
   if (e != hipSuccess || !a.rate_part) return e;
-  rate_kernel<<<dim3((unsigned)tiles), 1024, 0, st>>>(a.rate_part, a.d_rate, a.groups * a.nseg, a.D);
-  return hipGetLastError();
+  return sums::launch_columns(a.rate_part, a.groups * a.nseg, a.d_rate, a.D, nullptr, 0, st);
 }
 
 template <class F>

@@ -1,8 +1,9 @@
 """What a policy over token sequences has besides attention and sampling: checks and
-marshalling for librlscan's gated recurrence (declared in include/rlscan.h).
+marshalling for librlscan's gated recurrence, normalised and rotated heads, and rows of a table
+by token (declared in include/rlscan.h).
 
-Value tensors are float32, bfloat16 or float16, all of one dtype; states, rates and
-marks are float32.  Per-step tensors may be strided (time-major, slices of a fused
+Value tensors are float32, bfloat16 or float16, all of one dtype; states, rates, marks and the
+heads' weights are float32.  Per-step tensors may be strided (time-major, slices of a fused
 projection) as long as their last dimension is contiguous.  Scratch memory and outputs that are
 not given are allocated on the call's stream.  The functions are not differentiated by
 autograd: each has its backward as a function of its own.
@@ -12,7 +13,8 @@ from __future__ import annotations
 import ctypes
 
 from . import policy as _p
-from .policy import _call, _flags, _on, _on_gpu, _plain, _ptr, _raw_stream, _strided, _values, _workspace
+from .policy import (_call, _flags, _on, _on_gpu, _plain, _ptr, _raw_stream, _row_stride, _strided, _values,
+                     _workspace)
 
 _N = _p._HEADS_BYTES
 MARK_STEPS = 16  # RLSCAN_MARK_STEPS
@@ -147,3 +149,157 @@ def gated_recurrence_step(x, input_gate, decay_gate, rate, state, reset=None, sl
         _call("rlscan_gated_recurrence_step", _p._DTYPES[dt], h[0], h[1], h[2], rate.data_ptr(), _ptr(reset),
               _ptr(slots), state.data_ptr(), h[3], E, S, D, _raw_stream(stream, dev))
     return out
+
+
+def _head_rows(tensors, time_major):
+    """(array to keep alive, addresses) of the [E, T, H, D] or [E, H, D] tensors as rlscan_heads."""
+    v = []
+    for x in tensors:
+        s = x.stride()
+        if len(s) == 3:
+            v += (x.data_ptr(), s[0], 0, s[1])
+        else:
+            v += (x.data_ptr(), s[1], s[0], s[2]) if time_major else (x.data_ptr(), s[0], s[1], s[2])
+    a = (ctypes.c_int64 * len(v))(*v)
+    h = ctypes.addressof(a)
+    return a, [h + i * _N for i in range(len(tensors))]
+
+
+def _head_inputs(q, k, q_weight, k_weight, positions, rotate, time_major):
+    if _p.torch is None:
+        _p._import_torch()
+    torch = _p.torch
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [E, T, H, D] or, for one step, [E, H, D], got shape %s" % (tuple(q.shape),))
+    _values(q, "q", q.dim())
+    _values(k, "k", q.dim())
+    dev, dt = _on_gpu(q, "q"), q.dtype
+    lead, (H, D), Hk = tuple(q.shape[:-2]), q.shape[-2:], k.shape[-2]
+    if len(lead) == 1:
+        E, T = lead[0], 1
+    else:
+        E, T = (lead[1], lead[0]) if time_major else lead
+    _strided(q, "q", q.shape, dt, dev)
+    _strided(k, "k", lead + (Hk, D), dt, dev)
+    _plain(q_weight, "q_weight", (D,), torch.float32, dev)
+    _plain(k_weight, "k_weight", (D,), torch.float32, dev)
+    _plain(positions, "positions", lead, torch.int32, dev)
+    if rotate is None:
+        rotate = 0 if positions is None else D
+    rotate = int(rotate)
+    if rotate < 0 or rotate > D or rotate % 2:
+        raise ValueError("rotate must be even and in [0, %d], got %d" % (D, rotate))
+    if rotate and positions is None:
+        raise ValueError("positions must be given to rotate by them")
+    return dev, dt, E, T, H, Hk, D, rotate
+
+
+def norm_rotate_heads(q, k, q_weight=None, k_weight=None, positions=None, *, rotate=None, base=10000.0,
+                      interleaved=False, eps=1e-6, time_major=False, q_out=None, k_out=None, stream=None):
+    """Queries and keys of attention, each head normalised and rotated by its position.
+
+    Every head x becomes w x / sqrt(mean(x^2) + eps), and the pairs of its first ``rotate``
+    elements (all of them if not given) are turned by positions[e, t] base^(-2j / rotate):
+    pair j is (j, j + rotate / 2), or (2j, 2j + 1) if ``interleaved``.
+
+    q [E, T, H, D], k [E, T, Hk, D] (``time_major``: [T, E, ...]; one step: [E, H, D]), D up to
+    256; q_weight, k_weight [D] float32 (None: ones); positions [E, T] (one step: [E]) int32,
+    None for normalising alone.  Returns (q_out, k_out) of their shapes and dtype."""
+    dev, dt, E, T, H, Hk, D, rotate = _head_inputs(q, k, q_weight, k_weight, positions, rotate, time_major)
+    torch = _p.torch
+    with _on(stream, dev):
+        q_out = torch.empty(q.shape, dtype=dt, device=dev) if q_out is None else _strided(q_out, "q_out", q.shape, dt, dev)
+        k_out = torch.empty(k.shape, dtype=dt, device=dev) if k_out is None else _strided(k_out, "k_out", k.shape, dt, dev)
+        keep, h = _head_rows((q, k, q_out, k_out), time_major)
+        _call("rlscan_norm_rotate_heads", _p._DTYPES[dt], 1 if time_major and q.dim() == 4 else 0, h[0], h[1],
+              _ptr(q_weight), _ptr(k_weight), _ptr(positions), h[2], h[3], E, T, H, Hk, D, rotate, float(base),
+              bool(interleaved), float(eps), _raw_stream(stream, dev))
+    return q_out, k_out
+
+
+def norm_rotate_heads_backward(d_q_out, d_k_out, q, k, q_weight=None, k_weight=None, positions=None, *, rotate=None,
+                               base=10000.0, interleaved=False, eps=1e-6, time_major=False, dq=None, dk=None,
+                               d_q_weight=None, d_k_weight=None, stream=None):
+    """Gradients of ``norm_rotate_heads``: (dq, dk, d_q_weight, d_k_weight).
+
+    d_q_out and d_k_out like the outputs, the other arguments as in the forward call.  The
+    gradient of a weight that is None is None, unless its buffer is given."""
+    dev, dt, E, T, H, Hk, D, rotate = _head_inputs(q, k, q_weight, k_weight, positions, rotate, time_major)
+    torch = _p.torch
+    _strided(d_q_out, "d_q_out", q.shape, dt, dev)
+    _strided(d_k_out, "d_k_out", k.shape, dt, dev)
+    with _on(stream, dev):
+        dq = torch.empty(q.shape, dtype=dt, device=dev) if dq is None else _strided(dq, "dq", q.shape, dt, dev)
+        dk = torch.empty(k.shape, dtype=dt, device=dev) if dk is None else _strided(dk, "dk", k.shape, dt, dev)
+        _plain(d_q_weight, "d_q_weight", (D,), torch.float32, dev)
+        _plain(d_k_weight, "d_k_weight", (D,), torch.float32, dev)
+        if d_q_weight is None and q_weight is not None:
+            d_q_weight = torch.empty_like(q_weight)
+        if d_k_weight is None and k_weight is not None:
+            d_k_weight = torch.empty_like(k_weight)
+        ws, need = _workspace("rlscan_norm_rotate_heads_workspace", dev, E, T, H, Hk, D)
+        keep, h = _head_rows((d_q_out, d_k_out, q, k, dq, dk), time_major)
+        _call("rlscan_norm_rotate_heads_backward", _p._DTYPES[dt], 1 if time_major and q.dim() == 4 else 0, *h[:4],
+              _ptr(q_weight), _ptr(k_weight), _ptr(positions), h[4], h[5], _ptr(d_q_weight), _ptr(d_k_weight), _ptr(ws),
+              need, E, T, H, Hk, D, rotate, float(base), bool(interleaved), float(eps), _raw_stream(stream, dev))
+    return dq, dk, d_q_weight, d_k_weight
+
+
+def _table_rows(x, name):
+    """Elements between the rows of a [..., D] tensor that may have none."""
+    return _row_stride(x, name) if x.numel() else x.shape[-1]
+
+
+def embed_tokens(table, tokens, *, scale=1.0, out=None, stream=None):
+    """Rows of a table by token, times a scale: out[...] = scale * table[tokens[...]].
+
+    table [N, D], rows at one distance; tokens [...] int64, as ``sample_actions`` gives them:
+    one outside [0, N), as for a padded step, gives zeros.  Returns out [..., D] in the
+    table's dtype."""
+    _values(table, "table", 2)
+    dev, dt = _on_gpu(table, "table"), table.dtype
+    torch = _p.torch
+    N, D = table.shape
+    _strided(table, "table", table.shape, dt, dev)
+    if not isinstance(tokens, torch.Tensor):
+        raise TypeError("tokens must be a torch.Tensor")
+    _plain(tokens, "tokens", tokens.shape, torch.int64, dev)
+    shape = tuple(tokens.shape) + (D,)
+    with _on(stream, dev):
+        out = torch.empty(shape, dtype=dt, device=dev) if out is None else _strided(out, "out", shape, dt, dev)
+        _call("rlscan_embed_tokens", _p._DTYPES[dt], table.data_ptr(), _table_rows(table, "table"), tokens.data_ptr(),
+              out.data_ptr(), _table_rows(out, "out"), tokens.numel(), N, D, float(scale), _raw_stream(stream, dev))
+    return out
+
+
+def embed_tokens_backward(d_out, tokens, N, *, scale=1.0, d_table=None, stream=None):
+    """Gradient of the table of ``embed_tokens``: [N, D] in d_out's dtype.
+
+    Row n is scale times the sum of d_out [..., D] over the tokens that are n, in float32 and
+    in the order of the tokens: the same from run to run.  Rows without a token are zero."""
+    if _p.torch is None:
+        _p._import_torch()
+    torch = _p.torch
+    if not isinstance(d_out, torch.Tensor):
+        raise TypeError("d_out must be a torch.Tensor")
+    _values(d_out, "d_out", d_out.dim())
+    dev, dt = _on_gpu(d_out, "d_out"), d_out.dtype
+    if d_out.dim() < 1:
+        raise ValueError("d_out must be [..., D]")
+    D, N = d_out.shape[-1], int(N)
+    if not isinstance(tokens, torch.Tensor):
+        raise TypeError("tokens must be a torch.Tensor")
+    _plain(tokens, "tokens", d_out.shape[:-1], torch.int64, dev)
+    R = tokens.numel()
+    with _on(stream, dev):
+        ws, need = _workspace("rlscan_embed_tokens_workspace", dev, R, N, D)
+        if d_table is None:
+            d_table = torch.empty((N, D), dtype=dt, device=dev)
+        else:
+            _strided(d_table, "d_table", (N, D), dt, dev)
+        _call("rlscan_embed_tokens_backward", _p._DTYPES[dt], d_out.data_ptr(), _table_rows(d_out, "d_out"),
+              tokens.data_ptr(), d_table.data_ptr(), _table_rows(d_table, "d_table"), _ptr(ws), need, R, N, D,
+              float(scale), _raw_stream(stream, dev))
+    return d_table

@@ -130,3 +130,70 @@ class Recurrence:
         self.d_rate, self.d_rate_b = d_rate, d_rate_b + TINY[torch.float32]
         self.d_init = e
         self.d_init_b = eb + TINY[torch.float32]
+
+
+# ------------------------------------------------------------------ normalised and rotated heads
+class Heads:
+    """y and, given dy, dx and dw of [..., H, D] heads with positions [...], each with its bound
+    before storage.
+
+    Bounds: a mean of squares is off by a few roundings for each of the 16 terms that a lane adds, the
+    6 steps over lanes and the division: 26 of U at most, its root's reciprocal by 13 and 2; x inv w by
+    2 more.  A sine or cosine by 4 of U: the angle's two roundings and the series'.  A turned pair
+    by its members' errors, its angle's and two roundings: 26 of U of |a| + |b|; 32 here."""
+
+    def __init__(self, x, weight, positions, rotate, base=10000.0, interleaved=False, eps=1e-6, dy=None):
+        x = x.cpu().double()
+        D = x.shape[-1]
+        w = torch.ones(D, dtype=torch.float64) if weight is None else weight.cpu().double()
+        a = torch.arange(0, rotate, 2) if interleaved else torch.arange(rotate // 2)
+        b = a + 1 if interleaved else a + rotate // 2
+        freq = base ** (-2.0 * torch.arange(rotate // 2, dtype=torch.float64) / max(1, rotate))
+        pos = torch.zeros(x.shape[:-2]) if positions is None else positions.cpu()
+        angle = (pos.double()[..., None] * freq).unsqueeze(-2)  # the same for a token's heads
+
+        def turn(z, back=False):
+            sin = -angle.sin() if back else angle.sin()
+            za, zb = z[..., a], z[..., b]
+            out, size = z.clone(), z.abs()
+            out[..., a], out[..., b] = za * angle.cos() - zb * sin, zb * angle.cos() + za * sin
+            size[..., a] = size[..., b] = za.abs() + zb.abs()
+            return out, size
+
+        inv = 1.0 / torch.sqrt((x * x).mean(-1, keepdim=True) + eps)
+        n = x * inv
+        self.y, size = turn(n * w)
+        self.y_b = 32 * U * size
+        if dy is None:
+            return
+        dz, size = turn(dy.cpu().double(), back=True)
+        lead = tuple(range(x.dim() - 1))
+        count = x.numel() // D
+        self.dw = (dz * n).sum(lead)
+        self.dw_b = (32 + count) * U * (size * n.abs()).sum(lead) + TINY[torch.float32]
+        g, gabs = dz * w, size * w.abs()
+        self.dx = inv * (g - n * (g * n).mean(-1, keepdim=True))
+        # dz 8 of U, inv 15, n 16, the mean 26 and its factors' 24: under 100 in all, twice n's for its square
+        self.dx_b = 100 * U * inv * (gabs + n.abs() * (gabs * n.abs()).mean(-1, keepdim=True))
+
+
+# ------------------------------------------------------------------ rows of a table
+def lookup(table, tokens, scale):
+    t = tokens.cpu()
+    ok = (t >= 0) & (t < table.shape[0])
+    out = table.cpu().double()[t.clamp(0, table.shape[0] - 1)] * scale
+    return torch.where(ok[..., None], out, torch.zeros_like(out))
+
+
+def table_gradient(d_out, tokens, N, scale):
+    """(gradient, bound before storage): a row of c terms takes c additions and the scale."""
+    D = d_out.shape[-1]
+    t, d = tokens.cpu().reshape(-1), d_out.cpu().double().reshape(-1, D)
+    total, size, count = torch.zeros(N, D, dtype=torch.float64), torch.zeros(N, D, dtype=torch.float64), torch.zeros(N)
+    for r in range(t.numel()):
+        n = int(t[r])
+        if 0 <= n < N:
+            total[n] += d[r]
+            size[n] += d[r].abs()
+            count[n] += 1
+    return total * scale, (count.double()[:, None] + 2) * U * size * abs(scale)
