@@ -14,166 +14,274 @@
 namespace rlscan {
 namespace gr {
 
-// One block: 64 channels of the rows e, e + groups, ... (or of one segment of them), W waves of
-// kMark steps each at a time.  FOLD: the pair of the segment alone.
-template <class F, int W, bool FOLD>
-__global__ void __launch_bounds__(64 * W) backward_kernel(const Args p, int64_t tiles) {
-  using E = typename F::E;
-  constexpr int S = kMark;
-  __shared__ float s_a[2][W][64], s_y[2][W][64];
-  const int lane = threadIdx.x & 63;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t nseg = FOLD ? p.nseg - 1 : p.nseg;  // nothing comes before the first segment
-  const int64_t tile = blockIdx.x % tiles, es = blockIdx.x / tiles;
-  const int64_t seg = es % nseg + (FOLD ? 1 : 0), group = es / nseg;
-  const int64_t d = tile * 64 + lane;
-  const bool col_ok = d < p.D;
-  const int64_t dc = col_ok ? d : p.D - 1;  // loads stay inside the row
-  const float rate = p.rate[dc];
-  const int64_t begin = seg * p.seg_steps;
-  const int64_t end = p.T < begin + p.seg_steps ? p.T : begin + p.seg_steps;
-  const int64_t nmarks = (p.T + S - 1) / S;
-  float d_rate = 0.0f;
-  int buf = 0;
-  for (int64_t e = group; e < p.E; e += p.groups) {
-    const E* px = static_cast<const E*>(p.x.p) + e * p.x.se + dc;
-    const E* pi = static_cast<const E*>(p.ig.p) + e * p.ig.se + dc;
-    const E* pr = static_cast<const E*>(p.dg.p) + e * p.dg.se + dc;
-    const E* pg = static_cast<const E*>(p.dout.p) + e * p.dout.se + dc;
-    E* ox = static_cast<E*>(const_cast<void*>(p.dx.p)) + e * p.dx.se + d;
-    E* oi = static_cast<E*>(const_cast<void*>(p.dig.p)) + e * p.dig.se + d;
-    E* od = static_cast<E*>(const_cast<void*>(p.ddg.p)) + e * p.ddg.se + d;
-    const uint8_t* done = p.done ? p.done + e * p.d_se : nullptr;
-    float carry = 0.0f;  // e entering the super-tile from the steps behind it
-    if (!FOLD) {
-      if (p.d_final && !(done && p.T > 0 && done[(p.T - 1) * p.d_st] != 0)) carry = p.d_final[e * p.D + dc];
-      for (int64_t u = nseg - 1; u > seg; --u) {
-        const int64_t at = (e * p.nseg + u) * p.D + dc;
-        carry = enter(p.seg_a[at], p.seg_y[at], carry);
-      }
+// What the decays of a chunk are made of; the rest is asked for when these are at hand, and used
+// behind the barrier.
+template <class F, int S>
+struct Chunk {
+  typename F::E g[S], dg[S];
+  uint8_t flag;
+};
+template <class F, int S>
+struct Rest {
+  typename F::E x[S], ig[S];
+  float mark;
+};
+
+// sigmoid(r) and a - 1 of every step, the sum of y (logarithms of the decays) and what leaves
+// the chunk to the steps before it for an entering e of 0.
+template <int S>
+struct Decays {
+  float sr[S], em1[S];
+  float L, out;
+};
+
+// CARE: some steps start anew (cut) or lie past the end (not live).
+template <class F, int S, bool CARE>
+__device__ __forceinline__ void decays(Decays<S>& c, const Chunk<F, S>& in, float rate2, uint32_t cut, uint32_t live) {
+  c.L = c.out = 0.0f;
+#pragma unroll
+  for (int k = S - 1; k >= 0; --k) {
+    const float dg = F::get(CARE ? apart(in.dg[k]) : in.dg[k]);
+    float g = F::get(CARE ? apart(in.g[k]) : in.g[k]);
+    float sr = sigmoid(dg), y = rate2 * sr, em1 = decay_less_1(y);
+    if (CARE) {
+      sr = keep(sr, spread(live & ~cut, k));  // the gate of a step that starts anew is not looked at: it may be NaN
+      em1 = keep(pick(spread(cut, k), -1.0f, em1), spread(live, k));
+      y = keep(y, spread(live, k));
+      g = keep(g, spread(live, k));
     }
-    float total = 0.0f;  // FOLD: sum of s over the segment
-    bool dropped = false;
-    const int64_t units = (end - begin + W * S - 1) / (W * S);
-    for (int64_t n = units - 1; n >= 0; --n) {
-      const int64_t c0 = begin + (n * W + w) * S;
-      E gr[S], x[S], gi[S], gd[S];
-#pragma unroll
-      for (int k = 0; k < S; ++k) {
-        const int64_t t = c0 + k < end ? c0 + k : end - 1;
-        gd[k] = pr[t * p.dg.st];
-        gr[k] = pg[t * p.dout.st];
-        if (!FOLD) {
-          x[k] = px[t * p.x.st];
-          gi[k] = pi[t * p.ig.st];
-        }
-      }
-      float h = 0.0f;
-      if (!FOLD && c0 < end) h = p.marks[(e * nmarks + c0 / S) * p.D + dc];
-      bool dn = false;  // lane k: whether step c0 + k starts anew
-      if (done && lane < S) {
-        const int64_t t = c0 + lane;
-        if (t > 0 && t < end) dn = done[(t - 1) * p.d_st] != 0;
-      }
-      const uint32_t cut = (uint32_t)__builtin_amdgcn_ballot_w64(dn);
-      float em1[S], sr[S], L = 0.0f, y = 0.0f;
-#pragma unroll
-      for (int k = S - 1; k >= 0; --k) {
-        const bool live = c0 + k < end, fresh = (cut >> k) & 1;
-        sr[k] = fresh ? 0.0f : sigmoid(F::get(gd[k]));  // not looked at: it may be NaN
-        const float s = rate * sr[k];
-        em1[k] = live ? decay_less_1(s) : 0.0f;
-        L += live ? s : 0.0f;
-        const float g = y + (live ? F::get(gr[k]) : 0.0f);
-        y = fresh ? 0.0f : decayed(em1[k], g);
-      }
-      const float A = cut ? kDropped : exp2_fast(-kLog2E * L);
-      s_a[buf][w][lane] = A;
-      s_y[buf][w][lane] = y;
-      __syncthreads();
-      float c = carry;  // e entering this wave's chunk
-      for (int u = W - 1; u > w; --u) c = enter(s_a[buf][u][lane], s_y[buf][u][lane], c);
-      float next = c;
-      for (int u = w; u >= 0; --u) next = enter(s_a[buf][u][lane], s_y[buf][u][lane], next);
-      carry = next;
-      buf ^= 1;
-      if (FOLD) {
-        total += L;
-        dropped |= cut != 0;
-        continue;
-      }
-      float before[S], u_[S], si[S];
-#pragma unroll
-      for (int k = 0; k < S; ++k) {
-        const bool fresh = (cut >> k) & 1;
-        si[k] = sigmoid(F::get(gi[k]));
-        u_[k] = si[k] * F::get(x[k]);
-        before[k] = fresh ? 0.0f : h;
-        const float step = fresh ? -1.0f : em1[k];
-        h = decayed(step, before[k]) + __builtin_amdgcn_sqrtf(one_less_square(step)) * u_[k];
-      }
-#pragma unroll
-      for (int k = S - 1; k >= 0; --k) {
-        const bool live = c0 + k < end, fresh = (cut >> k) & 1;
-        const float g = c + (live ? F::get(gr[k]) : 0.0f);
-        const float m2 = fresh ? 1.0f : one_less_square(em1[k]);
-        const float over_m = m2 >= 1.1754944e-38f ? __builtin_amdgcn_rsqf(m2) : 0.0f;  // a held state has no part in u
-        const float du = m2 * over_m * g;
-        const float dx = si[k] * du;
-        const float a = 1.0f + em1[k];
-        const float dlog = g * (a * (before[k] - u_[k] * a * over_m));
-        const float t_ = fresh || !live ? 0.0f : sr[k] * dlog;
-        d_rate -= t_;
-        if (col_ok && live) {
-          const int64_t t = c0 + k;
-          ox[t * p.dx.st] = F::put(dx);
-          oi[t * p.dig.st] = F::put(u_[k] * du * (1.0f - si[k]));
-          od[t * p.ddg.st] = F::put(-(rate * (1.0f - sr[k])) * t_);
-        }
-        c = fresh ? 0.0f : decayed(em1[k], g);
-      }
-    }
-    if (FOLD) {
-      __syncthreads();
-      s_a[0][w][lane] = total;
-      s_y[0][w][lane] = dropped ? 1.0f : 0.0f;
-      __syncthreads();
-      if (w == 0 && col_ok) {
-        float sum = 0.0f, any = 0.0f;
-        for (int u = 0; u < W; ++u) {
-          sum += s_a[0][u][lane];
-          any += s_y[0][u][lane];
-        }
-        const int64_t at = (e * p.nseg + seg) * p.D + d;
-        p.seg_a[at] = any > 0.0f ? kDropped : exp2_fast(-kLog2E * sum);
-        p.seg_y[at] = carry;
-      }
-      __syncthreads();
-    } else if (w == 0 && col_ok && seg == 0 && p.d_init) {
-      p.d_init[e * p.D + d] = carry;
-    }
-  }
-  if (FOLD) return;
-  __syncthreads();
-  s_a[0][w][lane] = d_rate;
-  __syncthreads();
-  if (w == 0 && col_ok) {
-    float sum = 0.0f;
-    for (int u = 0; u < W; ++u) sum += s_a[0][u][lane];
-    (p.rate_part ? p.rate_part : p.d_rate)[(group * nseg + seg) * p.D + d] = sum;
+    c.sr[k] = sr;
+    c.em1[k] = em1;
+    c.L += y;
+    c.out = decayed(em1, c.out + g);
+    if (CARE) c.out = keep(c.out, ~spread(cut, k));
   }
 }
 
-template <class F, int W>
+// What a block's waves read and write: 64 channels of a row.
+template <class F, int S, bool NEAR>
+struct Tensors {
+  Stream<F, S, NEAR> g, dg, x, ig, dx, dig, ddg;
+  // bytes from a step to the next; NEAR: of d_out, of the inputs, of the outputs
+  int64_t g_st, dg_st, x_st, ig_st, dx_st, dig_st, ddg_st;
+  const uint8_t* done;
+  int64_t done_step, mark_step;
+  const float* marks;
+  int lane;
+  uint32_t at;  // byte of the lane's column
+
+  __device__ __forceinline__ Tensors(const Args& p, int64_t e, int64_t d0, int lane_, uint32_t col)
+      : g(p.dout, e, d0), dg(p.dg, e, d0), x(p.x, e, d0), ig(p.ig, e, d0), dx(p.dx, e, d0), dig(p.dig, e, d0),
+        ddg(p.ddg, e, d0), done(p.done ? p.done + e * p.d_se : nullptr), done_step(p.d_st), mark_step(p.D),
+        marks(p.marks + e * ((p.T + kMark - 1) / kMark) * p.D + d0 + col), lane(lane_),
+        at(col * (uint32_t)sizeof(typename F::E)) {
+    constexpr int64_t es = sizeof(typename F::E);
+    g_st = p.dout.st * es;
+    dg_st = p.dg.st * es;
+    dx_st = p.dx.st * es;
+    x_st = NEAR ? dg_st : p.x.st * es;
+    ig_st = NEAR ? dg_st : p.ig.st * es;
+    dig_st = NEAR ? dx_st : p.dig.st * es;
+    ddg_st = NEAR ? dx_st : p.ddg.st * es;
+  }
+  __device__ __forceinline__ void load(Chunk<F, S>& c, int64_t t, int64_t end) const {
+    dg.load(c.dg, t, end, Steps<S, NEAR>(dg_st, t, end), at);
+    g.load(c.g, t, end, Steps<S, NEAR>(g_st, t, end), at);
+    c.flag = load_flag<S>(done, done_step, t, end, lane);
+  }
+  __device__ __forceinline__ void load(Rest<F, S>& c, int64_t t, int64_t end) const {
+    c.mark = marks[(t < end ? t : end - 1) / kMark * mark_step];
+    ig.load(c.ig, t, end, Steps<S, NEAR>(ig_st, t, end), at);
+    x.load(c.x, t, end, Steps<S, NEAR>(x_st, t, end), at);
+  }
+};
+
+// The gradients of a chunk, from the e that enters it, to memory; returns the e that leaves it.
+template <class F, int S, bool NEAR, bool CARE>
+__device__ __forceinline__ float gradients(const Decays<S>& c, const Chunk<F, S>& in, const Rest<F, S>& rest, float e,
+                                           float rate, float& d_rate, const Tensors<F, S, NEAR>& to, int64_t t,
+                                           uint32_t out_at, uint32_t cut, uint32_t live) {
+  float before[S], u[S], si[S];
+  float h = rest.mark;
+#pragma unroll
+  for (int k = 0; k < S; ++k) {
+    si[k] = sigmoid(F::get(CARE ? apart(rest.ig[k]) : rest.ig[k]));
+    u[k] = si[k] * F::get(CARE ? apart(rest.x[k]) : rest.x[k]);
+    if (CARE) h = keep(h, ~spread(cut, k));
+    before[k] = h;
+    h = decayed(c.em1[k], h) + __builtin_amdgcn_sqrtf(one_less_square(c.em1[k])) * u[k];
+  }
+#pragma unroll
+  for (int k = S - 1; k >= 0; --k) {
+    float g = F::get(CARE ? apart(in.g[k]) : in.g[k]);
+    if (CARE) g = keep(g, spread(live, k));
+    g += e;
+    const float m2 = one_less_square(c.em1[k]);
+    const float over_m = m2 >= 1.1754944e-38f ? __builtin_amdgcn_rsqf(m2) : 0.0f;  // a held state has no part in u
+    const float du = m2 * over_m * g, ud = u[k] * du;
+    e = decayed(c.em1[k], g);
+    if (CARE) e = keep(e, ~spread(cut, k));
+    // a g (h - u a / m): the gradient of log a
+    const float a = 1.0f + c.em1[k];
+    float part = c.sr[k] * (e * (before[k] - u[k] * over_m * a));
+    if (CARE) part = keep(part, spread(live & ~cut, k));
+    d_rate -= part;
+    if (!CARE || (live >> k) & 1) {
+      to.dx.store(F::put(si[k] * du), t, k, to.dx_st, out_at);
+      to.dig.store(F::put(ud - ud * si[k]), t, k, to.dig_st, out_at);
+      to.ddg.store(F::put((rate * c.sr[k] - rate) * part), t, k, to.ddg_st, out_at);
+    }
+  }
+  return e;
+}
+
+// The pair of each segment but the first: a wave takes a share of it, chunk after chunk, from the end.
+template <class F, int S, int W, bool NEAR>
+__global__ void __launch_bounds__(64 * W) fold_back_kernel(const Args p, uint32_t tiles) {
+  __shared__ float s_a[W][64], s_y[W][64];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t tile = blockIdx.x % tiles, es = blockIdx.x / tiles, nseg = (uint32_t)p.nseg;
+  const int64_t seg = es % (nseg - 1) + 1, e = es / (nseg - 1), d0 = tile * 64;
+  const bool column = d0 + lane < p.D;
+  const uint32_t col = column ? lane : (uint32_t)(p.D - 1 - d0);  // loads stay inside the row
+  const float rate2 = kLog2E * p.rate[d0 + col];
+  const Tensors<F, S, NEAR> in(p, e, d0, lane, col);
+  const int64_t share = p.seg_steps / W, begin = seg * p.seg_steps + w * share;
+  const int64_t end = p.T < begin + share ? p.T : begin + share;  // the last segment may be short
+  float total = 0.0f, y = 0.0f;
+  bool dropped = false;
+  auto fold = [&](const Chunk<F, S>& c, uint32_t live) __attribute__((always_inline)) {
+    const uint32_t cut = flag_word(c.flag);
+    Decays<S> k;
+    if (cut == 0 && live == (1u << S) - 1) decays<F, S, false>(k, c, rate2, 0, 0);
+    else decays<F, S, true>(k, c, rate2, cut, live);
+    total += k.L;
+    dropped |= cut != 0;
+    y = enter(cut ? kDropped : exp2_fast(-k.L), k.out, y);
+  };
+  if (begin < end) {
+    Chunk<F, S> one, two;
+    int64_t t = begin + (end - begin - 1) / S * S;
+    in.load(one, t, end);
+    for (;;) {
+      if (t > begin) in.load(two, t - S, end);
+      fold(one, live_word<S>(t, end));
+      if (t == begin) break;
+      t -= S;
+      if (t > begin) in.load(one, t - S, end);
+      fold(two, (1u << S) - 1);
+      if (t == begin) break;
+      t -= S;
+    }
+  }
+  s_a[w][lane] = dropped ? kDropped : exp2_fast(-total);
+  s_y[w][lane] = y;
+  __syncthreads();
+  if (w == 0 && column) {
+    float A = 1.0f, out = 0.0f;
+    for (int v = W - 1; v >= 0; --v) {
+      out = enter(s_a[v][lane], s_y[v][lane], out);
+      A = A < 0.0f || s_a[v][lane] < 0.0f ? kDropped : A * s_a[v][lane];
+    }
+    const int64_t at = (e * p.nseg + seg) * p.D + d0 + lane;
+    p.seg_a[at] = A;
+    p.seg_y[at] = out;
+  }
+}
+
+// One block: 64 channels of the rows e, e + groups, ... (or of one segment of them), W waves of
+// S steps each at a time, from the end, the next ones' loads in flight meanwhile.
+template <class F, int S, int W, bool NEAR>
+__global__ void __launch_bounds__(64 * W) backward_kernel(const Args p, uint32_t tiles) {
+  static_assert(S == kMark, "a chunk begins at a marked state");
+  __shared__ Exchange<W> s;
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t tile = blockIdx.x % tiles, es = blockIdx.x / tiles, nseg = (uint32_t)p.nseg;
+  const int64_t seg = es % nseg, group = es / nseg, d0 = tile * 64;
+  const bool column = d0 + lane < p.D;
+  const uint32_t col = column ? lane : (uint32_t)(p.D - 1 - d0);  // loads stay inside the row
+  const float rate = p.rate[d0 + col], rate2 = kLog2E * rate;
+  const int64_t begin = seg * p.seg_steps;
+  const int64_t end = p.T < begin + p.seg_steps ? p.T : begin + p.seg_steps;
+  constexpr int64_t kStep = W * S;
+  const int64_t ahead = w * S;
+  float d_rate = 0.0f;
+  int buf = 0;
+  for (int64_t e = group; e < p.E; e += p.groups) {
+    const Tensors<F, S, NEAR> in(p, e, d0, lane, col);
+    const uint32_t out_at = column ? in.at : kNoColumn;
+    float carry = 0.0f;  // e entering the W chunks at hand from the steps behind them
+    if (p.d_final && !(in.done && p.T > 0 && in.done[(p.T - 1) * p.d_st] != 0)) carry = p.d_final[e * p.D + d0 + col];
+    for (int64_t v = p.nseg - 1; v > seg; --v) {
+      const int64_t at = (e * p.nseg + v) * p.D + d0 + col;
+      carry = enter(p.seg_a[at], p.seg_y[at], carry);
+    }
+    if (W > 1) {
+      meet();  // the row before has been read
+      s.carry[buf][lane] = carry;  // the same from every wave
+    }
+    auto take = [&](const Chunk<F, S>& c, const Rest<F, S>& rest, int64_t t) __attribute__((always_inline)) {
+      const uint32_t cut = flag_word(c.flag), live = live_word<S>(t, end);
+      const bool care = cut != 0 || live != (1u << S) - 1;
+      Decays<S> k;
+      if (!care) decays<F, S, false>(k, c, rate2, 0, 0);
+      else decays<F, S, true>(k, c, rate2, cut, live);
+      float g = carry;  // e entering this wave's chunk
+      if constexpr (W > 1) {
+        s.put(buf, w, lane, exp2_fast(-k.L), k.out, cut);
+        meet();
+        g = s.template entering<-1>(buf, w, lane);
+      }
+      if (!care) g = gradients<F, S, NEAR, false>(k, c, rest, g, rate, d_rate, in, t, out_at, 0, 0);
+      else g = gradients<F, S, NEAR, true>(k, c, rest, g, rate, d_rate, in, t, out_at, cut, live);
+      carry = g;
+      if constexpr (W > 1) {  // what leaves the first wave enters the chunks before
+        buf ^= 1;
+        if (w == 0) s.carry[buf][lane] = g;
+      }
+    };
+    if (begin < end) {
+      Chunk<F, S> one, two;
+      Rest<F, S> rest;
+      int64_t t = begin + (end - begin - 1) / kStep * kStep;
+      in.load(one, t + ahead, end);
+      for (;;) {
+        in.load(rest, t + ahead, end);
+        if (t > begin) in.load(two, t - kStep + ahead, end);
+        take(one, rest, t + ahead);
+        if (t == begin) break;
+        t -= kStep;
+        in.load(rest, t + ahead, end);
+        if (t > begin) in.load(one, t - kStep + ahead, end);
+        take(two, rest, t + ahead);
+        if (t == begin) break;
+        t -= kStep;
+      }
+    }
+    if (w == 0 && column && seg == 0 && p.d_init) p.d_init[e * p.D + d0 + lane] = carry;
+  }
+  if constexpr (W > 1) {
+    __syncthreads();
+    s.a[0][w][lane] = d_rate;
+    __syncthreads();
+    d_rate = 0.0f;
+    for (int v = 0; v < W; ++v) d_rate += s.a[0][v][lane];
+  }
+  if (w == 0 && column) (p.rate_part ? p.rate_part : p.d_rate)[(group * p.nseg + seg) * p.D + d0 + lane] = d_rate;
+}
+
+template <class F, int S, int W, bool NEAR>
 static hipError_t backward_waves(const Args& a, hipStream_t st) {
   const int64_t tiles = (a.D + 63) / 64;
   hipError_t e = hipSuccess;
   if (a.nseg > 1) {
-    backward_kernel<F, W, true><<<dim3((unsigned)(a.groups * (a.nseg - 1) * tiles)), 64 * W, 0, st>>>(a, tiles);
+    fold_back_kernel<F, S, W, NEAR><<<dim3((unsigned)(a.E * (a.nseg - 1) * tiles)), 64 * W, 0, st>>>(a, (uint32_t)tiles);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  backward_kernel<F, W, false><<<dim3((unsigned)(a.groups * a.nseg * tiles)), 64 * W, 0, st>>>(a, tiles);
+  backward_kernel<F, S, W, NEAR><<<dim3((unsigned)(a.groups * a.nseg * tiles)), 64 * W, 0, st>>>(a, (uint32_t)tiles);
   e = hipGetLastError();
   if (e != hipSuccess || !a.rate_part) return e;
   return sums::launch_columns(a.rate_part, a.groups * a.nseg, a.d_rate, a.D, nullptr, 0, st);
@@ -181,10 +289,14 @@ static hipError_t backward_waves(const Args& a, hipStream_t st) {
 
 template <class F>
 static hipError_t backward_fmt(const Args& a, const Plan& p, hipStream_t st) {
+  constexpr int64_t es = sizeof(typename F::E);
+  const View *in[] = {&a.dg, &a.x, &a.ig}, *out[] = {&a.dx, &a.dig, &a.ddg}, *grad[] = {&a.dout};
+  if (!near_alike(in, 3, es) || !near_alike(out, 3, es) || !near_alike(grad, 1, es))
+    return backward_waves<F, kMark, kBackWaves, false>(a, st);
   switch (p.waves) {
-    case 1: return backward_waves<F, 1>(a, st);
-    case 4: return backward_waves<F, 4>(a, st);
-    default: return backward_waves<F, 8>(a, st);
+    case 1: return backward_waves<F, kMark, 1, true>(a, st);
+    case 4: return backward_waves<F, kMark, 4, true>(a, st);
+    default: return backward_waves<F, kMark, kBackWaves, true>(a, st);
   }
 }
 

@@ -4,128 +4,236 @@
 namespace rlscan {
 namespace gr {
 
-// One block: 64 channels of one row (or of one segment of it), W waves of kMark steps each
-// at a time.  FOLD: the pair of the segment alone, for the blocks that follow it.
-template <class F, int W, bool FOLD>
-__global__ void __launch_bounds__(64 * W) forward_kernel(const Args p, int64_t tiles) {
-  using E = typename F::E;
-  constexpr int S = kMark;
-  __shared__ float s_a[2][W][64], s_y[2][W][64];
-  const int lane = threadIdx.x & 63;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t nseg = FOLD ? p.nseg - 1 : p.nseg;  // nothing follows the last segment
-  const int64_t tile = blockIdx.x % tiles, es = blockIdx.x / tiles, seg = es % nseg, e = es / nseg;
-  const int64_t d = tile * 64 + lane;
-  const bool col_ok = d < p.D;
-  const int64_t dc = col_ok ? d : p.D - 1;  // loads stay inside the row
-  const float rate = p.rate[dc];
-  const E* px = static_cast<const E*>(p.x.p) + e * p.x.se + dc;
-  const E* pi = static_cast<const E*>(p.ig.p) + e * p.ig.se + dc;
-  const E* pr = static_cast<const E*>(p.dg.p) + e * p.dg.se + dc;
-  E* po = FOLD ? nullptr : static_cast<E*>(const_cast<void*>(p.out.p)) + e * p.out.se + d;
-  const uint8_t* done = p.done ? p.done + e * p.d_se : nullptr;
-  const int64_t begin = seg * p.seg_steps;
-  const int64_t end = p.T < begin + p.seg_steps ? p.T : begin + p.seg_steps;
+template <class F, int S>
+struct Chunk {
+  typename F::E x[S], ig[S], dg[S];
+  uint8_t flag;
+};
 
-  float carry = 0.0f;  // the state entering the super-tile
-  if (!FOLD) {
-    if (p.init) carry = p.init[e * p.D + dc];
-    for (int64_t u = 0; u < seg; ++u) {
-      const int64_t at = (e * p.nseg + u) * p.D + dc;
-      carry = enter(p.seg_a[at], p.seg_y[at], carry);
-    }
-  }
-  float total = 0.0f;   // FOLD: sum of s over the segment
-  bool dropped = false;
-  int buf = 0;
-  for (int64_t t0 = begin; t0 < end; t0 += W * S) {
-    const int64_t c0 = t0 + w * S;
-    E x[S], gi[S], gd[S];
+// a - 1 and the term of every step, the sum of y (logarithms of the decays) and what leaves the
+// chunk for a state of 0.
+template <int S>
+struct Coefficients {
+  float em1[S], b[S];
+  float L, out;
+};
+
+// CARE: some steps start anew (cut) or lie past the end (not live).
+template <class F, int S, bool CARE>
+__device__ __forceinline__ void coefficients(Coefficients<S>& c, const Chunk<F, S>& in, float rate2, uint32_t cut,
+                                             uint32_t live) {
+  c.L = c.out = 0.0f;
 #pragma unroll
-    for (int k = 0; k < S; ++k) {
-      const int64_t t = c0 + k < end ? c0 + k : end - 1;
-      x[k] = px[t * p.x.st];
-      gi[k] = pi[t * p.ig.st];
-      gd[k] = pr[t * p.dg.st];
+  for (int k = 0; k < S; ++k) {
+    const float dg = F::get(CARE ? apart(in.dg[k]) : in.dg[k]), ig = F::get(CARE ? apart(in.ig[k]) : in.ig[k]),
+                x = F::get(CARE ? apart(in.x[k]) : in.x[k]);
+    float y = rate2 * sigmoid(dg);
+    float em1 = decay_less_1(y);
+    if (CARE) em1 = pick(spread(cut, k), -1.0f, em1);
+    float b = __builtin_amdgcn_sqrtf(one_less_square(em1)) * (sigmoid(ig) * x);
+    if (CARE) {
+      em1 = keep(em1, spread(live, k));
+      b = keep(b, spread(live, k));
+      y = keep(y, spread(live, k));
+      c.out = keep(c.out, ~spread(cut, k));
     }
-    bool dn = false;  // lane k: whether step c0 + k starts anew
-    if (done && lane < S) {
-      const int64_t t = c0 + lane;
-      if (t > 0 && t < end) dn = done[(t - 1) * p.d_st] != 0;
-    }
-    const uint32_t cut = (uint32_t)__builtin_amdgcn_ballot_w64(dn);
-    float em1[S], b[S], L = 0.0f, y = 0.0f;
-#pragma unroll
-    for (int k = 0; k < S; ++k) {
-      const bool live = c0 + k < end, fresh = (cut >> k) & 1;
-      const float s = rate * sigmoid(F::get(gd[k]));
-      em1[k] = fresh ? -1.0f : decay_less_1(s);
-      b[k] = __builtin_amdgcn_sqrtf(one_less_square(em1[k])) * (sigmoid(F::get(gi[k])) * F::get(x[k]));
-      if (!live) em1[k] = b[k] = 0.0f;
-      L += live ? s : 0.0f;
-      y = decayed(em1[k], fresh ? 0.0f : y) + b[k];
-    }
-    const float A = cut ? kDropped : exp2_fast(-kLog2E * L);
-    s_a[buf][w][lane] = A;
-    s_y[buf][w][lane] = y;
-    __syncthreads();
-    float h = carry;  // the state entering this wave's chunk
-    for (int u = 0; u < w; ++u) h = enter(s_a[buf][u][lane], s_y[buf][u][lane], h);
-    float next = h;
-    for (int u = w; u < W; ++u) next = enter(s_a[buf][u][lane], s_y[buf][u][lane], next);
-    carry = next;
-    buf ^= 1;
-    if (FOLD) {
-      total += L;
-      dropped |= cut != 0;
-      continue;
-    }
-    if (p.marks && col_ok && c0 < end) p.marks[(e * ((p.T + S - 1) / S) + c0 / S) * p.D + d] = h;
-#pragma unroll
-    for (int k = 0; k < S; ++k) {
-      h = decayed(em1[k], (cut >> k) & 1 ? 0.0f : h) + b[k];
-      if (col_ok && c0 + k < end) po[(c0 + k) * p.out.st] = F::put(h);
-    }
-  }
-  if (FOLD) {
-    __syncthreads();
-    s_a[0][w][lane] = total;
-    s_y[0][w][lane] = dropped ? 1.0f : 0.0f;
-    __syncthreads();
-    if (w == 0 && col_ok) {
-      float sum = 0.0f, any = 0.0f;
-      for (int u = 0; u < W; ++u) {
-        sum += s_a[0][u][lane];
-        any += s_y[0][u][lane];
-      }
-      const int64_t at = (e * p.nseg + seg) * p.D + d;
-      p.seg_a[at] = any > 0.0f ? kDropped : exp2_fast(-kLog2E * sum);
-      p.seg_y[at] = carry;
-    }
-  } else if (w == 0 && col_ok && seg == nseg - 1 && p.final_state) {
-    const bool ended = done && p.T > 0 && done[(p.T - 1) * p.d_st] != 0;
-    p.final_state[e * p.D + d] = ended ? 0.0f : carry;
+    c.em1[k] = em1;
+    c.b[k] = b;
+    c.L += y;
+    c.out = decayed(em1, c.out) + b;
   }
 }
 
-template <class F, int W>
+// The states of a chunk, from the one that enters it, to memory.  Returns the last.
+template <class F, int S, bool NEAR, bool CARE>
+__device__ __forceinline__ float states(const Coefficients<S>& c, float h, const Stream<F, S, NEAR>& out, int64_t t,
+                                        int64_t st, uint32_t lane, uint32_t cut, uint32_t live) {
+#pragma unroll
+  for (int k = 0; k < S; ++k) {
+    if (CARE) h = keep(h, ~spread(cut, k));
+    h = decayed(c.em1[k], h) + c.b[k];
+    if (!CARE || (live >> k) & 1) out.store(F::put(h), t, k, st, lane);
+  }
+  return h;
+}
+
+// What a block's waves read: the three inputs of 64 channels of a row.
+template <class F, int S, bool NEAR>
+struct Inputs {
+  Stream<F, S, NEAR> x, ig, dg;
+  int64_t st[NEAR ? 1 : 3];  // bytes from a step to the next
+  const uint8_t* done;
+  int64_t done_step;
+  int lane;
+  uint32_t at;  // byte of the lane's column
+
+  __device__ __forceinline__ Inputs(const Args& p, int64_t e, int64_t d0, int lane_, uint32_t col)
+      : x(p.x, e, d0), ig(p.ig, e, d0), dg(p.dg, e, d0), done(p.done ? p.done + e * p.d_se : nullptr),
+        done_step(p.d_st), lane(lane_), at(col * (uint32_t)sizeof(typename F::E)) {
+    st[0] = p.dg.st * (int64_t)sizeof(typename F::E);
+    if constexpr (!NEAR) {
+      st[1] = p.ig.st * (int64_t)sizeof(typename F::E);
+      st[2] = p.x.st * (int64_t)sizeof(typename F::E);
+    }
+  }
+  __device__ __forceinline__ void load(Chunk<F, S>& c, int64_t t, int64_t end) const {
+    using At = Steps<S, NEAR>;
+    const At steps(st[0], t, end);
+    dg.load(c.dg, t, end, steps, at);
+    if constexpr (NEAR) {
+      ig.load(c.ig, t, end, steps, at);
+      x.load(c.x, t, end, steps, at);
+    } else {
+      ig.load(c.ig, t, end, At(st[1], t, end), at);
+      x.load(c.x, t, end, At(st[2], t, end), at);
+    }
+    c.flag = load_flag<S>(done, done_step, t, end, lane);
+  }
+};
+
+// The pair of each segment but the last: a wave takes a share of it, chunk after chunk.
+template <class F, int S, int W, bool NEAR>
+__global__ void __launch_bounds__(64 * W) fold_kernel(const Args p, uint32_t tiles) {
+  __shared__ float s_a[W][64], s_y[W][64];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t tile = blockIdx.x % tiles, es = blockIdx.x / tiles, nseg = (uint32_t)p.nseg;
+  const int64_t seg = es % (nseg - 1), e = es / (nseg - 1), d0 = tile * 64;
+  const bool column = d0 + lane < p.D;
+  const uint32_t col = column ? lane : (uint32_t)(p.D - 1 - d0);  // loads stay inside the row
+  const float rate2 = kLog2E * p.rate[d0 + col];
+  const Inputs<F, S, NEAR> in(p, e, d0, lane, col);
+  const int64_t share = p.seg_steps / W, begin = seg * p.seg_steps + w * share, end = begin + share;
+  float total = 0.0f, y = 0.0f;
+  bool dropped = false;
+  auto fold = [&](const Chunk<F, S>& c) __attribute__((always_inline)) {
+    const uint32_t cut = flag_word(c.flag);
+    Coefficients<S> k;
+    if (cut == 0) coefficients<F, S, false>(k, c, rate2, 0, 0);
+    else coefficients<F, S, true>(k, c, rate2, cut, (1u << S) - 1);
+    total += k.L;
+    dropped |= cut != 0;
+    y = enter(cut ? kDropped : exp2_fast(-k.L), k.out, y);
+  };
+  Chunk<F, S> one, two;
+  in.load(one, begin, end);
+  for (int64_t t = begin;;) {  // a share holds whole chunks
+    if (t + S < end) in.load(two, t + S, end);
+    fold(one);
+    t += S;
+    if (t >= end) break;
+    if (t + S < end) in.load(one, t + S, end);
+    fold(two);
+    t += S;
+    if (t >= end) break;
+  }
+  s_a[w][lane] = dropped ? kDropped : exp2_fast(-total);
+  s_y[w][lane] = y;
+  __syncthreads();
+  if (w == 0 && column) {
+    float A = 1.0f, out = 0.0f;
+    for (int u = 0; u < W; ++u) {
+      out = enter(s_a[u][lane], s_y[u][lane], out);
+      A = A < 0.0f || s_a[u][lane] < 0.0f ? kDropped : A * s_a[u][lane];
+    }
+    const int64_t at = (e * p.nseg + seg) * p.D + d0 + lane;
+    p.seg_a[at] = A;
+    p.seg_y[at] = out;
+  }
+}
+
+// One block: 64 channels of one row (or of one segment of it), W waves of S steps each at a
+// time, the next ones' loads in flight meanwhile.
+template <class F, int S, int W, bool NEAR>
+__global__ void __launch_bounds__(64 * W) forward_kernel(const Args p, uint32_t tiles) {
+  __shared__ Exchange<W> s;
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t tile = blockIdx.x % tiles, es = blockIdx.x / tiles, nseg = (uint32_t)p.nseg;
+  const int64_t seg = nseg - 1 - es % nseg, e = es / nseg, d0 = tile * 64;
+  const bool column = d0 + lane < p.D;
+  const uint32_t col = column ? lane : (uint32_t)(p.D - 1 - d0);  // loads stay inside the row
+  const float rate2 = kLog2E * p.rate[d0 + col];
+  const Inputs<F, S, NEAR> in(p, e, d0, lane, col);
+  const Stream<F, S, NEAR> out(p.out, e, d0);
+  const int64_t out_st = p.out.st * (int64_t)sizeof(typename F::E);
+  const uint32_t out_at = column ? in.at : kNoColumn;
+  const int64_t begin = seg * p.seg_steps;
+  const int64_t end = p.T < begin + p.seg_steps ? p.T : begin + p.seg_steps;
+  float* marks = p.marks ? p.marks + (e * ((p.T + kMark - 1) / kMark)) * p.D + d0 + lane : nullptr;
+
+  float carry = p.init ? p.init[e * p.D + d0 + col] : 0.0f;  // the state entering the W chunks at hand
+  for (int64_t u = 0; u < seg; ++u) {
+    const int64_t at = (e * p.nseg + u) * p.D + d0 + col;
+    carry = enter(p.seg_a[at], p.seg_y[at], carry);
+  }
+  if (W > 1) s.carry[0][lane] = carry;  // the same from every wave
+  int buf = 0;
+  auto take = [&](const Chunk<F, S>& c, int64_t t) __attribute__((always_inline)) {
+    const uint32_t cut = flag_word(c.flag), live = live_word<S>(t, end);
+    const bool care = cut != 0 || live != (1u << S) - 1;
+    Coefficients<S> k;
+    if (!care) coefficients<F, S, false>(k, c, rate2, 0, 0);
+    else coefficients<F, S, true>(k, c, rate2, cut, live);
+    float h = carry;  // the state entering this wave's chunk
+    if constexpr (W > 1) {
+      s.put(buf, w, lane, exp2_fast(-k.L), k.out, cut);
+      meet();
+      h = s.template entering<1>(buf, w, lane);
+    }
+    if (marks && column && live && t % kMark == 0) marks[t / kMark * p.D] = h;
+    if (!care) h = states<F, S, NEAR, false>(k, h, out, t, out_st, out_at, 0, 0);
+    else h = states<F, S, NEAR, true>(k, h, out, t, out_st, out_at, cut, live);
+    carry = h;
+    if constexpr (W > 1) {  // the last wave's state is what enters the chunks behind
+      buf ^= 1;
+      if (w == W - 1) s.carry[buf][lane] = h;
+    }
+  };
+  constexpr int64_t kStep = W * S;
+  const int64_t ahead = w * S;
+  if (begin < end) {
+    Chunk<F, S> one, two;
+    in.load(one, begin + ahead, end);
+    for (int64_t t = begin;;) {
+      if (t + kStep < end) in.load(two, t + kStep + ahead, end);
+      take(one, t + ahead);
+      t += kStep;
+      if (t >= end) break;
+      if (t + kStep < end) in.load(one, t + kStep + ahead, end);
+      take(two, t + ahead);
+      t += kStep;
+      if (t >= end) break;
+    }
+  }
+  // The state behind the row is the last wave's: its steps, or those past the end, which change nothing.
+  if (w == W - 1 && column && seg == nseg - 1 && p.final_state) {
+    const bool ended = in.done && p.T > 0 && in.done[(p.T - 1) * p.d_st] != 0;
+    p.final_state[e * p.D + d0 + lane] = ended ? 0.0f : carry;
+  }
+}
+
+template <class F, int S, int W, bool NEAR>
 static hipError_t forward_waves(const Args& a, hipStream_t st) {
   const int64_t tiles = (a.D + 63) / 64;
   if (a.nseg > 1) {
-    forward_kernel<F, W, true><<<dim3((unsigned)(a.E * (a.nseg - 1) * tiles)), 64 * W, 0, st>>>(a, tiles);
+    fold_kernel<F, S, W, NEAR><<<dim3((unsigned)(a.E * (a.nseg - 1) * tiles)), 64 * W, 0, st>>>(a, (uint32_t)tiles);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  forward_kernel<F, W, false><<<dim3((unsigned)(a.E * a.nseg * tiles)), 64 * W, 0, st>>>(a, tiles);
+  forward_kernel<F, S, W, NEAR><<<dim3((unsigned)(a.E * a.nseg * tiles)), 64 * W, 0, st>>>(a, (uint32_t)tiles);
   return hipGetLastError();
 }
 
 template <class F>
 static hipError_t forward_fmt(const Args& a, const Plan& p, hipStream_t st) {
+  constexpr int64_t es = sizeof(typename F::E);
+  const View *in[] = {&a.x, &a.ig, &a.dg}, *out[] = {&a.out};
+  if (!near_alike(in, 3, es) || !near_alike(out, 1, es)) return forward_waves<F, 8, kMaxWaves, false>(a, st);
   switch (p.waves) {
-    case 1: return forward_waves<F, 1>(a, st);
-    case 4: return forward_waves<F, 4>(a, st);
-    default: return forward_waves<F, 16>(a, st);
+    case 1: return forward_waves<F, 8, 1, true>(a, st);
+    case 4: return forward_waves<F, 8, 4, true>(a, st);
+    default: return forward_waves<F, 8, kMaxWaves, true>(a, st);
   }
 }
 
@@ -138,14 +246,14 @@ hipError_t launch_forward(rlscan_format f, const Args& a, const Plan& p, hipStre
 }
 
 // Waves of a block and segments of a row.
-Plan make_plan(rlscan_format, int64_t E, int64_t T, int64_t D, bool backward) {
+Plan make_plan(int64_t E, int64_t T, int64_t D, bool backward) {
   Plan p{};
   const int64_t tiles = E * ((D + 63) / 64);
-  p.waves = T <= kMark || tiles >= 4096 ? 1 : T <= 4 * kMark || tiles >= 1024 ? 4 : 16;
-  if (backward && p.waves == 16) p.waves = 8;
-  const int64_t unit = (int64_t)p.waves * kMark, units = (T + unit - 1) / unit;
-  int64_t want = tiles > 0 && tiles < 512 ? (512 + tiles - 1) / tiles : 1;
-  if (want > units / 4) want = units / 4;  // a segment costs one more pass over its inputs
+  p.waves = T <= kMark || tiles >= 4096 ? 1 : T <= 4 * kMark || tiles >= 1024 ? 4 : kMaxWaves;
+  // segments: whole super-tiles of the widest block, whatever the block is
+  const int64_t unit = (int64_t)kMaxWaves * kMark, units = (T + unit - 1) / unit;
+  int64_t want = tiles > 0 && tiles < 192 ? 256 / tiles : 1;
+  if (want > units / 2) want = units / 2;  // a segment costs one more pass over its inputs
   if (want < 1) want = 1;
   const int64_t per = units > 0 ? (units + want - 1) / want : 1;
   p.seg_steps = per * unit;

@@ -26,6 +26,8 @@ using logits::LF16;
 using logits::LF32;
 
 constexpr int kMark = RLSCAN_MARK_STEPS;  // steps from one marked state to the next
+constexpr int kMaxWaves = 16;              // of a block
+constexpr int kBackWaves = 128 / kMark;    // the same, of the gradients
 
 struct Args {
   View x, ig, dg;         // values and the two gates' logits (heads unused)
@@ -49,12 +51,12 @@ struct Args {
 };
 
 struct Plan {
-  int waves;           // of a block, each with kMark steps
+  int waves;           // of a block
   int64_t nseg, seg_steps, groups;
   int64_t seg, part;   // floats of one array
   int64_t floats;      // workspace in all
 };
-Plan make_plan(rlscan_format f, int64_t E, int64_t T, int64_t D, bool backward);
+Plan make_plan(int64_t E, int64_t T, int64_t D, bool backward);
 
 hipError_t launch_forward(rlscan_format f, const Args& a, const Plan& p, hipStream_t st);
 hipError_t launch_backward(rlscan_format f, const Args& a, const Plan& p, hipStream_t st);
@@ -79,16 +81,15 @@ __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.0f + exp2_fast(-kLog2E * z));
 }
 
-// exp(-s) - 1 for s >= 0: below a quarter the series (its next term is 2^-24 of the
-// value), above it 1 - exp(-s) >= 0.22 loses at most two bits.
-__device__ __forceinline__ float decay_less_1(float s) {
-  const float far = exp2_fast(-kLog2E * s) - 1.0f;
-  float p = __builtin_fmaf(s, 1.0f / 720.0f, -1.0f / 120.0f);
-  p = __builtin_fmaf(s, p, 1.0f / 24.0f);
-  p = __builtin_fmaf(s, p, -1.0f / 6.0f);
-  p = __builtin_fmaf(s, p, 0.5f);
-  p = __builtin_fmaf(s, p, -1.0f);
-  return s < 0.25f ? s * p : far;
+// a - 1 = 2^-y - 1 for y >= 0 (y: s in units of log 2).  Below a quarter a cubic times y,
+// fitted to (1 - 2^-y) / y by least largest relative error, 2^-24 of the value; above it
+// 1 - a >= 0.16 loses at most three bits.
+__device__ __forceinline__ float decay_less_1(float y) {
+  const float far = exp2_fast(-y) - 1.0f;
+  float p = __builtin_fmaf(y, 0.008974975906f, -0.055404357612f);
+  p = __builtin_fmaf(y, p, 0.240221500397f);
+  p = __builtin_fmaf(y, p, -0.693147122860f);
+  return y < 0.25f ? y * p : far;
 }
 // 1 - a^2 from a - 1
 __device__ __forceinline__ float one_less_square(float em1) { return -em1 * (2.0f + em1); }
@@ -96,10 +97,148 @@ __device__ __forceinline__ float one_less_square(float em1) { return -em1 * (2.0
 // a h from a - 1
 __device__ __forceinline__ float decayed(float em1, float h) { return __builtin_fmaf(em1, h, h); }
 
-// The pair of a chunk as the waves and segments exchange it: A is kDropped where the chunk
-// holds a cut, which takes any c, inf and NaN too, to y.
+// A segment's pair in the workspace: A is kDropped where it holds a cut, which takes any c, inf
+// and NaN too, to y.
 constexpr float kDropped = -1.0f;
 __device__ __forceinline__ float enter(float A, float y, float c) { return A < 0.0f ? y : __builtin_fmaf(A, c, y); }
+
+// ------------------------------------------------------------------ chunks of S steps
+// A wave holds 64 channels of S steps in registers.  Addresses are scalars and the lane's
+// column, so that a step costs no vector instructions but its arithmetic.
+
+// Bit k of a chunk's words, as a mask of 32 bits.  An AND with it takes inf and NaN to 0 too.
+__device__ __forceinline__ uint32_t spread(uint32_t word, int k) { return (uint32_t)((int32_t)(word << (31 - k)) >> 31); }
+__device__ __forceinline__ float keep(float x, uint32_t mask) {
+  return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x) & mask);
+}
+// x where the mask is set, else y
+__device__ __forceinline__ float pick(uint32_t mask, float x, float y) {
+  return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x) & mask) | (__builtin_bit_cast(uint32_t, y) & ~mask));
+}
+
+// The same value, of which the compiler knows nothing: keeps it from doing the work that both
+// forms of a branch begin with before the branch, where its results lie in registers for long.
+__device__ __forceinline__ float apart(float x) {
+  asm("" : "+v"(x));
+  return x;
+}
+__device__ __forceinline__ uint16_t apart(uint16_t x) {
+  uint32_t y = x;
+  asm("" : "+v"(y));
+  return (uint16_t)y;
+}
+
+// The steps of a chunk as offsets from its first: t + k, or the row's last step where that is past
+// the end.  Tensors of equal strides share them.  NEAR: 32-bit offsets of buffer instructions.
+template <int S, bool NEAR>
+struct Steps {
+  int64_t st;  // bytes from a step to the next
+  int last;
+  __device__ __forceinline__ Steps(int64_t st_, int64_t t, int64_t end)
+      : st(st_), last(end - t < S ? (end > t ? (int)(end - t) - 1 : 0) : S - 1) {}
+  __device__ __forceinline__ int64_t far(int k) const { return (k < last ? k : last) * st; }
+  __device__ __forceinline__ int near(int k) const { return (k < last ? k : last) * (int)st; }
+};
+
+// One [E, T, D] tensor at a row and a tile of columns.
+constexpr uint32_t kNoColumn = 0x80000000u;
+template <class F, int S, bool NEAR>
+struct Stream {
+  using E = typename F::E;
+  static constexpr int kNonTemporal = 2;
+  char* p;
+
+  __device__ __forceinline__ Stream(const View& v, int64_t e, int64_t column)
+      : p(static_cast<char*>(const_cast<void*>(v.p)) + (e * v.se + column) * (int64_t)sizeof(E)) {}
+  static __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(char* q) {
+    return __builtin_amdgcn_make_buffer_rsrc(q, 0, 0x7fffffff, 0x00020000);
+  }
+  // Steps [t, t + S) of the lane whose column is `lane` bytes behind the tile's first.
+  __device__ __forceinline__ void load(E (&x)[S], int64_t t, int64_t end, const Steps<S, NEAR>& steps, uint32_t lane) const {
+    char* const q = p + (t < end ? t : end - 1) * steps.st;
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      if constexpr (!NEAR) x[k] = *reinterpret_cast<const E*>(q + steps.far(k) + lane);
+      else if constexpr (sizeof(E) == 4)
+        x[k] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(resource(q), lane, steps.near(k), 0));
+      else x[k] = __builtin_amdgcn_raw_buffer_load_b16(resource(q), lane, steps.near(k), 0);
+    }
+  }
+  // Step t + k; lane: kNoColumn for one that has none, which a buffer instruction drops as out of range.
+  __device__ __forceinline__ void store(E v, int64_t t, int k, int64_t st, uint32_t lane) const {
+    char* const q = p + t * st;
+    if constexpr (!NEAR) {
+      if (lane != kNoColumn) *reinterpret_cast<E*>(q + k * st + lane) = v;
+    } else if constexpr (sizeof(E) == 4) {
+      __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), resource(q), lane, k * (int)st, kNonTemporal);
+    } else {
+      __builtin_amdgcn_raw_buffer_store_b16(v, resource(q), lane, k * (int)st, kNonTemporal);
+    }
+  }
+};
+
+// Whether tensors go by one stride, with a chunk within 2^31 bytes.
+inline bool near_alike(const View* const* v, int n, int64_t es) {
+  for (int i = 0; i < n; ++i)
+    if (v[i]->st != v[0]->st || v[i]->st * es >= (int64_t)1 << 27) return false;
+  return true;
+}
+
+// Bit k: step t + k starts anew; the lane's byte of `done` is loaded ahead.
+template <int S>
+__device__ __forceinline__ uint8_t load_flag(const uint8_t* done, int64_t step, int64_t t, int64_t end, int lane) {
+  const int64_t at = t + lane;
+  return done && lane < S && at > 0 && at < end ? done[(at - 1) * step] : 0;
+}
+__device__ __forceinline__ uint32_t flag_word(uint8_t flag) { return (uint32_t)__builtin_amdgcn_ballot_w64(flag != 0); }
+
+// Bit k: step t + k lies before the end.
+template <int S>
+__device__ __forceinline__ uint32_t live_word(int64_t t, int64_t end) {
+  const int64_t n = end - t;
+  return n >= S ? (1u << S) - 1 : n > 0 ? (1u << n) - 1 : 0;
+}
+
+// The block's barrier: LDS writes are done, loads and stores to memory stay in flight.
+__device__ __forceinline__ void meet() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// What the waves of a block tell each other of their chunks, twice: one set is written
+// while the other is read.
+template <int W>
+struct Exchange {
+  float a[2][W][64], y[2][W][64], carry[2][64];
+  uint32_t cut[2][W];
+
+  __device__ __forceinline__ void put(int buf, int w, int lane, float A, float out, uint32_t cut_word) {
+    a[buf][w][lane] = A;
+    y[buf][w][lane] = out;
+    if (lane == 0) cut[buf][w] = cut_word;
+  }
+  // What enters wave w's chunk from the chunks `before` it (STEP 1: lower waves, -1: higher ones).
+  // A wave with a cut takes anything to its y, so the walk begins behind the nearest of these.
+  template <int STEP>
+  __device__ __forceinline__ float entering(int buf, int w, int lane) const {
+    const uint32_t cuts = (uint32_t)__builtin_amdgcn_ballot_w64(lane < W && cut[buf][lane < W ? lane : 0] != 0);
+    float c = carry[buf][lane];
+    int u;
+    if constexpr (STEP > 0) {
+      const uint32_t mine = cuts & ((1u << w) - 1);
+      u = mine ? 31 - __builtin_clz(mine) : 0;
+      if (mine) c = y[buf][u++][lane];
+      for (; u < w; ++u) c = __builtin_fmaf(a[buf][u][lane], c, y[buf][u][lane]);
+    } else {
+      const uint32_t mine = cuts & ~((2u << w) - 1);
+      u = mine ? __builtin_ctz(mine) : W - 1;
+      if (mine) c = y[buf][u--][lane];
+      for (; u > w; --u) c = __builtin_fmaf(a[buf][u][lane], c, y[buf][u][lane]);
+    }
+    return c;
+  }
+};
 
 }  // namespace gr
 }  // namespace rlscan
