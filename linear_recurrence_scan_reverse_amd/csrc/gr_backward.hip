@@ -84,12 +84,12 @@ struct Tensors {
     dig_st = NEAR ? dx_st : p.dig.st * es;
     ddg_st = NEAR ? dx_st : p.ddg.st * es;
   }
-  __device__ __forceinline__ void load(Chunk<F, S>& c, int64_t t, int64_t end) const {
+  __device__ __forceinline__ void load(Chunk<F, S>& c, int t, int end) const {
     dg.load(c.dg, t, end, Steps<S, NEAR>(dg_st, t, end), at);
     g.load(c.g, t, end, Steps<S, NEAR>(g_st, t, end), at);
     c.flag = load_flag<S>(done, done_step, t, end, lane);
   }
-  __device__ __forceinline__ void load(Rest<F, S>& c, int64_t t, int64_t end) const {
+  __device__ __forceinline__ void load(Rest<F, S>& c, int t, int end) const {
     c.mark = marks[(t < end ? t : end - 1) / kMark * mark_step];
     ig.load(c.ig, t, end, Steps<S, NEAR>(ig_st, t, end), at);
     x.load(c.x, t, end, Steps<S, NEAR>(x_st, t, end), at);
@@ -99,7 +99,7 @@ struct Tensors {
 // The gradients of a chunk, from the e that enters it, to memory; returns the e that leaves it.
 template <class F, int S, bool NEAR, bool CARE>
 __device__ __forceinline__ float gradients(const Decays<S>& c, const Chunk<F, S>& in, const Rest<F, S>& rest, float e,
-                                           float rate, float& d_rate, const Tensors<F, S, NEAR>& to, int64_t t,
+                                           float rate, float& d_rate, const Tensors<F, S, NEAR>& to, int t,
                                            uint32_t out_at, uint32_t cut, uint32_t live) {
   float before[S], u[S], si[S];
   float h = rest.mark;
@@ -147,8 +147,8 @@ __global__ void __launch_bounds__(64 * W) fold_back_kernel(const Args p, uint32_
   const uint32_t col = column ? lane : (uint32_t)(p.D - 1 - d0);  // loads stay inside the row
   const float rate2 = kLog2E * p.rate[d0 + col];
   const Tensors<F, S, NEAR> in(p, e, d0, lane, col);
-  const int64_t share = p.seg_steps / W, begin = seg * p.seg_steps + w * share;
-  const int64_t end = p.T < begin + share ? p.T : begin + share;  // the last segment may be short
+  const int share = (int)p.seg_steps / W, begin = (int)seg * (int)p.seg_steps + w * share;
+  const int end = (int)p.T < begin + share ? (int)p.T : begin + share;  // the last segment may be short
   float total = 0.0f, y = 0.0f;
   bool dropped = false;
   auto fold = [&](const Chunk<F, S>& c, uint32_t live) __attribute__((always_inline)) {
@@ -162,14 +162,14 @@ __global__ void __launch_bounds__(64 * W) fold_back_kernel(const Args p, uint32_
   };
   if (begin < end) {
     Chunk<F, S> one, two;
-    int64_t t = begin + (end - begin - 1) / S * S;
+    int t = begin + (end - begin - 1) / S * S;
     in.load(one, t, end);
     for (;;) {
-      if (t > begin) in.load(two, t - S, end);
+      in.load(two, t > begin ? t - S : begin, end);
       fold(one, live_word<S>(t, end));
       if (t == begin) break;
       t -= S;
-      if (t > begin) in.load(one, t - S, end);
+      in.load(one, t > begin ? t - S : begin, end);
       fold(two, (1u << S) - 1);
       if (t == begin) break;
       t -= S;
@@ -203,10 +203,10 @@ __global__ void __launch_bounds__(64 * W) backward_kernel(const Args p, uint32_t
   const bool column = d0 + lane < p.D;
   const uint32_t col = column ? lane : (uint32_t)(p.D - 1 - d0);  // loads stay inside the row
   const float rate = p.rate[d0 + col], rate2 = kLog2E * rate;
-  const int64_t begin = seg * p.seg_steps;
-  const int64_t end = p.T < begin + p.seg_steps ? p.T : begin + p.seg_steps;
-  constexpr int64_t kStep = W * S;
-  const int64_t ahead = w * S;
+  const int begin = (int)seg * (int)p.seg_steps;
+  const int end = (int)(p.T < begin + p.seg_steps ? p.T : begin + p.seg_steps);
+  constexpr int kStep = W * S;
+  const int ahead = w * S;
   float d_rate = 0.0f;
   int buf = 0;
   for (int64_t e = group; e < p.E; e += p.groups) {
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(64 * W) backward_kernel(const Args p, uint32_t
       meet();  // the row before has been read
       s.carry[buf][lane] = carry;  // the same from every wave
     }
-    auto take = [&](const Chunk<F, S>& c, const Rest<F, S>& rest, int64_t t) __attribute__((always_inline)) {
+    auto take = [&](const Chunk<F, S>& c, const Rest<F, S>& rest, int t) __attribute__((always_inline)) {
       const uint32_t cut = flag_word(c.flag), live = live_word<S>(t, end);
       const bool care = cut != 0 || live != (1u << S) - 1;
       Decays<S> k;
@@ -245,16 +245,16 @@ __global__ void __launch_bounds__(64 * W) backward_kernel(const Args p, uint32_t
     if (begin < end) {
       Chunk<F, S> one, two;
       Rest<F, S> rest;
-      int64_t t = begin + (end - begin - 1) / kStep * kStep;
+      int t = begin + (end - begin - 1) / kStep * kStep;
       in.load(one, t + ahead, end);
       for (;;) {
         in.load(rest, t + ahead, end);
-        if (t > begin) in.load(two, t - kStep + ahead, end);
+        in.load(two, (t > begin ? t - kStep : begin) + ahead, end);
         take(one, rest, t + ahead);
         if (t == begin) break;
         t -= kStep;
         in.load(rest, t + ahead, end);
-        if (t > begin) in.load(one, t - kStep + ahead, end);
+        in.load(one, (t > begin ? t - kStep : begin) + ahead, end);
         take(two, rest, t + ahead);
         if (t == begin) break;
         t -= kStep;
@@ -284,7 +284,7 @@ static hipError_t backward_waves(const Args& a, hipStream_t st) {
   backward_kernel<F, S, W, NEAR><<<dim3((unsigned)(a.groups * a.nseg * tiles)), 64 * W, 0, st>>>(a, (uint32_t)tiles);
   e = hipGetLastError();
   if (e != hipSuccess || !a.rate_part) return e;
-  return sums::launch_columns(a.rate_part, a.groups * a.nseg, a.d_rate, a.D, nullptr, 0, st);
+  return sums::launch_columns(a.rate_part, a.groups * a.nseg, a.rate_more, a.d_rate, a.D, nullptr, 0, st);
 }
 
 template <class F>

@@ -1,5 +1,6 @@
 // The gated recurrence over whole rows (rlscan_gated_recurrence).
 #include "rlscan_gr.hpp"
+#include "rlscan_sums.hpp"
 
 namespace rlscan {
 namespace gr {
@@ -46,7 +47,7 @@ __device__ __forceinline__ void coefficients(Coefficients<S>& c, const Chunk<F, 
 
 // The states of a chunk, from the one that enters it, to memory.  Returns the last.
 template <class F, int S, bool NEAR, bool CARE>
-__device__ __forceinline__ float states(const Coefficients<S>& c, float h, const Stream<F, S, NEAR>& out, int64_t t,
+__device__ __forceinline__ float states(const Coefficients<S>& c, float h, const Stream<F, S, NEAR>& out, int t,
                                         int64_t st, uint32_t lane, uint32_t cut, uint32_t live) {
 #pragma unroll
   for (int k = 0; k < S; ++k) {
@@ -76,7 +77,7 @@ struct Inputs {
       st[2] = p.x.st * (int64_t)sizeof(typename F::E);
     }
   }
-  __device__ __forceinline__ void load(Chunk<F, S>& c, int64_t t, int64_t end) const {
+  __device__ __forceinline__ void load(Chunk<F, S>& c, int t, int end) const {
     using At = Steps<S, NEAR>;
     const At steps(st[0], t, end);
     dg.load(c.dg, t, end, steps, at);
@@ -103,7 +104,7 @@ __global__ void __launch_bounds__(64 * W) fold_kernel(const Args p, uint32_t til
   const uint32_t col = column ? lane : (uint32_t)(p.D - 1 - d0);  // loads stay inside the row
   const float rate2 = kLog2E * p.rate[d0 + col];
   const Inputs<F, S, NEAR> in(p, e, d0, lane, col);
-  const int64_t share = p.seg_steps / W, begin = seg * p.seg_steps + w * share, end = begin + share;
+  const int share = (int)p.seg_steps / W, begin = (int)seg * (int)p.seg_steps + w * share, end = begin + share;
   float total = 0.0f, y = 0.0f;
   bool dropped = false;
   auto fold = [&](const Chunk<F, S>& c) __attribute__((always_inline)) {
@@ -117,12 +118,12 @@ __global__ void __launch_bounds__(64 * W) fold_kernel(const Args p, uint32_t til
   };
   Chunk<F, S> one, two;
   in.load(one, begin, end);
-  for (int64_t t = begin;;) {  // a share holds whole chunks
-    if (t + S < end) in.load(two, t + S, end);
+  for (int t = begin;;) {  // a share holds whole chunks
+    in.load(two, t + S, end);
     fold(one);
     t += S;
     if (t >= end) break;
-    if (t + S < end) in.load(one, t + S, end);
+    in.load(one, t + S, end);
     fold(two);
     t += S;
     if (t >= end) break;
@@ -158,8 +159,8 @@ __global__ void __launch_bounds__(64 * W) forward_kernel(const Args p, uint32_t 
   const Stream<F, S, NEAR> out(p.out, e, d0);
   const int64_t out_st = p.out.st * (int64_t)sizeof(typename F::E);
   const uint32_t out_at = column ? in.at : kNoColumn;
-  const int64_t begin = seg * p.seg_steps;
-  const int64_t end = p.T < begin + p.seg_steps ? p.T : begin + p.seg_steps;
+  const int begin = (int)seg * (int)p.seg_steps;
+  const int end = (int)(p.T < begin + p.seg_steps ? p.T : begin + p.seg_steps);
   float* marks = p.marks ? p.marks + (e * ((p.T + kMark - 1) / kMark)) * p.D + d0 + lane : nullptr;
 
   float carry = p.init ? p.init[e * p.D + d0 + col] : 0.0f;  // the state entering the W chunks at hand
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(64 * W) forward_kernel(const Args p, uint32_t 
   }
   if (W > 1) s.carry[0][lane] = carry;  // the same from every wave
   int buf = 0;
-  auto take = [&](const Chunk<F, S>& c, int64_t t) __attribute__((always_inline)) {
+  auto take = [&](const Chunk<F, S>& c, int t) __attribute__((always_inline)) {
     const uint32_t cut = flag_word(c.flag), live = live_word<S>(t, end);
     const bool care = cut != 0 || live != (1u << S) - 1;
     Coefficients<S> k;
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(64 * W) forward_kernel(const Args p, uint32_t 
       meet();
       h = s.template entering<1>(buf, w, lane);
     }
-    if (marks && column && live && t % kMark == 0) marks[t / kMark * p.D] = h;
+    if (marks && column && live && t % kMark == 0) marks[(int64_t)(t / kMark) * p.D] = h;
     if (!care) h = states<F, S, NEAR, false>(k, h, out, t, out_st, out_at, 0, 0);
     else h = states<F, S, NEAR, true>(k, h, out, t, out_st, out_at, cut, live);
     carry = h;
@@ -190,17 +191,17 @@ __global__ void __launch_bounds__(64 * W) forward_kernel(const Args p, uint32_t 
       if (w == W - 1) s.carry[buf][lane] = h;
     }
   };
-  constexpr int64_t kStep = W * S;
-  const int64_t ahead = w * S;
+  constexpr int kStep = W * S;
+  const int ahead = w * S;
   if (begin < end) {
     Chunk<F, S> one, two;
     in.load(one, begin + ahead, end);
-    for (int64_t t = begin;;) {
-      if (t + kStep < end) in.load(two, t + kStep + ahead, end);
+    for (int t = begin;;) {
+      in.load(two, t + kStep + ahead, end);
       take(one, t + ahead);
       t += kStep;
       if (t >= end) break;
-      if (t + kStep < end) in.load(one, t + kStep + ahead, end);
+      in.load(one, t + kStep + ahead, end);
       take(two, t + ahead);
       t += kStep;
       if (t >= end) break;
@@ -264,8 +265,9 @@ Plan make_plan(int64_t E, int64_t T, int64_t D, bool backward) {
     const int64_t columns = (D + 63) / 64, most = 8192 / (columns * p.nseg) + 1;
     if (p.groups > most) p.groups = most;
     p.part = p.groups * p.nseg > 1 ? (p.groups * p.nseg * D + 3) / 4 * 4 : 0;
+    p.more = sums::more_floats(p.groups * p.nseg, D);
   }
-  p.floats = 2 * p.seg + p.part;
+  p.floats = 2 * p.seg + p.part + p.more;
   return p;
 }
 

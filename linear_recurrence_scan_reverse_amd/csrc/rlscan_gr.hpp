@@ -45,6 +45,7 @@ struct Args {
   float* seg_y;
   float* d_rate;          // [D]
   float* rate_part;       // workspace [groups * nseg, D]
+  float* rate_more;       // workspace of the sum of rate_part's rows
   int64_t E, T, D;
   int64_t nseg, seg_steps;  // steps of a segment, a multiple of what a block takes at once
   int64_t groups;           // backward: blocks take the rows e, e + groups, ...
@@ -53,7 +54,7 @@ struct Args {
 struct Plan {
   int waves;           // of a block
   int64_t nseg, seg_steps, groups;
-  int64_t seg, part;   // floats of one array
+  int64_t seg, part, more;  // floats of one array
   int64_t floats;      // workspace in all
 };
 Plan make_plan(int64_t E, int64_t T, int64_t D, bool backward);
@@ -134,8 +135,8 @@ template <int S, bool NEAR>
 struct Steps {
   int64_t st;  // bytes from a step to the next
   int last;
-  __device__ __forceinline__ Steps(int64_t st_, int64_t t, int64_t end)
-      : st(st_), last(end - t < S ? (end > t ? (int)(end - t) - 1 : 0) : S - 1) {}
+  __device__ __forceinline__ Steps(int64_t st_, int t, int end)
+      : st(st_), last(end - t < S ? (end > t ? end - t - 1 : 0) : S - 1) {}
   __device__ __forceinline__ int64_t far(int k) const { return (k < last ? k : last) * st; }
   __device__ __forceinline__ int near(int k) const { return (k < last ? k : last) * (int)st; }
 };
@@ -154,7 +155,7 @@ struct Stream {
     return __builtin_amdgcn_make_buffer_rsrc(q, 0, 0x7fffffff, 0x00020000);
   }
   // Steps [t, t + S) of the lane whose column is `lane` bytes behind the tile's first.
-  __device__ __forceinline__ void load(E (&x)[S], int64_t t, int64_t end, const Steps<S, NEAR>& steps, uint32_t lane) const {
+  __device__ __forceinline__ void load(E (&x)[S], int t, int end, const Steps<S, NEAR>& steps, uint32_t lane) const {
     char* const q = p + (t < end ? t : end - 1) * steps.st;
 #pragma unroll
     for (int k = 0; k < S; ++k) {
@@ -165,7 +166,7 @@ struct Stream {
     }
   }
   // Step t + k; lane: kNoColumn for one that has none, which a buffer instruction drops as out of range.
-  __device__ __forceinline__ void store(E v, int64_t t, int k, int64_t st, uint32_t lane) const {
+  __device__ __forceinline__ void store(E v, int t, int k, int64_t st, uint32_t lane) const {
     char* const q = p + t * st;
     if constexpr (!NEAR) {
       if (lane != kNoColumn) *reinterpret_cast<E*>(q + k * st + lane) = v;
@@ -184,18 +185,22 @@ inline bool near_alike(const View* const* v, int n, int64_t es) {
   return true;
 }
 
-// Bit k: step t + k starts anew; the lane's byte of `done` is loaded ahead.
+// Bit k: step t + k starts anew; the lane's byte of `done` is loaded ahead.  Out of range, which reads
+// as 0, is what lies outside the row, and everything where there are no flags: the load is always made,
+// since behind one that may not have been made the compiler waits for all of them.
 template <int S>
-__device__ __forceinline__ uint8_t load_flag(const uint8_t* done, int64_t step, int64_t t, int64_t end, int lane) {
-  const int64_t at = t + lane;
-  return done && lane < S && at > 0 && at < end ? done[(at - 1) * step] : 0;
+__device__ __forceinline__ uint8_t load_flag(const uint8_t* done, int64_t step, int t, int end, int lane) {
+  const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(done) + (t - 1) * step, 0,
+                                                    done ? 0x7fffffff : 0, 0x00020000);
+  const bool in = lane < S && t + lane > 0 && t + lane < end;  // a row's steps lie at most 2^22 bytes apart
+  return __builtin_amdgcn_raw_buffer_load_b8(rs, in ? lane * (int)step : (int)kNoColumn, 0, 0);
 }
 __device__ __forceinline__ uint32_t flag_word(uint8_t flag) { return (uint32_t)__builtin_amdgcn_ballot_w64(flag != 0); }
 
 // Bit k: step t + k lies before the end.
 template <int S>
-__device__ __forceinline__ uint32_t live_word(int64_t t, int64_t end) {
-  const int64_t n = end - t;
+__device__ __forceinline__ uint32_t live_word(int t, int end) {
+  const int n = end - t;
   return n >= S ? (1u << S) - 1 : n > 0 ? (1u << n) - 1 : 0;
 }
 
@@ -224,17 +229,27 @@ struct Exchange {
   __device__ __forceinline__ float entering(int buf, int w, int lane) const {
     const uint32_t cuts = (uint32_t)__builtin_amdgcn_ballot_w64(lane < W && cut[buf][lane < W ? lane : 0] != 0);
     float c = carry[buf][lane];
-    int u;
-    if constexpr (STEP > 0) {
-      const uint32_t mine = cuts & ((1u << w) - 1);
-      u = mine ? 31 - __builtin_clz(mine) : 0;
-      if (mine) c = y[buf][u++][lane];
-      for (; u < w; ++u) c = __builtin_fmaf(a[buf][u][lane], c, y[buf][u][lane]);
-    } else {
-      const uint32_t mine = cuts & ~((2u << w) - 1);
-      u = mine ? __builtin_ctz(mine) : W - 1;
-      if (mine) c = y[buf][u--][lane];
-      for (; u > w; --u) c = __builtin_fmaf(a[buf][u][lane], c, y[buf][u][lane]);
+    const uint32_t mine = STEP > 0 ? cuts & ((1u << w) - 1) : cuts & ~((2u << w) - 1);
+    const int near = STEP > 0 ? 31 - __builtin_clz(mine | 1) : __builtin_ctz(mine | (1u << (W - 1)));
+    const int from = mine ? near : STEP > 0 ? 0 : W - 1;
+    // Eight pairs are asked for at once: one after the other their latencies would add up.
+    constexpr int B = W < 8 ? W : 8;
+#pragma unroll
+    for (int half = 0; half < W / B; ++half) {
+      const int base = STEP > 0 ? half * B : W - B - half * B;
+      if (STEP > 0 ? base + B <= from || base >= w : base > from || base + B - 1 <= w) continue;
+      float A[B], Y[B];
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        A[i] = a[buf][base + i][lane];
+        Y[i] = y[buf][base + i][lane];
+      }
+#pragma unroll
+      for (int j = 0; j < B; ++j) {
+        const int i = STEP > 0 ? j : B - 1 - j, u = base + i;
+        if (mine && u == from) c = Y[i];
+        else if (STEP > 0 ? u >= from && u < w : u <= from && u > w) c = __builtin_fmaf(A[i], c, Y[i]);
+      }
     }
     return c;
   }
