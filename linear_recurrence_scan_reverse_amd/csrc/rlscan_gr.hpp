@@ -151,18 +151,19 @@ struct Stream {
 
   __device__ __forceinline__ Stream(const View& v, int64_t e, int64_t column)
       : p(static_cast<char*>(const_cast<void*>(v.p)) + (e * v.se + column) * (int64_t)sizeof(E)) {}
-  static __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(char* q) {
-    return __builtin_amdgcn_make_buffer_rsrc(q, 0, 0x7fffffff, 0x00020000);
+  static __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(char* q, bool some = true) {
+    return __builtin_amdgcn_make_buffer_rsrc(q, 0, some ? 0x7fffffff : 0, 0x00020000);
   }
-  // Steps [t, t + S) of the lane whose column is `lane` bytes behind the tile's first.
+  // Steps [t, t + S) of the lane whose column is `lane` bytes behind the tile's first.  A chunk that
+  // lies past the end altogether is asked for out of range, which reads no memory.
   __device__ __forceinline__ void load(E (&x)[S], int t, int end, const Steps<S, NEAR>& steps, uint32_t lane) const {
     char* const q = p + (t < end ? t : end - 1) * steps.st;
 #pragma unroll
     for (int k = 0; k < S; ++k) {
       if constexpr (!NEAR) x[k] = *reinterpret_cast<const E*>(q + steps.far(k) + lane);
       else if constexpr (sizeof(E) == 4)
-        x[k] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(resource(q), lane, steps.near(k), 0));
-      else x[k] = __builtin_amdgcn_raw_buffer_load_b16(resource(q), lane, steps.near(k), 0);
+        x[k] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(resource(q, t < end), lane, steps.near(k), 0));
+      else x[k] = __builtin_amdgcn_raw_buffer_load_b16(resource(q, t < end), lane, steps.near(k), 0);
     }
   }
   // Step t + k; lane: kNoColumn for one that has none, which a buffer instruction drops as out of range.
