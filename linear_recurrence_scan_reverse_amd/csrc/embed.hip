@@ -16,20 +16,35 @@ using logits::LBf16;
 using logits::LF16;
 using logits::LF32;
 
-// V elements as they lie in memory: 16 bytes, or one element.
+// V elements as they lie in memory: 16, 8 or 4 bytes, or one element of 2.
+template <int kBytes>
+struct WordOf;
+template <>
+struct WordOf<16> {
+  using T = logits::u32x4;
+};
+template <>
+struct WordOf<8> {
+  using T = uint64_t;
+};
+template <>
+struct WordOf<4> {
+  using T = uint32_t;
+};
+template <>
+struct WordOf<2> {
+  using T = uint16_t;
+};
 template <class F, int V>
 struct Piece {
+  using Word = typename WordOf<V * (int)sizeof(typename F::E)>::T;
   typename F::E e[V];
 };
 template <class F, int V>
 __device__ __forceinline__ Piece<F, V> load_piece(const typename F::E* p) {
   Piece<F, V> r;
-  if constexpr (V == 1) {
-    r.e[0] = *p;
-  } else {
-    const logits::u32x4 v = *reinterpret_cast<const logits::u32x4*>(p);
-    __builtin_memcpy(&r, &v, 16);
-  }
+  const typename Piece<F, V>::Word v = *reinterpret_cast<const typename Piece<F, V>::Word*>(p);
+  __builtin_memcpy(&r, &v, sizeof(v));
   return r;
 }
 template <class F, int V>
@@ -37,49 +52,63 @@ __device__ __forceinline__ void store_piece(typename F::E* p, const float (&x)[V
   Piece<F, V> r;
 #pragma unroll
   for (int i = 0; i < V; ++i) r.e[i] = F::put(x[i]);
-  if constexpr (V == 1) {
-    *p = r.e[0];
-  } else {
-    logits::u32x4 v;
-    __builtin_memcpy(&v, &r, 16);
-    *reinterpret_cast<logits::u32x4*>(p) = v;
-  }
+  typename Piece<F, V>::Word v;
+  __builtin_memcpy(&v, &r, sizeof(v));
+  *reinterpret_cast<typename Piece<F, V>::Word*>(p) = v;
+}
+// The widest piece, of at most 16 bytes, that rows of D elements at these addresses and strides are made of.
+static int piece_of(const void* a, int64_t sa, const void* b, int64_t sb, int64_t D, int es) {
+  int v = 16 / es;
+  while (v > 1 && (D % v || (uintptr_t)a % (uintptr_t)(v * es) || (uintptr_t)b % (uintptr_t)(v * es) || sa % v || sb % v))
+    v /= 2;
+  return v;
 }
 
-// A wave takes 64 V columns of one token.
+constexpr int kLookups = 4;  // tokens to a wave, whose rows are asked for together
+
+// A wave takes 64 V columns of kLookups tokens.
 template <class F, int V>
-__global__ void __launch_bounds__(256) lookup_kernel(const LookupArgs p, int64_t tiles) {
+__global__ void __launch_bounds__(256) lookup_kernel(const LookupArgs p, uint32_t tiles) {
   using E = typename F::E;
-  const int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int64_t r = u / tiles, d = (u - r * tiles) * 64 * V + (threadIdx.x & 63) * V;
-  if (r >= p.R || d >= p.D) return;
-  const int64_t n = p.tokens[r];
-  float x[V];
+  const uint32_t u = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t r0 = (int64_t)(u / tiles) * kLookups, d = (int64_t)(u % tiles) * 64 * V + (threadIdx.x & 63) * V;
+  if (r0 >= p.R || d >= p.D) return;
+  int64_t n[kLookups];
+  Piece<F, V> w[kLookups];
 #pragma unroll
-  for (int i = 0; i < V; ++i) x[i] = 0.0f;
-  if (n >= 0 && n < p.N) {
-    const Piece<F, V> w = load_piece<F, V>(static_cast<const E*>(p.table) + n * p.t_stride + d);
+  for (int i = 0; i < kLookups; ++i) n[i] = r0 + i < p.R ? p.tokens[r0 + i] : -1;
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = p.scale * F::get(w.e[i]);
+  for (int i = 0; i < kLookups; ++i) {
+    const bool in = n[i] >= 0 && n[i] < p.N;
+    w[i] = load_piece<F, V>(static_cast<const E*>(p.table) + (in ? n[i] : 0) * p.t_stride + d);
+    if (!in) w[i] = Piece<F, V>{};
   }
-  store_piece<F, V>(static_cast<E*>(p.out) + r * p.o_stride + d, x);
+#pragma unroll
+  for (int i = 0; i < kLookups; ++i) {
+    float x[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] = p.scale * F::get(w[i].e[j]);
+    if (r0 + i < p.R) store_piece<F, V>(static_cast<E*>(p.out) + (r0 + i) * p.o_stride + d, x);
+  }
 }
 
-static bool wide(const void* a, int64_t sa, const void* b, int64_t sb, int64_t D, int V, int es) {
-  return D % V == 0 && (uintptr_t)a % 16 == 0 && (uintptr_t)b % 16 == 0 && sa * es % 16 == 0 && sb * es % 16 == 0;
+template <class F, int V>
+static hipError_t lookup_of(const LookupArgs& a, hipStream_t st) {
+  const int64_t tiles = (a.D + 64 * V - 1) / (64 * V), units = (a.R + kLookups - 1) / kLookups * tiles;
+  lookup_kernel<F, V><<<dim3((unsigned)((units + 3) / 4)), 256, 0, st>>>(a, (uint32_t)tiles);
+  return hipGetLastError();
 }
 
 template <class F>
 static hipError_t lookup_fmt(const LookupArgs& a, hipStream_t st) {
-  constexpr int V = F::W, es = sizeof(typename F::E);
-  if (wide(a.table, a.t_stride, a.out, a.o_stride, a.D, V, es)) {
-    const int64_t tiles = (a.D + 64 * V - 1) / (64 * V);
-    lookup_kernel<F, V><<<dim3((unsigned)((a.R * tiles + 3) / 4)), 256, 0, st>>>(a, tiles);
-  } else {
-    const int64_t tiles = (a.D + 63) / 64;
-    lookup_kernel<F, 1><<<dim3((unsigned)((a.R * tiles + 3) / 4)), 256, 0, st>>>(a, tiles);
+  switch (piece_of(a.table, a.t_stride, a.out, a.o_stride, a.D, sizeof(typename F::E))) {
+    case 8:
+      if constexpr (F::W == 8) return lookup_of<F, 8>(a, st);
+      break;
+    case 4: return lookup_of<F, 4>(a, st);
+    case 2: return lookup_of<F, 2>(a, st);
   }
-  return hipGetLastError();
+  return lookup_of<F, 1>(a, st);
 }
 
 hipError_t launch_lookup(rlscan_format f, const LookupArgs& a, hipStream_t st) {
@@ -97,11 +126,11 @@ constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 struct SortArgs {
   const int64_t* tokens;
   int32_t *key_a, *at_a, *key_b, *at_b;  // by the first digit, and by both
-  int32_t* hist;      // [blocks, kBins], of the pass at hand
+  int32_t *hist_a, *hist_b;              // [blocks, kBins], of either pass
   int32_t* valid;     // how many tokens are in range
   uint8_t* present;   // [N]: whether a row has a token
   int64_t R, N, per;
-  int blocks, shift, bits;
+  int blocks, passes, bits[2];
 };
 
 // The token at place i of a pass's input, or -1.
@@ -113,40 +142,52 @@ __device__ __forceinline__ int32_t key_at(const SortArgs& p, int64_t i, int64_t 
   return t >= 0 && t < p.N ? (int32_t)t : -1;
 }
 
-// How often each digit stands in a block's share; the first pass also clears `present`.
-template <bool FIRST>
+// The lanes whose key has the same bits [from, from + bits); only those with a key.
+__device__ __forceinline__ uint64_t alike(uint64_t among, int32_t key, int from, int bits) {
+  for (int b = from; b < from + bits; ++b) {
+    const uint64_t set = __ballot((key >> b) & 1);
+    among &= (key >> b) & 1 ? set : ~set;
+  }
+  return among;
+}
+
+// How often each first digit stands in a block's share; also clears `present` and the second pass's counts.
 __global__ void __launch_bounds__(kSortThreads) count_kernel(const SortArgs p) {
   __shared__ int32_t bins[kBins];
   const int tid = threadIdx.x;
   bins[tid] = 0;
-  if (FIRST) {
-    for (int64_t n = (int64_t)blockIdx.x * kSortThreads + tid; n < p.N; n += (int64_t)p.blocks * kSortThreads)
-      p.present[n] = 0;
-  }
+  p.hist_b[blockIdx.x * kBins + tid] = 0;
+  for (int64_t n = (int64_t)blockIdx.x * kSortThreads + tid; n < p.N; n += (int64_t)p.blocks * kSortThreads)
+    p.present[n] = 0;
   __syncthreads();
-  const int64_t n = FIRST ? p.R : (int64_t)*p.valid;
-  const int64_t lo = blockIdx.x * p.per, hi = lo + p.per < n ? lo + p.per : n;
+  const int64_t lo = blockIdx.x * p.per, hi = lo + p.per < p.R ? lo + p.per : p.R;
   for (int64_t i = lo + tid; i < hi; i += kSortThreads) {
-    const int32_t key = key_at<FIRST>(p, i, hi);
-    if (key >= 0) atomicAdd(&bins[(key >> p.shift) & (kBins - 1) & ((1 << p.bits) - 1)], 1);
+    const int32_t key = key_at<true>(p, i, hi);
+    if (key >= 0) atomicAdd(&bins[key & ((1 << p.bits[0]) - 1)], 1);
   }
   __syncthreads();
-  p.hist[blockIdx.x * kBins + tid] = bins[tid];
+  p.hist_a[blockIdx.x * kBins + tid] = bins[tid];
 }
 
 // Places a block's share by its digit: behind the smaller digits, behind the same digit in
-// earlier blocks and waves, and in the order of the share.
+// earlier blocks and waves, and in the order of the share.  The first pass counts, where its tokens go,
+// the second's digits: whole numbers, whose sums do not depend on their order.
 template <bool FIRST>
 __global__ void __launch_bounds__(kSortThreads) place_kernel(const SortArgs p) {
   __shared__ int32_t at[kSortWaves][kBins];
   __shared__ int32_t sums[kSortWaves];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int shift = FIRST ? 0 : p.bits[0], bits = p.bits[FIRST ? 0 : 1];
+  const int32_t* const hist = FIRST ? p.hist_a : p.hist_b;
   const int64_t n = FIRST ? p.R : (int64_t)*p.valid;
   int32_t before = 0, total = 0;
-  for (int b = 0; b < p.blocks; ++b) {
-    const int32_t c = p.hist[b * kBins + tid];
-    before += b < (int)blockIdx.x ? c : 0;
-    total += c;
+  if (tid < 1 << bits) {
+#pragma unroll 16
+    for (int b = 0; b < p.blocks; ++b) {
+      const int32_t c = hist[b * kBins + tid];
+      before += b < (int)blockIdx.x ? c : 0;
+      total += c;
+    }
   }
   int32_t run = total;  // inclusive sums over the bins: in the wave, then over the waves
   for (int o = 1; o < 64; o *= 2) {
@@ -154,6 +195,7 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const SortArgs p) {
     run += lane >= o ? v : 0;
   }
   if (lane == 63) sums[w] = run;
+#pragma unroll
   for (int v = 0; v < kSortWaves; ++v) at[v][tid] = 0;
   __syncthreads();
   int32_t base = run - total + before;
@@ -166,12 +208,13 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const SortArgs p) {
   const int64_t share = p.per / kSortWaves;  // a multiple of 64
   const int64_t first = blockIdx.x * p.per + w * share;
   const int64_t end = first + share < n ? first + share : n;
-  const int32_t mask = (1 << p.bits) - 1;
+  const int32_t mask = (1 << bits) - 1;
   for (int64_t i = first; i < end; i += 64) {
     const int32_t key = key_at<FIRST>(p, i + lane, end);
-    if (key >= 0) atomicAdd(&at[w][(key >> p.shift) & mask], 1);
+    if (key >= 0) atomicAdd(&at[w][(key >> shift) & mask], 1);
   }
   __syncthreads();
+#pragma unroll
   for (int v = 0; v < kSortWaves; ++v) {
     const int32_t c = at[v][tid];
     at[v][tid] = base;
@@ -180,12 +223,11 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const SortArgs p) {
   __syncthreads();
   for (int64_t i = first; i < end; i += 64) {
     const int32_t key = key_at<FIRST>(p, i + lane, end);
-    const int32_t digit = (key >> p.shift) & mask;
-    uint64_t same = __ballot(key >= 0);
-    for (int b = 0; b < p.bits; ++b) {
-      const uint64_t set = __ballot((digit >> b) & 1);
-      same &= (digit >> b) & 1 ? set : ~set;
-    }
+    const int32_t source = !FIRST && key >= 0 ? p.at_a[i + lane] : (int32_t)(i + lane);
+    const int32_t digit = (key >> shift) & mask;
+    const uint64_t same = alike(__ballot(key >= 0), key, shift, bits);
+    // those of them that are the same token stand side by side in their block of the second pass, but for a border
+    const uint64_t twins = FIRST && p.passes == 2 ? alike(same, key, p.bits[0], p.bits[1]) : 0;
     if (key >= 0) {
       const int leader = __ffsll((unsigned long long)same) - 1;
       int32_t start = 0;
@@ -193,8 +235,27 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const SortArgs p) {
       start = __shfl(start, leader);
       const int32_t to = start + __popcll(same & ((1ull << lane) - 1));
       (FIRST ? p.key_a : p.key_b)[to] = key;
-      (FIRST ? p.at_a : p.at_b)[to] = FIRST ? (int32_t)(i + lane) : p.at_a[i + lane];
-      if (FIRST) p.present[key] = 1;
+      (FIRST ? p.at_a : p.at_b)[to] = source;
+      if (FIRST) {
+        p.present[key] = 1;
+        if (p.passes == 2) {
+          // one lane counts for all twins that go to the same block of the second pass
+          const int32_t block = to / (int32_t)p.per;
+          const int32_t before_me = lane > 0 ? 63 - __builtin_clzll(twins & ((1ull << lane) - 1) | 1) : 0;
+          const bool has = (twins & ((1ull << lane) - 1)) != 0;
+          const int32_t block_before = __shfl(block, has ? before_me : lane);
+          const bool heads = !has || block_before != block;
+          const uint64_t ends = __ballot(heads);
+          if (heads) {
+            // twins from here to the next that begins anew
+            const uint64_t behind = lane == 63 ? 0 : twins & ~((2ull << lane) - 1);
+            const uint64_t stop = behind & ends;
+            const uint64_t mine = stop ? behind & ((1ull << (__ffsll((unsigned long long)stop) - 1)) - 1) : behind;
+            atomicAdd(&p.hist_b[(int64_t)block * kBins + ((key >> p.bits[0]) & ((1 << p.bits[1]) - 1))],
+                      1 + __popcll(mine));
+          }
+        }
+      }
     }
   }
 }
@@ -271,47 +332,53 @@ __global__ void __launch_bounds__(256) sum_kernel(const SumArgs p) {
   }
 }
 
+constexpr int kJoinWaves = 4;
+
 // The sums that pass a border: the block of the chunk in which one begins adds its parts up,
 // a wave a run of chunks, and joins those in order.
 template <class F, int V>
-__global__ void __launch_bounds__(512) join_kernel(const SumArgs p) {
+__global__ void __launch_bounds__(64 * kJoinWaves) join_kernel(const SumArgs p) {
   using E = typename F::E;
-  __shared__ float s[8][64 * V];
+  __shared__ float s[kJoinWaves][64 * V];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t c = blockIdx.x / p.tiles, d = (blockIdx.x - c * p.tiles) * 64 * V + lane * V;
+  const uint32_t chunk = blockIdx.x / (uint32_t)p.tiles;
+  const int64_t c = chunk, d = (int64_t)(blockIdx.x - chunk * (uint32_t)p.tiles) * 64 * V + lane * V;
   const int64_t valid = *p.valid, i0 = c * kChunk, i1 = i0 + kChunk;
   if (i1 >= valid) return;
-  const int32_t k = p.key[i1 - 1];
-  if (p.key[i1] != k || (p.key[i0] == k && i0 > 0 && p.key[i0 - 1] == k)) return;  // none begins here and goes on
-  // the last chunk it reaches: chunks lo hold its first token beyond doubt, chunks hi do not
-  int64_t lo = c + 1, hi = (valid + kChunk - 1) / kChunk;
+  const int64_t chunks = (valid + kChunk - 1) / kChunk;
+  // all at once: the borders of the chunk, and the first tokens of the 64 behind it
+  const int32_t first = p.key[i0], k = p.key[i1 - 1], next = p.key[i1], last = p.key[i0 > 0 ? i0 - 1 : 0];
+  const int32_t probe = c + 1 + lane < chunks ? p.key[(c + 1 + lane) * kChunk] : -1;
+  if (next != k || (first == k && i0 > 0 && last == k)) return;  // none begins here and goes on
+  // the last chunk it reaches: chunk lo holds it beyond doubt, chunk hi does not
+  int64_t n = __popcll(__ballot(probe == k));  // sorted: these hold for the first lanes
+  int64_t lo = c + n, hi = n < 64 ? lo + 1 : chunks;
   while (hi - lo > 1) {
     const int64_t step = (hi - lo + 63) / 64, m = lo + lane * step;
-    const bool in = m < hi && p.key[m * kChunk] == k;  // sorted: these hold for the first lanes
-    const int n = __popcll(__ballot(in));
+    n = __popcll(__ballot(m < hi && p.key[m < hi ? m * kChunk : 0] == k));
     const int64_t to = lo + n * step;
     lo = lo + (n - 1) * step;
     hi = to < hi ? to : hi;
   }
-  const int64_t n = lo - c;  // chunks after c
-  const int64_t share = (n + 7) / 8, from = c + 1 + w * share;
+  const int64_t share = (lo - c + kJoinWaves - 1) / kJoinWaves, from = c + 1 + w * share;
   const int64_t to = from + share < lo + 1 ? from + share : lo + 1;
   const bool some = d < p.g.D;
+  const float* const part = p.part + (some ? d : 0);
   float acc[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) acc[i] = w == 0 && some ? p.part[(2 * c + 1) * p.g.D + d + i] : 0.0f;
+  for (int i = 0; i < V; ++i) acc[i] = w == 0 ? part[(2 * c + 1) * p.g.D + i] : 0.0f;
 #pragma unroll 4
   for (int64_t m = from; m < to; ++m) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] += some ? p.part[2 * m * p.g.D + d + i] : 0.0f;
+    for (int i = 0; i < V; ++i) acc[i] += part[2 * m * p.g.D + i];
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i) s[w][lane * V + i] = acc[i];
+  for (int i = 0; i < V; ++i) s[w][i * 64 + lane] = acc[i];
   __syncthreads();
   if (w == 0 && some) {
-    for (int v = 1; v < 8; ++v) {
+    for (int v = 1; v < kJoinWaves; ++v) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += s[v][lane * V + i];
+      for (int i = 0; i < V; ++i) acc[i] += s[v][i * 64 + lane];
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] *= p.g.scale;
@@ -350,15 +417,20 @@ static hipError_t sums_of(const SumArgs& a, hipStream_t st) {
   sum_kernel<F, V><<<dim3((unsigned)((units + 3) / 4)), 256, 0, st>>>(s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || s.chunks < 2) return e;
-  join_kernel<F, V><<<dim3((unsigned)(s.chunks * s.tiles)), 512, 0, st>>>(s);
+  join_kernel<F, V><<<dim3((unsigned)(s.chunks * s.tiles)), 64 * kJoinWaves, 0, st>>>(s);
   return hipGetLastError();
 }
 
 template <class F>
 static hipError_t sums_fmt(const SumArgs& a, hipStream_t st) {
-  constexpr int V = F::W, es = sizeof(typename F::E);
-  const bool w = wide(a.g.d_out, a.g.o_stride, a.g.d_table, a.g.t_stride, a.g.D, V, es);
-  return w ? sums_of<F, V>(a, st) : sums_of<F, 1>(a, st);
+  switch (piece_of(a.g.d_out, a.g.o_stride, a.g.d_table, a.g.t_stride, a.g.D, sizeof(typename F::E))) {
+    case 8:
+      if constexpr (F::W == 8) return sums_of<F, 8>(a, st);
+      break;
+    case 4: return sums_of<F, 4>(a, st);
+    case 2: return sums_of<F, 2>(a, st);
+  }
+  return sums_of<F, 1>(a, st);
 }
 
 hipError_t launch_backward(rlscan_format f, const GradArgs& g, hipStream_t st) {
@@ -375,27 +447,21 @@ hipError_t launch_backward(rlscan_format f, const GradArgs& g, hipStream_t st) {
   s.at_a = reinterpret_cast<int32_t*>(take(p.keys));
   s.key_b = reinterpret_cast<int32_t*>(take(p.keys));
   s.at_b = reinterpret_cast<int32_t*>(take(p.keys));
-  int32_t* hist[2];
-  hist[0] = reinterpret_cast<int32_t*>(take(p.hist));
-  hist[1] = reinterpret_cast<int32_t*>(take(p.hist));
+  s.hist_a = reinterpret_cast<int32_t*>(take(p.hist));
+  s.hist_b = reinterpret_cast<int32_t*>(take(p.hist));
   s.valid = reinterpret_cast<int32_t*>(take(16));
   s.present = reinterpret_cast<uint8_t*>(take(p.present));
   s.R = g.R;
   s.N = g.N;
   s.per = p.per;
   s.blocks = (int)p.blocks;
-  s.hist = hist[0];
-  s.bits = p.bits[0];
+  s.passes = p.passes;
+  s.bits[0] = p.bits[0];
+  s.bits[1] = p.bits[1];
   const dim3 grid((unsigned)p.blocks);
-  count_kernel<true><<<grid, kSortThreads, 0, st>>>(s);
+  count_kernel<<<grid, kSortThreads, 0, st>>>(s);
   place_kernel<true><<<grid, kSortThreads, 0, st>>>(s);
-  if (p.passes == 2) {
-    s.hist = hist[1];
-    s.shift = p.bits[0];
-    s.bits = p.bits[1];
-    count_kernel<false><<<grid, kSortThreads, 0, st>>>(s);
-    place_kernel<false><<<grid, kSortThreads, 0, st>>>(s);
-  }
+  if (p.passes == 2) place_kernel<false><<<grid, kSortThreads, 0, st>>>(s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   SumArgs a{};
