@@ -582,7 +582,7 @@ rlscan_status rlscan_gated_recurrence_step(rlscan_format fmt, const rlscan_heads
  *      (optional: ones); positions [E,T] int32 in the layout, of either sign
  *      (not read, and optional, if rotate is 0).
  * Out: q_out, k_out like q, k, rounded once.
- * 1 <= D <= RLSCAN_MAX_NORM_DIM, rotate even and at most D, base > 0, eps >= 0 (with
+ * H + Hk <= 2^20, 1 <= D <= RLSCAN_MAX_NORM_DIM, rotate even and at most D, base > 0, eps >= 0 (with
  * eps 0 a row of zeros gives NaN). */
 #define RLSCAN_MAX_NORM_DIM 256
 

@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(1024) columns_kernel(const In* part, int64_t r
 hipError_t launch_columns(const float* part, int64_t rows, float* more, float* out0, int64_t n0, float* out1,
                           int64_t n1, hipStream_t st) {
   const unsigned tiles = (unsigned)((n0 + n1 + 15) / 16);
-  if (more_floats(rows, n0 + n1) == 0) {
+  if (!more || more_floats(rows, n0 + n1) == 0) {
     columns_kernel<float><<<dim3(tiles), 1024, 0, st>>>(part, rows, rows, nullptr, out0, n0, out1, n1);
     return hipGetLastError();
   }

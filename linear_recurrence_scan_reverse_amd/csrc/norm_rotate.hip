@@ -11,6 +11,7 @@
 // turns, in float64 (a position times a frequency keeps 2^-52 of itself, so far positions turn
 // like near ones), of which the part behind the point goes to a float32 sine and cosine.
 #include <cmath>
+#include <type_traits>
 
 #include "rlscan_nr.hpp"
 #include "rlscan_sums.hpp"
@@ -23,6 +24,9 @@ using logits::LF16;
 using logits::LF32;
 
 constexpr int kThreads = 256;
+// Blocks of the gradients, each with its share of the weights' sums: as many as run at once (three to a
+// compute unit).
+constexpr int64_t kBackBlocks = 768;
 
 struct Turns {      // frequencies in quarter turns, as products of powers
   double first;     // 2 / pi
@@ -38,6 +42,14 @@ struct KernelArgs {
 };
 
 // V elements as they lie in memory.
+template <int kBytes>
+struct WordOf {
+  using T = uint64_t;
+};
+template <>
+struct WordOf<4> {
+  using T = uint32_t;
+};
 template <class F, int V>
 struct Raw {
   typename F::E e[V];
@@ -54,9 +66,9 @@ __device__ __forceinline__ Raw<F, V> load_vec(const typename F::E* p) {
       __builtin_memcpy(reinterpret_cast<char*>(&r) + 16 * i, &v, 16);
     }
   } else {
-    static_assert(kBytes == 8, "");
-    const uint64_t v = *reinterpret_cast<const uint64_t*>(p);
-    __builtin_memcpy(&r, &v, 8);
+    using Word = typename WordOf<kBytes>::T;
+    const Word v = *reinterpret_cast<const Word*>(p);
+    __builtin_memcpy(&r, &v, kBytes);
   }
   return r;
 }
@@ -72,9 +84,9 @@ __device__ __forceinline__ void store_vec(typename F::E* p, const Raw<F, V>& r) 
       reinterpret_cast<u32x4*>(p)[i] = v;
     }
   } else {
-    uint64_t v;
-    __builtin_memcpy(&v, &r, 8);
-    *reinterpret_cast<uint64_t*>(p) = v;
+    typename WordOf<kBytes>::T v;
+    __builtin_memcpy(&v, &r, kBytes);
+    *reinterpret_cast<typename WordOf<kBytes>::T*>(p) = v;
   }
 }
 
@@ -205,32 +217,35 @@ __device__ __forceinline__ void angle(double quarters, float& cs, float& sn) {
   if (q >= 2) sn = -sn;
 }
 
+// The sum over a group of 2^log_lanes lanes, in every one of them: up to 16 by lane moves within a
+// row of 16, which take no trip through LDS.
 __device__ __forceinline__ float group_sum(float v, int log_lanes) {
-  for (int b = 0; b < log_lanes; ++b) v += __shfl_xor(v, 1 << b);
+  auto moved = [](float x, auto control) __attribute__((always_inline)) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(control)::value,
+                                                                 0xf, 0xf, true));
+  };
+  if (log_lanes > 0) v += moved(v, std::integral_constant<int, 0xb1>{});   // lanes 1 0 3 2 of four
+  if (log_lanes > 1) v += moved(v, std::integral_constant<int, 0x4e>{});   // lanes 2 3 0 1
+  if (log_lanes > 2) v += moved(v, std::integral_constant<int, 0x141>{});  // eight reversed
+  if (log_lanes > 3) v += moved(v, std::integral_constant<int, 0x140>{});  // sixteen reversed
+  if (log_lanes > 4) v += __shfl_xor(v, 16);
+  if (log_lanes > 5) v += __shfl_xor(v, 32);
   return v;
 }
 
-// A unit is a token's heads s, s + split, ...; a group of lanes takes units in turn.
-template <class F, int V, bool VEC, bool INTER, bool BWD>
-__global__ void __launch_bounds__(kThreads) heads_kernel(const KernelArgs k) {
+// A unit is a token's heads s, s + split, ...; a group of lanes takes units in turn.  The heads' loads
+// go out ahead (RING of them), always, and ahead of the stores: behind one that may not have been
+// made, a wait for one would wait for all.
+template <class F, int V, bool VEC, bool INTER, bool BWD, int RING>
+__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(BWD ? 3 : 4))) heads_kernel(const KernelArgs k) {
   using E = typename F::E;
   using At = Place<V, VEC, INTER>;
+  using H = Head<F, V, VEC, INTER>;
   __shared__ float s_w[BWD ? kThreads * 2 * V : 1];
   const Args& p = k.a;
   const int lanes = 1 << k.log_lanes, lane = threadIdx.x & (lanes - 1), group = threadIdx.x >> k.log_lanes;
   const int groups = kThreads >> k.log_lanes;
   const At at(lane, lanes, p.D, p.R);
-  double freq[V];
-  {
-    double f = k.t.first;
-#pragma unroll
-    for (int b = 0; b < 6; ++b) f *= (lane >> b) & 1 ? k.t.bit[b] : 1.0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      freq[i] = At::pair(i, lane, lanes) < p.R / 2 ? f : 0.0;
-      f *= k.t.step;
-    }
-  }
   const float over_d = 1.0f / (float)p.D;
   float dwa[2][BWD ? V : 1], dwb[2][BWD ? V : 1];
   if constexpr (BWD) {
@@ -240,78 +255,96 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const KernelArgs k) {
   // Groups leave the loop together with their wave: shuffles stay within a group, whose lanes
   // all have the same unit.
   for (int64_t u = (int64_t)blockIdx.x * groups + group; u < k.units; u += (int64_t)gridDim.x * groups) {
-    const int64_t token = u / k.split, s = u - token * k.split;
-    const int64_t e = token / p.T, t = token - e * p.T;
+    const int64_t token = k.split == 1 ? u : u / k.split;
+    int h = (int)(u - token * k.split);
+    const int64_t e = p.E == 1 ? 0 : token / p.T, t = token - e * p.T;
     float cs[V], sn[V];
-    const double pos = p.R > 0 ? (double)p.pos[e * p.p_se + t * p.p_st] : 0.0;
+    {
+      const double pos = p.R > 0 ? (double)p.pos[e * p.p_se + t * p.p_st] : 0.0;
+      double f = k.t.first;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      angle(pos * freq[i], cs[i], sn[i]);
-      if (BWD) sn[i] = -sn[i];
-    }
-    int64_t h = s;
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      const int64_t heads = p.heads[which];
-      const E* px = static_cast<const E*>(p.in[which].p) + e * p.in[which].se + t * p.in[which].st;
-      const E* pg = BWD ? static_cast<const E*>(p.grad[which].p) + e * p.grad[which].se + t * p.grad[which].st : nullptr;
-      E* po = static_cast<E*>(const_cast<void*>(p.out[which].p)) + e * p.out[which].se + t * p.out[which].st;
-      float wa[V], wb[V];
+      for (int b = 0; b < 6; ++b) f *= (lane >> b) & 1 ? k.t.bit[b] : 1.0;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int oa = VEC ? at.oa[0] + i : at.oa[VEC ? 0 : i], ob = VEC ? at.ob[0] + i : at.ob[VEC ? 0 : i];
-        const bool ok = p.weight[which] != nullptr && at.some;
-        wa[i] = ok && oa >= 0 ? p.weight[which][oa] : 1.0f;
-        wb[i] = ok && ob >= 0 ? p.weight[which][ob] : 1.0f;
+        angle(At::pair(i, lane, lanes) < p.R / 2 ? pos * f : 0.0, cs[i], sn[i]);
+        if (BWD) sn[i] = -sn[i];
+        f *= k.t.step;
       }
-      Head<F, V, VEC, INTER> next, next_g;
+    }
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const int heads = (int)p.heads[which], split = (int)k.split;
       if (h < heads) {
-        next.load(px + h * p.in[which].sh, at);
-        if constexpr (BWD) next_g.load(pg + h * p.grad[which].sh, at);
-      }
-      for (; h < heads; h += k.split) {
-        const Head<F, V, VEC, INTER> now = next, now_g = next_g;
-        if (h + k.split < heads) {
-          next.load(px + (h + k.split) * p.in[which].sh, at);
-          if constexpr (BWD) next_g.load(pg + (h + k.split) * p.grad[which].sh, at);
+        const int64_t sh = p.in[which].sh, gh = BWD ? p.grad[which].sh : 0, oh = p.out[which].sh;
+        const E* const px = static_cast<const E*>(p.in[which].p) + e * p.in[which].se + t * p.in[which].st;
+        const E* const pg = BWD ? static_cast<const E*>(p.grad[which].p) + e * p.grad[which].se + t * p.grad[which].st : nullptr;
+        E* const po = static_cast<E*>(const_cast<void*>(p.out[which].p)) + e * p.out[which].se + t * p.out[which].st;
+        float wa[V], wb[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int oa = VEC ? at.oa[0] + i : at.oa[VEC ? 0 : i], ob = VEC ? at.ob[0] + i : at.ob[VEC ? 0 : i];
+          const bool ok = p.weight[which] != nullptr && at.some;
+          wa[i] = ok && oa >= 0 ? p.weight[which][oa] : 1.0f;
+          wb[i] = ok && ob >= 0 ? p.weight[which][ob] : 1.0f;
         }
-        float x[V], y[V];
-        now.get(x, y, at);
-        float sq = 0.0f;
+        const int last = h + (heads - 1 - h) / split * split;
+        H raw[RING], raw_g[RING];
 #pragma unroll
-        for (int i = 0; i < V; ++i) sq += x[i] * x[i] + y[i] * y[i];
-        const float inv = __builtin_amdgcn_rsqf(group_sum(sq, k.log_lanes) * over_d + p.eps);
-        E* out = po + h * p.out[which].sh;
-        if constexpr (!BWD) {
+        for (int r = 0; r < RING; ++r) {
+          const int hr = h + r * split < last ? h + r * split : last;
+          raw[r].load(px + hr * sh, at);
+          if constexpr (BWD) raw_g[r].load(pg + hr * gh, at);
+        }
+        auto take = [&](H& now, H& now_g, int h) __attribute__((always_inline)) {
+          float x[V], y[V], gx[V], gy[V];
+          now.get(x, y, at);
+          if constexpr (BWD) now_g.get(gx, gy, at);
+          const int then = h + RING * split < last ? h + RING * split : last;
+          now.load(px + then * sh, at);
+          if constexpr (BWD) now_g.load(pg + then * gh, at);
+          float sq = 0.0f;
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            x[i] = x[i] * inv * wa[i];
-            y[i] = y[i] * inv * wb[i];
+          for (int i = 0; i < V; ++i) sq += x[i] * x[i] + y[i] * y[i];
+          const float inv = __builtin_amdgcn_rsqf(group_sum(sq, k.log_lanes) * over_d + p.eps);
+          if constexpr (!BWD) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              x[i] = x[i] * inv * wa[i];
+              y[i] = y[i] * inv * wb[i];
+            }
+            turn<V, VEC && INTER>(x, y, cs, sn);
+          } else {
+            turn<V, VEC && INTER>(gx, gy, cs, sn);
+            float dot = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              x[i] *= inv;
+              y[i] *= inv;
+              dwa[which][i] += gx[i] * x[i];
+              dwb[which][i] += gy[i] * y[i];
+              gx[i] *= wa[i];
+              gy[i] *= wb[i];
+              dot += gx[i] * x[i] + gy[i] * y[i];
+            }
+            dot = group_sum(dot, k.log_lanes) * over_d;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              x[i] = inv * (gx[i] - x[i] * dot);
+              y[i] = inv * (gy[i] - y[i] * dot);
+            }
           }
-          turn<V, VEC && INTER>(x, y, cs, sn);
-          Head<F, V, VEC, INTER>::store(out, x, y, at);
-        } else {
-          float gx[V], gy[V];
-          now_g.get(gx, gy, at);
-          turn<V, VEC && INTER>(gx, gy, cs, sn);
-          float dot = 0.0f;
+          H::store(po + h * oh, x, y, at);
+        };
+        for (; h + (RING - 1) * split <= last; h += RING * split) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            x[i] *= inv;
-            y[i] *= inv;
-            dwa[which][i] += gx[i] * x[i];
-            dwb[which][i] += gy[i] * y[i];
-            gx[i] *= wa[i];
-            gy[i] *= wb[i];
-            dot += gx[i] * x[i] + gy[i] * y[i];
-          }
-          dot = group_sum(dot, k.log_lanes) * over_d;
+          for (int r = 0; r < RING; ++r) take(raw[r], raw_g[r], h + r * split);
+        }
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            x[i] = inv * (gx[i] - x[i] * dot);
-            y[i] = inv * (gy[i] - y[i] * dot);
+        for (int r = 0; r < RING - 1; ++r) {
+          if (h <= last) {
+            take(raw[r], raw_g[r], h);
+            h += split;
           }
-          Head<F, V, VEC, INTER>::store(out, x, y, at);
         }
       }
       h -= heads;
@@ -355,7 +388,7 @@ int64_t backward_blocks(int64_t tokens, int64_t heads, int D) {
   const int64_t pairs = (D + 1) / 2, units = tokens * heads;
   const int64_t lanes = (int64_t)1 << log2_up((pairs + 3) / 4);
   const int64_t want = (units * lanes + kThreads - 1) / kThreads;
-  return want < 1 ? 1 : want < 1024 ? want : 1024;
+  return want < 1 ? 1 : want < kBackBlocks ? want : kBackBlocks;
 }
 
 Plan make_plan(rlscan_format f, const Args& a, bool backward) {
@@ -372,7 +405,7 @@ Plan make_plan(rlscan_format f, const Args& a, bool backward) {
     }
     return true;
   };
-  const int wide = 16 / es;
+  const int wide = backward && es == 2 ? 4 : 16 / es;
   p.V = 4;
   if (fits(wide)) {
     p.V = wide;
@@ -397,8 +430,9 @@ Plan make_plan(rlscan_format f, const Args& a, bool backward) {
 
 template <class F, int V, bool VEC, bool BWD>
 static void run_heads(const KernelArgs& k, int64_t blocks, hipStream_t st) {
-  if (k.a.interleaved) heads_kernel<F, V, VEC, true, BWD><<<dim3((unsigned)blocks), kThreads, 0, st>>>(k);
-  else heads_kernel<F, V, VEC, false, BWD><<<dim3((unsigned)blocks), kThreads, 0, st>>>(k);
+  constexpr int kRing = BWD && sizeof(typename F::E) == 4 ? 1 : 2;
+  if (k.a.interleaved) heads_kernel<F, V, VEC, true, BWD, kRing><<<dim3((unsigned)blocks), kThreads, 0, st>>>(k);
+  else heads_kernel<F, V, VEC, false, BWD, kRing><<<dim3((unsigned)blocks), kThreads, 0, st>>>(k);
 }
 
 template <class F, bool BWD>
@@ -416,8 +450,9 @@ static hipError_t run_fmt(rlscan_format f, const Args& a, hipStream_t st) {
   k.t.first = 0.63661977236758134308;
   for (int b = 0; b < 6; ++b) k.t.bit[b] = std::exp2(log_ratio * (double)(stride << b));
   k.t.step = std::exp2(log_ratio * (double)(p.vec ? 1 : 1 << p.log_lanes));
-  if (p.vec && p.V == kWide) run_heads<F, kWide, true, BWD>(k, p.blocks, st);
-  else if (p.vec) run_heads<F, kWide / 2, true, BWD>(k, p.blocks, st);
+  constexpr int kV = BWD && kWide == 8 ? 4 : kWide;
+  if (p.vec && p.V == kV) run_heads<F, kV, true, BWD>(k, p.blocks, st);
+  else if (p.vec) run_heads<F, kV / 2, true, BWD>(k, p.blocks, st);
   else run_heads<F, 4, false, BWD>(k, p.blocks, st);
   hipError_t e = hipGetLastError();
   if (!BWD || e != hipSuccess || (!a.d_weight[0] && !a.d_weight[1])) return e;

@@ -16,6 +16,7 @@ namespace {
 using namespace rlscan::checks;
 
 constexpr int64_t kMaxBlocks = ((int64_t)1 << 22) - 1;  // of up to 1024 threads: below 2^32 work-items
+constexpr int64_t kMaxHeads = (int64_t)1 << 20;
 
 bool layout_ok(rlscan_layout l) { return l == RLSCAN_LAYOUT_ENV_MAJOR || l == RLSCAN_LAYOUT_TIME_MAJOR; }
 
@@ -58,7 +59,7 @@ rlscan_status check_heads(rlscan_format f, int64_t E, int64_t T, int64_t H, int6
                           float base, float eps) {
   if (E < 0 || T < 0 || T >= RLSCAN_MAX_T || H < 0 || Hk < 0) return RLSCAN_ERR_SHAPE;
   if (D < 1 || D > RLSCAN_MAX_NORM_DIM || rotate < 0 || rotate > D || rotate % 2 != 0) return RLSCAN_ERR_SHAPE;
-  if (H > kMaxElems || Hk > kMaxElems || (E > 0 && H + Hk > kMaxElems / D / E)) return RLSCAN_ERR_SHAPE;
+  if (H > kMaxHeads || H + Hk > kMaxHeads || (E > 0 && H + Hk > kMaxElems / D / E)) return RLSCAN_ERR_SHAPE;
   if (E * (H + Hk) > 0 && T > kMaxElems / D / (E * (H + Hk))) return RLSCAN_ERR_SHAPE;
   if (elem_size(f) == 0) return RLSCAN_ERR_PARAM;
   if (!(base > 0.0f && std::isfinite(base)) || !(eps >= 0.0f && std::isfinite(eps))) return RLSCAN_ERR_PARAM;
