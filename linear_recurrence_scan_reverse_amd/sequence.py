@@ -20,18 +20,27 @@ _N = _p._HEADS_BYTES
 MARK_STEPS = 16  # RLSCAN_MARK_STEPS
 
 
+_TYPES = {n: ctypes.c_int64 * (4 * n) for n in (4, 6, 7)}  # n rlscan_heads in a row
+
+
 def _rows(tensors, time_major=False):
-    """(array to keep alive, addresses) of the [E, T, D] or [E, D] tensors as rlscan_heads."""
+    """(array to keep alive, addresses) of [E, T, D] tensors as rlscan_heads."""
     v = []
     for x in tensors:
-        s = x.stride()
-        if len(s) == 2:
-            v += (x.data_ptr(), s[0], 0, 0)
-        else:
-            v += (x.data_ptr(), s[1], s[0], 0) if time_major else (x.data_ptr(), s[0], s[1], 0)
-    a = (ctypes.c_int64 * len(v))(*v)
+        s0, s1, _ = x.stride()
+        v += (x.data_ptr(), s1, s0, 0) if time_major else (x.data_ptr(), s0, s1, 0)
+    a = _TYPES[len(tensors)](*v)
     h = ctypes.addressof(a)
-    return a, [h + i * _N for i in range(len(tensors))]
+    return a, range(h, h + len(tensors) * _N, _N)
+
+
+def _empty_like(x):
+    """Memory for an output that takes x's place: of its shape, contiguous."""
+    return _p.torch.empty_like(x) if x.is_contiguous() else _p.torch.empty(x.shape, dtype=x.dtype, device=x.device)
+
+
+def _out(x, name, like):
+    return _empty_like(like) if x is None else _strided(x, name, like.shape, like.dtype, like.device)
 
 
 def _recurrence_inputs(x, input_gate, decay_gate, rate, done, time_major):
@@ -66,7 +75,7 @@ def gated_recurrence(x, input_gate, decay_gate, rate, done=None, init_state=None
     _plain(init_state, "init_state", (E, D), torch.float32, dev)
     fmt = _p._DTYPES[dt]
     with _on(stream, dev):
-        out = torch.empty(x.shape, dtype=dt, device=dev) if out is None else _strided(out, "out", x.shape, dt, dev)
+        out = _out(out, "out", x)
         if final_state is not None:
             _plain(final_state, "final_state", (E, D), torch.float32, dev)
         elif with_state:
@@ -101,8 +110,7 @@ def gated_recurrence_backward(d_out, x, input_gate, decay_gate, rate, marks, don
     _plain(d_final_state, "d_final_state", (E, D), torch.float32, dev)
     fmt = _p._DTYPES[dt]
     with _on(stream, dev):
-        dx, di, dd = [torch.empty(x.shape, dtype=dt, device=dev) if g is None else _strided(g, name, x.shape, dt, dev)
-                      for g, name in ((dx, "dx"), (d_input_gate, "d_input_gate"), (d_decay_gate, "d_decay_gate"))]
+        dx, di, dd = _out(dx, "dx", x), _out(d_input_gate, "d_input_gate", x), _out(d_decay_gate, "d_decay_gate", x)
         dr = torch.empty_like(rate) if d_rate is None else _plain(d_rate, "d_rate", (D,), torch.float32, dev)
         dh = d_init_state
         if dh is None:
@@ -128,10 +136,11 @@ def gated_recurrence_step(x, input_gate, decay_gate, rate, state, reset=None, sl
     _values(x, "x", 2)
     dev, dt = _on_gpu(x, "x"), x.dtype
     torch = _p.torch
-    E, D = x.shape
-    _strided(x, "x", (E, D), dt, dev)
-    _strided(input_gate, "input_gate", (E, D), dt, dev)
-    _strided(decay_gate, "decay_gate", (E, D), dt, dev)
+    shape = x.shape
+    E, D = shape
+    _strided(x, "x", shape, dt, dev)
+    _strided(input_gate, "input_gate", shape, dt, dev)
+    _strided(decay_gate, "decay_gate", shape, dt, dev)
     if not isinstance(rate, torch.Tensor):
         raise TypeError("rate must be a torch.Tensor")
     _plain(rate, "rate", (D,), torch.float32, dev)
@@ -144,10 +153,12 @@ def gated_recurrence_step(x, input_gate, decay_gate, rate, state, reset=None, sl
     if slots is None and S < E:
         raise ValueError("state has %d slots for %d rows" % (S, E))
     with _on(stream, dev):
-        out = torch.empty((E, D), dtype=dt, device=dev) if out is None else _strided(out, "out", (E, D), dt, dev)
-        keep, h = _rows((x, input_gate, decay_gate, out))
-        _call("rlscan_gated_recurrence_step", _p._DTYPES[dt], h[0], h[1], h[2], rate.data_ptr(), _ptr(reset),
-              _ptr(slots), state.data_ptr(), h[3], E, S, D, _raw_stream(stream, dev))
+        out = _out(out, "out", x)
+        keep = _TYPES[4](x.data_ptr(), x.stride(0), 0, 0, input_gate.data_ptr(), input_gate.stride(0), 0, 0,
+                         decay_gate.data_ptr(), decay_gate.stride(0), 0, 0, out.data_ptr(), out.stride(0), 0, 0)
+        h = ctypes.addressof(keep)
+        _call("rlscan_gated_recurrence_step", _p._DTYPES[dt], h, h + _N, h + 2 * _N, rate.data_ptr(), _ptr(reset),
+              _ptr(slots), state.data_ptr(), h + 3 * _N, E, S, D, _raw_stream(stream, dev))
     return out
 
 
@@ -160,9 +171,9 @@ def _head_rows(tensors, time_major):
             v += (x.data_ptr(), s[0], 0, s[1])
         else:
             v += (x.data_ptr(), s[1], s[0], s[2]) if time_major else (x.data_ptr(), s[0], s[1], s[2])
-    a = (ctypes.c_int64 * len(v))(*v)
+    a = _TYPES[len(tensors)](*v)
     h = ctypes.addressof(a)
-    return a, [h + i * _N for i in range(len(tensors))]
+    return a, range(h, h + len(tensors) * _N, _N)
 
 
 def _head_inputs(q, k, q_weight, k_weight, positions, rotate, time_major):
@@ -176,12 +187,16 @@ def _head_inputs(q, k, q_weight, k_weight, positions, rotate, time_major):
     _values(q, "q", q.dim())
     _values(k, "k", q.dim())
     dev, dt = _on_gpu(q, "q"), q.dtype
-    lead, (H, D), Hk = tuple(q.shape[:-2]), q.shape[-2:], k.shape[-2]
-    if len(lead) == 1:
-        E, T = lead[0], 1
+    shape = tuple(q.shape)
+    if len(shape) == 3:
+        E, H, D = shape
+        T = 1
     else:
-        E, T = (lead[1], lead[0]) if time_major else lead
-    _strided(q, "q", q.shape, dt, dev)
+        E, T, H, D = shape
+        if time_major:
+            E, T = T, E
+    lead, Hk = shape[:-2], k.shape[-2]
+    _strided(q, "q", shape, dt, dev)
     _strided(k, "k", lead + (Hk, D), dt, dev)
     _plain(q_weight, "q_weight", (D,), torch.float32, dev)
     _plain(k_weight, "k_weight", (D,), torch.float32, dev)
@@ -208,10 +223,8 @@ def norm_rotate_heads(q, k, q_weight=None, k_weight=None, positions=None, *, rot
     256; q_weight, k_weight [D] float32 (None: ones); positions [E, T] (one step: [E]) int32,
     None for normalising alone.  Returns (q_out, k_out) of their shapes and dtype."""
     dev, dt, E, T, H, Hk, D, rotate = _head_inputs(q, k, q_weight, k_weight, positions, rotate, time_major)
-    torch = _p.torch
     with _on(stream, dev):
-        q_out = torch.empty(q.shape, dtype=dt, device=dev) if q_out is None else _strided(q_out, "q_out", q.shape, dt, dev)
-        k_out = torch.empty(k.shape, dtype=dt, device=dev) if k_out is None else _strided(k_out, "k_out", k.shape, dt, dev)
+        q_out, k_out = _out(q_out, "q_out", q), _out(k_out, "k_out", k)
         keep, h = _head_rows((q, k, q_out, k_out), time_major)
         _call("rlscan_norm_rotate_heads", _p._DTYPES[dt], 1 if time_major and q.dim() == 4 else 0, h[0], h[1],
               _ptr(q_weight), _ptr(k_weight), _ptr(positions), h[2], h[3], E, T, H, Hk, D, rotate, float(base),
@@ -231,8 +244,7 @@ def norm_rotate_heads_backward(d_q_out, d_k_out, q, k, q_weight=None, k_weight=N
     _strided(d_q_out, "d_q_out", q.shape, dt, dev)
     _strided(d_k_out, "d_k_out", k.shape, dt, dev)
     with _on(stream, dev):
-        dq = torch.empty(q.shape, dtype=dt, device=dev) if dq is None else _strided(dq, "dq", q.shape, dt, dev)
-        dk = torch.empty(k.shape, dtype=dt, device=dev) if dk is None else _strided(dk, "dk", k.shape, dt, dev)
+        dq, dk = _out(dq, "dq", q), _out(dk, "dk", k)
         _plain(d_q_weight, "d_q_weight", (D,), torch.float32, dev)
         _plain(d_k_weight, "d_k_weight", (D,), torch.float32, dev)
         if d_q_weight is None and q_weight is not None:
