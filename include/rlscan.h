@@ -525,10 +525,12 @@ rlscan_status rlscan_action_log_probs_backward(rlscan_format fmt, const float *d
  * whatever r_t is, so that inf and NaN stay within their episode.
  * In:  x, input_gate (i), decay_gate (r) [E,T,D] in fmt (rlscan_heads with head
  *      unused); rate [D], >= 0 (below: NaN in the channel); done [E,T] in the
- *      layout (optional); init_state [E,D] (optional), h_{-1}.
+ *      layout (optional); reset [E] (optional): rows whose step before the first
+ *      ended an episode, so that the first has a_0 = 0 (the state is dropped
+ *      unread); init_state [E,D] (optional), h_{-1}.
  * Out: out [E,T,D] in fmt: h, rounded once from float32;
  *      final_state [E,D] (optional): the state that the next window takes as
- *      init_state, zero where the row's last step is flagged;
+ *      init_state, zero where the row's last step is flagged (that flag is its reset);
  *      marks [E,ceil(T/RLSCAN_MARK_STEPS),D] float32 (optional): the state before
  *      every RLSCAN_MARK_STEPS-th step, for the backward call.
  * E*ceil(D/64) < 2^22.  With T = 0 the state is passed through. */
@@ -538,8 +540,8 @@ int64_t rlscan_gated_recurrence_workspace(rlscan_format fmt, int64_t E, int64_t 
 
 rlscan_status rlscan_gated_recurrence(rlscan_format fmt, rlscan_layout layout, const rlscan_heads *x,
                                       const rlscan_heads *input_gate, const rlscan_heads *decay_gate,
-                                      const float *rate, const uint8_t *done, const float *init_state,
-                                      const rlscan_heads *out, float *final_state, float *marks, void *workspace,
+                                      const float *rate, const uint8_t *done, const uint8_t *reset,
+                                      const float *init_state, const rlscan_heads *out, float *final_state, float *marks, void *workspace,
                                       int64_t workspace_bytes, int64_t E, int64_t T, int64_t D, hipStream_t stream);
 
 /* Gradients of rlscan_gated_recurrence.
@@ -553,8 +555,8 @@ rlscan_status rlscan_gated_recurrence(rlscan_format fmt, rlscan_layout layout, c
 rlscan_status rlscan_gated_recurrence_backward(
     rlscan_format fmt, rlscan_layout layout, const rlscan_heads *d_out, const rlscan_heads *x,
     const rlscan_heads *input_gate, const rlscan_heads *decay_gate, const float *rate, const float *marks,
-    const uint8_t *done, const float *d_final_state, const rlscan_heads *dx, const rlscan_heads *d_input_gate,
-    const rlscan_heads *d_decay_gate, float *d_rate, float *d_init_state, void *workspace, int64_t workspace_bytes,
+    const uint8_t *done, const uint8_t *reset, const float *d_final_state, const rlscan_heads *dx,
+    const rlscan_heads *d_input_gate, const rlscan_heads *d_decay_gate, float *d_rate, float *d_init_state, void *workspace, int64_t workspace_bytes,
     int64_t E, int64_t T, int64_t D, hipStream_t stream);
 
 /* The same recurrence for one step of E rows, on states kept from call to call

@@ -76,8 +76,8 @@ _SIGNATURES.update({
     "rlscan_action_log_probs": [_int, _vp, _i64, _vp, _vp, _f32] + [_vp] * 4 + [_i64] * 3 + [_vp],
     "rlscan_action_log_probs_backward": [_int, _vp, _vp, _vp, _i64, _vp, _vp, _f32, _vp, _vp, _vp, _i64, _i64, _i64,
                                          _vp],
-    "rlscan_gated_recurrence": [_int, _int] + [_vp] * 10 + [_i64] * 4 + [_vp],
-    "rlscan_gated_recurrence_backward": [_int, _int] + [_vp] * 14 + [_i64] * 4 + [_vp],
+    "rlscan_gated_recurrence": [_int, _int] + [_vp] * 11 + [_i64] * 4 + [_vp],
+    "rlscan_gated_recurrence_backward": [_int, _int] + [_vp] * 15 + [_i64] * 4 + [_vp],
     "rlscan_gated_recurrence_step": [_int] + [_vp] * 8 + [_i64] * 3 + [_vp],
     "rlscan_norm_rotate_heads": [_int, _int] + [_vp] * 7 + [_i64] * 6 + [_f32, _int, _f32, _vp],
     "rlscan_norm_rotate_heads_backward": [_int, _int] + [_vp] * 12 + [_i64] * 7 + [_f32, _int, _f32, _vp],

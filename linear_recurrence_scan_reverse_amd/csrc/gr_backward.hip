@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(64 * W) fold_back_kernel(const Args p, uint32_
   float total = 0.0f, y = 0.0f;
   bool dropped = false;
   auto fold = [&](const Chunk<F, S>& c, uint32_t live) __attribute__((always_inline)) {
-    const uint32_t cut = flag_word(c.flag);
+    const uint32_t cut = flag_word(c.flag, 1, 0);  // never the row's first step
     Decays<S> k;
     if (cut == 0 && live == (1u << S) - 1) decays<F, S, false>(k, c, rate2, 0, 0);
     else decays<F, S, true>(k, c, rate2, cut, live);
@@ -212,6 +212,7 @@ __global__ void __launch_bounds__(64 * W) backward_kernel(const Args p, uint32_t
   for (int64_t e = group; e < p.E; e += p.groups) {
     const Tensors<F, S, NEAR> in(p, e, d0, lane, col);
     const uint32_t out_at = column ? in.at : kNoColumn;
+    const uint32_t first = first_flag(p, e);
     float carry = 0.0f;  // e entering the W chunks at hand from the steps behind them
     if (p.d_final && !(in.done && p.T > 0 && in.done[(p.T - 1) * p.d_st] != 0)) carry = p.d_final[e * p.D + d0 + col];
     for (int64_t v = p.nseg - 1; v > seg; --v) {
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(64 * W) backward_kernel(const Args p, uint32_t
       s.carry[buf][lane] = carry;  // the same from every wave
     }
     auto take = [&](const Chunk<F, S>& c, const Rest<F, S>& rest, int t) __attribute__((always_inline)) {
-      const uint32_t cut = flag_word(c.flag), live = live_word<S>(t, end);
+      const uint32_t cut = flag_word(c.flag, t, first), live = live_word<S>(t, end);
       const bool care = cut != 0 || live != (1u << S) - 1;
       Decays<S> k;
       if (!care) decays<F, S, false>(k, c, rate2, 0, 0);

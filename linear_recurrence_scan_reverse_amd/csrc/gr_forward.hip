@@ -107,8 +107,9 @@ __global__ void __launch_bounds__(64 * W) fold_kernel(const Args p, uint32_t til
   const int share = (int)p.seg_steps / W, begin = (int)seg * (int)p.seg_steps + w * share, end = begin + share;
   float total = 0.0f, y = 0.0f;
   bool dropped = false;
-  auto fold = [&](const Chunk<F, S>& c) __attribute__((always_inline)) {
-    const uint32_t cut = flag_word(c.flag);
+  const uint32_t first = first_flag(p, e);
+  auto fold = [&](const Chunk<F, S>& c, int t) __attribute__((always_inline)) {
+    const uint32_t cut = flag_word(c.flag, t, first);
     Coefficients<S> k;
     if (cut == 0) coefficients<F, S, false>(k, c, rate2, 0, 0);
     else coefficients<F, S, true>(k, c, rate2, cut, (1u << S) - 1);
@@ -120,11 +121,11 @@ __global__ void __launch_bounds__(64 * W) fold_kernel(const Args p, uint32_t til
   in.load(one, begin, end);
   for (int t = begin;;) {  // a share holds whole chunks
     in.load(two, t + S, end);
-    fold(one);
+    fold(one, t);
     t += S;
     if (t >= end) break;
     in.load(one, t + S, end);
-    fold(two);
+    fold(two, t);
     t += S;
     if (t >= end) break;
   }
@@ -170,8 +171,9 @@ __global__ void __launch_bounds__(64 * W) forward_kernel(const Args p, uint32_t 
   }
   if (W > 1) s.carry[0][lane] = carry;  // the same from every wave
   int buf = 0;
+  const uint32_t first = first_flag(p, e);
   auto take = [&](const Chunk<F, S>& c, int t) __attribute__((always_inline)) {
-    const uint32_t cut = flag_word(c.flag), live = live_word<S>(t, end);
+    const uint32_t cut = flag_word(c.flag, t, first), live = live_word<S>(t, end);
     const bool care = cut != 0 || live != (1u << S) - 1;
     Coefficients<S> k;
     if (!care) coefficients<F, S, false>(k, c, rate2, 0, 0);

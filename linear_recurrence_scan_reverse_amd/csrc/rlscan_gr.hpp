@@ -36,6 +36,7 @@ struct Args {
   const float* rate;      // [D]
   const uint8_t* done;    // [E, T] or [T, E] by strides, or NULL
   int64_t d_se, d_st;
+  const uint8_t* reset;   // [E] or NULL: whether step 0 starts anew
   const float* init;      // [E, D] or NULL
   const float* d_final;   // [E, D] or NULL
   float* final_state;     // [E, D] or NULL
@@ -196,7 +197,13 @@ __device__ __forceinline__ uint8_t load_flag(const uint8_t* done, int64_t step, 
   const bool in = lane < S && t + lane > 0 && t + lane < end;  // a row's steps lie at most 2^22 bytes apart
   return __builtin_amdgcn_raw_buffer_load_b8(rs, in ? lane * (int)step : (int)kNoColumn, 0, 0);
 }
-__device__ __forceinline__ uint32_t flag_word(uint8_t flag) { return (uint32_t)__builtin_amdgcn_ballot_w64(flag != 0); }
+// first: bit 0 if the row's first step starts anew.
+__device__ __forceinline__ uint32_t flag_word(uint8_t flag, int t, uint32_t first) {
+  return (uint32_t)__builtin_amdgcn_ballot_w64(flag != 0) | (t == 0 ? first : 0);
+}
+__device__ __forceinline__ uint32_t first_flag(const Args& p, int64_t e) {
+  return __builtin_amdgcn_readfirstlane(p.reset && p.reset[e] != 0 ? 1 : 0);
+}
 
 // Bit k: step t + k lies before the end.
 template <int S>

@@ -35,10 +35,11 @@ int64_t marks_bytes(int64_t E, int64_t T, int64_t D) {
 }
 
 void fill_recurrence(rlscan::gr::Args& a, const rlscan::gr::Plan& p, rlscan_layout l, const float* rate,
-                     const uint8_t* done, int64_t E, int64_t T, int64_t D, void* workspace) {
+                     const uint8_t* done, const uint8_t* reset, int64_t E, int64_t T, int64_t D, void* workspace) {
   const bool tm = l == RLSCAN_LAYOUT_TIME_MAJOR;
   a.rate = rate;
   a.done = done;
+  a.reset = reset;
   a.d_se = tm ? 1 : T;
   a.d_st = tm ? E : 1;
   a.E = E;
@@ -110,7 +111,7 @@ int64_t rlscan_gated_recurrence_workspace(rlscan_format fmt, int64_t E, int64_t 
 
 rlscan_status rlscan_gated_recurrence(rlscan_format fmt, rlscan_layout layout, const rlscan_heads* x,
                                       const rlscan_heads* input_gate, const rlscan_heads* decay_gate,
-                                      const float* rate, const uint8_t* done, const float* init_state,
+                                      const float* rate, const uint8_t* done, const uint8_t* reset, const float* init_state,
                                       const rlscan_heads* out, float* final_state, float* marks, void* workspace,
                                       int64_t workspace_bytes, int64_t E, int64_t T, int64_t D, hipStream_t stream) {
   rlscan_status st = check_recurrence(fmt, E, T, D);
@@ -137,12 +138,13 @@ rlscan_status rlscan_gated_recurrence(rlscan_format fmt, rlscan_layout layout, c
     return RLSCAN_ERR_ALIGN;
   io.add_in(plain(rate, D * 4));
   io.add_in(plain(done, E * T));
+  io.add_in(plain(reset, E));
   io.add_in(plain(init_state, E * D * 4));
   io.add_out(plain(final_state, E * D * 4));
   io.add_out(plain(marks, marks_bytes(E, T, D)));
   io.add_out(plain(workspace, need));
   if (io.clash()) return RLSCAN_ERR_ALIAS;
-  fill_recurrence(a, p, layout, rate, done, E, T, D, workspace);
+  fill_recurrence(a, p, layout, rate, done, reset, E, T, D, workspace);
   a.init = init_state;
   a.final_state = final_state;
   a.marks = marks;
@@ -152,7 +154,7 @@ rlscan_status rlscan_gated_recurrence(rlscan_format fmt, rlscan_layout layout, c
 rlscan_status rlscan_gated_recurrence_backward(
     rlscan_format fmt, rlscan_layout layout, const rlscan_heads* d_out, const rlscan_heads* x,
     const rlscan_heads* input_gate, const rlscan_heads* decay_gate, const float* rate, const float* marks,
-    const uint8_t* done, const float* d_final_state, const rlscan_heads* dx, const rlscan_heads* d_input_gate,
+    const uint8_t* done, const uint8_t* reset, const float* d_final_state, const rlscan_heads* dx, const rlscan_heads* d_input_gate,
     const rlscan_heads* d_decay_gate, float* d_rate, float* d_init_state, void* workspace, int64_t workspace_bytes,
     int64_t E, int64_t T, int64_t D, hipStream_t stream) {
   rlscan_status st = check_recurrence(fmt, E, T, D);
@@ -184,12 +186,13 @@ rlscan_status rlscan_gated_recurrence_backward(
   io.add_in(plain(rate, D * 4));
   io.add_in(plain(marks, marks_bytes(E, T, D)));
   io.add_in(plain(done, E * T));
+  io.add_in(plain(reset, E));
   io.add_in(plain(d_final_state, E * D * 4));
   io.add_out(plain(d_rate, D * 4));
   io.add_out(plain(d_init_state, E * D * 4));
   io.add_out(plain(workspace, need));
   if (io.clash()) return RLSCAN_ERR_ALIAS;
-  fill_recurrence(a, p, layout, rate, done, E, T, D, workspace);
+  fill_recurrence(a, p, layout, rate, done, reset, E, T, D, workspace);
   if (E == 0) a.groups = 1;  // one block a tile, which writes zeros
   a.marks = const_cast<float*>(marks);
   a.d_final = d_final_state;

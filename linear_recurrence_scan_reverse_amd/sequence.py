@@ -58,7 +58,7 @@ def _recurrence_inputs(x, input_gate, decay_gate, rate, done, time_major):
 
 
 def gated_recurrence(x, input_gate, decay_gate, rate, done=None, init_state=None, *, time_major=False,
-                     with_state=False, with_marks=False, out=None, final_state=None, marks=None, stream=None):
+                     with_state=False, with_marks=False, reset=None, out=None, final_state=None, marks=None, stream=None):
     """A gated memory of one number a channel, over whole rows.
 
     Per row and channel s_t = rate sigmoid(decay_gate_t), a_t = exp(-s_t) and
@@ -66,13 +66,15 @@ def gated_recurrence(x, input_gate, decay_gate, rate, done=None, init_state=None
     ``done`` has a_t = 0, whatever the state was: inf and NaN stay within their episode.
 
     x, input_gate, decay_gate [E, T, D] (``time_major``: [T, E, D]); rate [D] float32, not
-    negative; done [E, T]; init_state [E, D] float32.  Returns out, h in x's dtype, followed
+    negative; done [E, T]; init_state [E, D] float32; reset [E]: rows whose step before the first
+    ended an episode (the last column of the window before's done).  Returns out, h in x's dtype, followed
     by final_state [E, D] with ``with_state`` or ``final_state`` (what the next window takes as
     init_state) and by marks [E, ceil(T / 16), D] float32 with ``with_marks`` or ``marks``
     (states on the way, which the backward call takes)."""
     dev, dt, E, T, D, done = _recurrence_inputs(x, input_gate, decay_gate, rate, done, time_major)
     torch = _p.torch
     _plain(init_state, "init_state", (E, D), torch.float32, dev)
+    reset = _flags(reset, "reset", (E,), dev)
     fmt = _p._DTYPES[dt]
     with _on(stream, dev):
         out = _out(out, "out", x)
@@ -88,14 +90,14 @@ def gated_recurrence(x, input_gate, decay_gate, rate, done=None, init_state=None
         ws, need = _workspace("rlscan_gated_recurrence_workspace", dev, fmt, E, T, D, 0)
         keep, h = _rows((x, input_gate, decay_gate, out), time_major)
         _call("rlscan_gated_recurrence", fmt, 1 if time_major else 0, h[0], h[1], h[2], rate.data_ptr(), _ptr(done),
-              _ptr(init_state), h[3], _ptr(final_state), _ptr(marks), _ptr(ws), need, E, T, D,
+              _ptr(reset), _ptr(init_state), h[3], _ptr(final_state), _ptr(marks), _ptr(ws), need, E, T, D,
               _raw_stream(stream, dev))
     outs = (out,) + tuple(t for t in (final_state, marks) if t is not None)
     return outs if len(outs) > 1 else out
 
 
 def gated_recurrence_backward(d_out, x, input_gate, decay_gate, rate, marks, done=None, d_final_state=None, *,
-                              time_major=False, dx=None, d_input_gate=None, d_decay_gate=None, d_rate=None,
+                              time_major=False, reset=None, dx=None, d_input_gate=None, d_decay_gate=None, d_rate=None,
                               d_init_state=None, stream=None):
     """Gradients of ``gated_recurrence``: (dx, d_input_gate, d_decay_gate, d_rate, d_init_state).
 
@@ -108,6 +110,7 @@ def gated_recurrence_backward(d_out, x, input_gate, decay_gate, rate, marks, don
         raise TypeError("marks must be a torch.Tensor")
     _plain(marks, "marks", (E, -(-T // MARK_STEPS), D), torch.float32, dev)
     _plain(d_final_state, "d_final_state", (E, D), torch.float32, dev)
+    reset = _flags(reset, "reset", (E,), dev)
     fmt = _p._DTYPES[dt]
     with _on(stream, dev):
         dx, di, dd = _out(dx, "dx", x), _out(d_input_gate, "d_input_gate", x), _out(d_decay_gate, "d_decay_gate", x)
@@ -120,7 +123,7 @@ def gated_recurrence_backward(d_out, x, input_gate, decay_gate, rate, marks, don
         ws, need = _workspace("rlscan_gated_recurrence_workspace", dev, fmt, E, T, D, 1)
         keep, h = _rows((d_out, x, input_gate, decay_gate, dx, di, dd), time_major)
         _call("rlscan_gated_recurrence_backward", fmt, 1 if time_major else 0, *h[:4], rate.data_ptr(),
-              marks.data_ptr(), _ptr(done), _ptr(d_final_state), *h[4:], dr.data_ptr(), dh.data_ptr(), _ptr(ws), need,
+              marks.data_ptr(), _ptr(done), _ptr(reset), _ptr(d_final_state), *h[4:], dr.data_ptr(), dh.data_ptr(), _ptr(ws), need,
               E, T, D, _raw_stream(stream, dev))
     return dx, di, dd, dr, dh
 

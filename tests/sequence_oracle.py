@@ -54,12 +54,15 @@ class Recurrence:
     """Forward values and, given d_out, gradients of [E, T, D] inputs (env-major, any storage type),
     each with its bound before storage: attributes name and name + '_b'."""
 
-    def __init__(self, x, ig, dg, rate, done=None, init=None, d_out=None, d_final=None):
+    def __init__(self, x, ig, dg, rate, done=None, init=None, d_out=None, d_final=None,
+                 reset=None):
         x, ig, dg, rate = x.cpu().double(), ig.cpu().double(), dg.cpu().double(), rate.cpu().double()
         E, T, D = x.shape
         live = torch.ones(E, T + 1, 1, dtype=torch.float64)
         if done is not None:
             live[:, 1:, 0] = (done.cpu() == 0).double()
+        if reset is not None:
+            live[:, 0, 0] = (reset.cpu() == 0).double()
         si, sr = logistic(ig), logistic(dg)
         s = rate * sr
         fresh = live[:, :T] == 0

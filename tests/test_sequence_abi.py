@@ -42,23 +42,23 @@ def by_reference(x):
 
 def recurrence(lib, E=2, T=100, D=70, fmt=BF16, layout=0, **kw):
     a = {"x": rows(0, T, D), "ig": rows(1, T, D), "dg": rows(2, T, D), "rate": addr(3), "done": addr(4),
-         "init": addr(5), "out": rows(6, T, D), "final": addr(7), "marks": addr(8), "ws": addr(9)}
+         "reset": addr(17), "init": addr(5), "out": rows(6, T, D), "final": addr(7), "marks": addr(8), "ws": addr(9)}
     a["bytes"] = max(0, lib.rlscan_gated_recurrence_workspace(fmt, E, T, D, 0))
     a.update(kw)
     p = by_reference
-    return lib.rlscan_gated_recurrence(fmt, layout, p(a["x"]), p(a["ig"]), p(a["dg"]), a["rate"], a["done"], a["init"],
-                                       p(a["out"]), a["final"], a["marks"], a["ws"], a["bytes"], E, T, D, None)
+    return lib.rlscan_gated_recurrence(fmt, layout, p(a["x"]), p(a["ig"]), p(a["dg"]), a["rate"], a["done"],
+                                       a["reset"], a["init"], p(a["out"]), a["final"], a["marks"], a["ws"], a["bytes"], E, T, D, None)
 
 
 def recurrence_backward(lib, E=2, T=100, D=70, fmt=BF16, layout=0, **kw):
     a = {"do": rows(10, T, D), "x": rows(0, T, D), "ig": rows(1, T, D), "dg": rows(2, T, D), "rate": addr(3),
-         "marks": addr(8), "done": addr(4), "d_final": addr(5), "dx": rows(11, T, D), "di": rows(12, T, D),
+         "marks": addr(8), "done": addr(4), "reset": addr(17), "d_final": addr(5), "dx": rows(11, T, D), "di": rows(12, T, D),
          "dr": rows(13, T, D), "d_rate": addr(14), "d_init": addr(15), "ws": addr(9)}
     a["bytes"] = max(0, lib.rlscan_gated_recurrence_workspace(fmt, E, T, D, 1))
     a.update(kw)
     p = by_reference
     return lib.rlscan_gated_recurrence_backward(
-        fmt, layout, p(a["do"]), p(a["x"]), p(a["ig"]), p(a["dg"]), a["rate"], a["marks"], a["done"], a["d_final"],
+        fmt, layout, p(a["do"]), p(a["x"]), p(a["ig"]), p(a["dg"]), a["rate"], a["marks"], a["done"], a["reset"], a["d_final"],
         p(a["dx"]), p(a["di"]), p(a["dr"]), a["d_rate"], a["d_init"], a["ws"], a["bytes"], E, T, D, None)
 
 
@@ -112,6 +112,7 @@ def test_recurrence_strides_and_overlap(lib):
         assert recurrence(lib, out=rows({"x": 0, "ig": 1, "dg": 2}[name], 100, 70)) == ERR_ALIAS, name
     assert recurrence(lib, final=addr(5)) == ERR_ALIAS
     assert recurrence(lib, marks=addr(4)) == ERR_ALIAS
+    assert recurrence(lib, marks=addr(17)) == ERR_ALIAS
     assert recurrence(lib, marks=addr(7)) == ERR_ALIAS
     assert recurrence(lib, E=1, T=4000, marks=addr(9)) == ERR_ALIAS
     assert recurrence_backward(lib, dx=rows(11, 100, 70), di=rows(11, 100, 70)) == ERR_ALIAS
@@ -119,6 +120,7 @@ def test_recurrence_strides_and_overlap(lib):
     assert recurrence_backward(lib, d_rate=addr(3)) == ERR_ALIAS
     assert recurrence_backward(lib, d_init=addr(5)) == ERR_ALIAS
     assert recurrence_backward(lib, d_init=addr(8)) == ERR_ALIAS
+    assert recurrence_backward(lib, d_rate=addr(17)) == ERR_ALIAS
 
 
 def test_recurrence_workspace(lib):
