@@ -3,10 +3,10 @@
 //
 //   out_r = scale table[token_r],   d_table_n = scale sum over token_r = n of d_out_r
 //
-// Both are bound by memory.  For the gradient the tokens are sorted (stable, by one or two
-// digits of up to ten bits), so that a row's terms follow one another in the order of the
-// tokens: chunks of sorted tokens are summed by a wave each, and what passes a chunk's border is
-// joined afterwards, in order.  No atomics on values: results do not vary from run to run.
+// Both are bound by memory.  For the gradient of more than a few kinds of token the tokens are sorted
+// (stable, by one or two digits of up to ten bits), so that a row's terms follow one another in the
+// order of the tokens: chunks of sorted tokens are summed by a wave each, and what passes a chunk's border
+// is joined afterwards, in order.  No atomics on values: results do not vary from run to run.
 #include "rlscan_embed.hpp"
 
 namespace rlscan {
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(const SortArgs p) {
         if (p.passes == 2) {
           // one lane counts for all twins that go to the same block of the second pass
           const int32_t block = to / (int32_t)p.per;
-          const int32_t before_me = lane > 0 ? 63 - __builtin_clzll(twins & ((1ull << lane) - 1) | 1) : 0;
+          const int32_t before_me = lane > 0 ? 63 - __builtin_clzll((twins & ((1ull << lane) - 1)) | 1) : 0;
           const bool has = (twins & ((1ull << lane) - 1)) != 0;
           const int32_t block_before = __shfl(block, has ? before_me : lane);
           const bool heads = !has || block_before != block;
@@ -386,10 +386,109 @@ __global__ void __launch_bounds__(64 * kJoinWaves) join_kernel(const SumArgs p) 
   }
 }
 
+// ------------------------------------------------------------------ few kinds of token
+// A wave adds its tokens' rows up in a table of its own in LDS, a block's waves in order to a share, and
+// the shares in order to the gradient: two launches and one pass over d_out, no sort.  Bound by memory
+// where there are many tokens (262144 x 256 float32: 53 us, 5.1 TB/s), by the latencies of two short kernels
+// where there are few (16384 x 250 of 18 kinds, float32: 7.7 and 2.9 us).
+// Up to 31 kinds and one for tokens out of range, pieces of two elements: four tables take 64 KiB at most, so
+// that two blocks share a compute unit.  Measured against the sort, us: 16384 x 250 float32, 18 kinds, 12
+// against 18; 262144 x 256 bfloat16, 4 kinds 36 against 95, 31 kinds 37 against 62, 64 kinds (one element a
+// lane) 80 against 58.  Pieces of four elements leave fewer waves to a compute unit: 8 kinds 58 against 44.
+constexpr int64_t kFewKinds = 31;
+constexpr int kFewWaves = 4, kFewAhead = 16;
+struct FewArgs {
+  GradArgs g;
+  float* part;  // [rows, N, D]
+  int64_t per;  // tokens of a share
+  int64_t rows;
+  uint32_t tiles;
+};
+
+template <class F, int V>
+__global__ void __launch_bounds__(64 * kFewWaves) few_kernel(const FewArgs p) {
+  using E = typename F::E;
+  extern __shared__ __align__(16) float few_table[];  // [kFewWaves, N + 1, 64 V]: the last for tokens out of range
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), N = (int)p.g.N;
+  const int size = (N + 1) * 64 * V;  // of a wave's table
+  const uint32_t row = blockIdx.x / p.tiles, tile = blockIdx.x % p.tiles;
+  const int64_t d = (int64_t)tile * 64 * V + lane * V;
+  const bool some = d < p.g.D;
+  float* const mine = few_table + w * size + lane * V;
+  for (int n = 0; n < N; ++n) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) mine[n * 64 * V + i] = 0.0f;
+  }
+  const int64_t share = p.per / kFewWaves, first = row * p.per + w * share;
+  const int64_t end = first + share < p.g.R ? first + share : p.g.R;
+  const E* const rows = static_cast<const E*>(p.g.d_out) + (some ? d : 0);
+  for (int64_t i0 = first; i0 < end; i0 += 64) {
+    const int64_t t = i0 + lane < end ? p.g.tokens[i0 + lane] : -1;
+    const int32_t key = t >= 0 && t < p.g.N ? (int32_t)t : N;
+    const int count = end - i0 < 64 ? (int)(end - i0) : 64;
+    for (int j0 = 0; j0 < count; j0 += kFewAhead) {
+      Piece<F, V> x[kFewAhead];
+#pragma unroll
+      for (int j = 0; j < kFewAhead; ++j)
+        x[j] = load_piece<F, V>(rows + (i0 + (j0 + j < count ? j0 + j : count - 1)) * p.g.o_stride);
+#pragma unroll
+      for (int j = 0; j < kFewAhead; ++j) {
+        // Every row is added, those past the end to the last table too: loads under a condition would go out
+        // one by one
+        float* const at = mine + __builtin_amdgcn_readlane(key, j0 + j) * 64 * V;
+#pragma unroll
+        for (int i = 0; i < V; ++i) at[i] += F::get(x[j].e[i]);
+      }
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < N * 64 * V; i += 64 * kFewWaves) {
+    float sum = few_table[i];
+#pragma unroll
+    for (int v = 1; v < kFewWaves; ++v) sum += few_table[v * size + i];
+    const int64_t column = (int64_t)tile * 64 * V + i % (64 * V);
+    if (column < p.g.D) p.part[(row * p.g.N + i / (64 * V)) * p.g.D + column] = sum;
+  }
+}
+
+constexpr int kFewGroups = 16;
+template <class F>
+__global__ void __launch_bounds__(64 * kFewGroups) few_join_kernel(const FewArgs p) {
+  __shared__ float s[kFewGroups][64];
+  const int lane = threadIdx.x & 63, group = threadIdx.x >> 6;
+  const int64_t columns = p.g.N * p.g.D, c = (int64_t)blockIdx.x * 64 + lane;
+  const int64_t share = (p.rows + kFewGroups - 1) / kFewGroups, from = group * share;
+  const int64_t to = from + share < p.rows ? from + share : p.rows;
+  float sum = 0.0f;
+  if (c < columns) {
+#pragma unroll 8
+    for (int64_t r = from; r < to; ++r) sum += p.part[r * columns + c];
+  }
+  s[group][lane] = sum;
+  __syncthreads();
+  if (group != 0 || c >= columns) return;
+#pragma unroll
+  for (int v = 1; v < kFewGroups; ++v) sum += s[v][lane];
+  const int64_t n = c / p.g.D;
+  static_cast<typename F::E*>(p.g.d_table)[n * p.g.t_stride + (c - n * p.g.D)] = F::put(p.g.scale * sum);
+}
+
 static int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
 
 Plan make_plan(int64_t R, int64_t N, int64_t D) {
   Plan p{};
+  if (N <= kFewKinds) {
+    // shares of 128 tokens and more, as many as fill the card
+    int64_t most = 65536 / D;
+    most = most > 512 ? 512 : most < 8 ? 8 : most;
+    const int64_t unit = 32 * kFewWaves, per = (R + most - 1) / most;
+    p.per = (per + unit - 1) / unit * unit;
+    if (p.per < unit) p.per = unit;
+    p.blocks = R > 0 ? (R + p.per - 1) / p.per : 1;
+    p.part = round16(p.blocks * N * D * 4);
+    p.bytes = p.part;
+    return p;
+  }
   int bits = 1;
   while (((int64_t)1 << bits) < N) ++bits;
   p.passes = bits <= 10 ? 1 : 2;
@@ -421,6 +520,22 @@ static hipError_t sums_of(const SumArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+template <class F, int V>
+static hipError_t few_of(FewArgs a, hipStream_t st) {
+  a.tiles = (uint32_t)((a.g.D + 64 * V - 1) / (64 * V));
+  few_kernel<F, V><<<dim3((unsigned)(a.rows * a.tiles)), 64 * kFewWaves, kFewWaves * (a.g.N + 1) * 64 * V * 4, st>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  few_join_kernel<F><<<dim3((unsigned)((a.g.N * a.g.D + 63) / 64)), 64 * kFewGroups, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+template <class F>
+static hipError_t few_fmt(const FewArgs& a, hipStream_t st) {
+  const bool pairs = piece_of(a.g.d_out, a.g.o_stride, a.g.d_out, a.g.o_stride, a.g.D, sizeof(typename F::E)) > 1;
+  return pairs ? few_of<F, 2>(a, st) : few_of<F, 1>(a, st);
+}
+
 template <class F>
 static hipError_t sums_fmt(const SumArgs& a, hipStream_t st) {
   switch (piece_of(a.g.d_out, a.g.o_stride, a.g.d_table, a.g.t_stride, a.g.D, sizeof(typename F::E))) {
@@ -435,6 +550,14 @@ static hipError_t sums_fmt(const SumArgs& a, hipStream_t st) {
 
 hipError_t launch_backward(rlscan_format f, const GradArgs& g, hipStream_t st) {
   const Plan p = make_plan(g.R, g.N, g.D);
+  if (g.N <= kFewKinds) {
+    const FewArgs a{g, static_cast<float*>(g.workspace), p.per, p.blocks, 0};
+    switch (f) {
+      case RLSCAN_FORMAT_BF16: return few_fmt<LBf16>(a, st);
+      case RLSCAN_FORMAT_F16: return few_fmt<LF16>(a, st);
+      default: return few_fmt<LF32>(a, st);
+    }
+  }
   char* ws = static_cast<char*>(g.workspace);
   auto take = [&](int64_t bytes) {
     char* at = ws;

@@ -293,7 +293,7 @@ def embed_tokens_backward(d_out, tokens, N, *, scale=1.0, d_table=None, stream=N
     """Gradient of the table of ``embed_tokens``: [N, D] in d_out's dtype.
 
     Row n is scale times the sum of d_out [..., D] over the tokens that are n, in float32 and
-    in the order of the tokens: the same from run to run.  Rows without a token are zero."""
+    in a fixed order: the same from run to run.  Rows without a token are zero."""
     if _p.torch is None:
         _p._import_torch()
     torch = _p.torch

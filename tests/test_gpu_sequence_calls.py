@@ -232,6 +232,34 @@ def test_one_token_of_no_dimension():
     assert torch.equal(got[4], d_out) and not got[[0, 1, 2, 3, 5, 6, 7, 8]].any()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("R,N,D", [(1, 1, 1), (127, 31, 2), (128, 32, 2), (129, 7, 130), (700, 31, 129), (700, 32, 129),
+                                   (5000, 2, 1), (70000, 3, 3)])
+def test_few_kinds_and_more(R, N, D, dtype):
+    # both sides of the number of kinds that are added up without a sort; one share, several, and all of them
+    g = torch.Generator().manual_seed(R + N)
+    tokens = torch.randint(-1, N + 1, (R,), generator=g)
+    d_out = torch.randn(R, D + 2, generator=g).to(dtype)
+    want, bound = so.table_gradient(d_out[:, :D], tokens, N, 0.7)
+    on = d_out.cuda()[:, :D]
+    for x in (on, on.contiguous()):
+        big = torch.full((N, D + 3), 5.0, dtype=dtype, device="cuda")
+        rl.embed_tokens_backward(x, tokens.cuda(), N, scale=0.7, d_table=big[:, 2:D + 2])
+        so.close(big[:, 2:D + 2], want, so.stored(want, bound, dtype), "gradient")
+        assert (big[:, :2] == 5).all() and (big[:, D + 2:] == 5).all()
+
+
+def test_few_kinds_not_finite():
+    tokens = torch.arange(600).remainder(5).cuda()
+    d_out = torch.randn(600, 40, device="cuda")
+    want = rl.embed_tokens_backward(d_out, tokens, 6)
+    d_out[7, 3], d_out[11, 4], d_out[599, 5] = math.inf, math.nan, -math.inf  # of tokens 2, 1 and 4
+    got = rl.embed_tokens_backward(d_out, tokens, 6)
+    bad = torch.zeros(6, 40, dtype=torch.bool, device="cuda")
+    bad[[2, 1, 4], [3, 4, 5]] = True
+    assert torch.equal(torch.isfinite(got), ~bad) and torch.equal(got[~bad], want[~bad])
+
+
 def test_no_tokens():
     table = torch.randn(9, 40, device="cuda")
     none = torch.empty(0, dtype=torch.int64, device="cuda")
