@@ -248,27 +248,50 @@ hipError_t launch_forward(rlscan_format f, const Args& a, const Plan& p, hipStre
   }
 }
 
-// Waves of a block and segments of a row.  A compute unit holds one block of the widest kind and
-// four (the gradients: two) of four waves.  Where a call's tiles do not fill the card, or fill a last
-// round of it badly, rows are cut into segments: their pairs take a pass over the inputs of their own, about
-// 0.6 (0.35) of the time of the walk.  The count that takes the fewest units by that reckoning:
-// Measured, bfloat16, us forward and backward with them and without: 20 tiles of 32768 steps 149 and 197
-// against 907 and 1491, 64 tiles of 4096 61 and 80 against 119 and 199, 264 tiles 321 backward against 399.
-Plan make_plan(int64_t E, int64_t T, int64_t D, bool backward) {
+// Waves of a block.  Sixteen walk a row in the fewest rounds, where there is no more than one tile for a
+// compute unit; of blocks of four a compute unit takes several, which fill each other's waits, and short
+// rows waste less of them.  A wave by itself waits for no other: for rows of one chunk, and where there are
+// many tiles and the last round of four would waste much.  Measured, bfloat16, us forward and backward:
+//   256 tiles of 4096 steps   16 waves 151 and 228   4 waves 179 and 251
+//   264 tiles of 4096                  245     333           218     300   (in segments, see below)
+//   384 tiles of 333                    28      49            26      42
+//   800 tiles of 128                    24      44            17      33   1 wave 20 and 33
+//   3200 tiles of 64                                          25      59          24     48
+//   3200 tiles of 16                                          16      60          12     22
+//   8000 tiles of 128                                        110     235         119    213
+//   8192 tiles of 256                                        229     425         240    487
+static int waves_of(int64_t tiles, int64_t T, bool backward) {
+  if (T <= kMark || (tiles >= 2048 && T < (backward ? 256 : 128))) return 1;
+  return T <= 4 * kMark || tiles > 256 ? 4 : kMaxWaves;
+}
+
+// Segments of a row.  Where a call's tiles do not fill the card, or leave some compute units one more than the
+// others, rows are cut into segments: their pairs take a pass over the inputs of their own, about 0.6 (0.35)
+// of the time of the walk.  A compute unit takes its blocks one after another if they are of sixteen waves,
+// and if they are of four each adds about 0.6 of the time of the first.  The count that is done first by that
+// reckoning.  Measured, bfloat16, us forward and backward with them and without: 20 tiles of 32768 steps 149
+// and 197 against 907 and 1491, 64 tiles of 4096 61 and 80 against 119 and 199, 264 tiles of 4096 222 and 314
+// against 266 and 382; and where the reckoning takes none, 384 tiles of 4096 forward 276 against 273.  Float32
+// is nearer to what memory gives, and more of its time is the second pass: 384 tiles 452 and 676 against 350 and
+// 619, 264 tiles 372 and 517 against 310 and 569.
+Plan make_plan(rlscan_format f, int64_t E, int64_t T, int64_t D, bool backward) {
   Plan p{};
   const int64_t tiles = E * ((D + 63) / 64);
-  p.waves = T <= kMark || tiles >= 4096 ? 1 : T <= 4 * kMark || tiles >= 1024 ? 4 : kMaxWaves;
+  p.waves = waves_of(tiles, T, backward);
   // segments: whole super-tiles of the widest block, whatever the block is
   const int64_t unit = (int64_t)kMaxWaves * kMark, units = (T + unit - 1) / unit;
-  const int64_t slots = p.waves == kMaxWaves ? 256 : p.waves == 4 ? (backward ? 512 : 1024) : 2048;
   const double pass = backward ? 0.35 : 0.6;
+  auto time = [&](int64_t blocks) {
+    const double each = (double)((blocks + 255) / 256);
+    return p.waves == kMaxWaves ? each : 0.4 + 0.6 * each;
+  };
   int64_t want = 1;
   double least = 0.0;
-  for (int64_t n = 1; tiles > 0 && tiles < 1024 && n <= 64 && (n == 1 || n <= units / 2); ++n) {
+  const int64_t most = f == RLSCAN_FORMAT_F32 ? 256 : 1023;  // tiles
+  for (int64_t n = 1; tiles > 0 && tiles <= most && n <= 64 && (n == 1 || n <= units / 2); ++n) {
     const int64_t per = (units + n - 1) / n;
-    const double rounds = (double)((tiles * n + slots - 1) / slots);
-    const double before = n > 1 ? pass * (double)((tiles * (n - 1) + slots - 1) / slots) : 0.0;
-    const double cost = (rounds + before) * (double)(per + 1);  // one more: a block's start and end
+    const double before = n > 1 ? pass * time(tiles * (n - 1)) : 0.0;
+    const double cost = (time(tiles * n) + before) * (double)(per + 1);  // one more: a block's start and end
     if (n == 1 || cost < 0.95 * least) {
       want = n;
       least = cost;

@@ -58,7 +58,7 @@ struct Plan {
   int64_t seg, part, more;  // floats of one array
   int64_t floats;      // workspace in all
 };
-Plan make_plan(int64_t E, int64_t T, int64_t D, bool backward);
+Plan make_plan(rlscan_format f, int64_t E, int64_t T, int64_t D, bool backward);
 
 hipError_t launch_forward(rlscan_format f, const Args& a, const Plan& p, hipStream_t st);
 hipError_t launch_backward(rlscan_format f, const Args& a, const Plan& p, hipStream_t st);

@@ -106,7 +106,7 @@ extern "C" {
 int64_t rlscan_gated_recurrence_workspace(rlscan_format fmt, int64_t E, int64_t T, int64_t D, int backward) {
   if (check_recurrence(fmt, E, T, D) != RLSCAN_OK) return -1;
   if (E * D == 0) return 0;
-  return rlscan::gr::make_plan(E, T, D, backward != 0).floats * (int64_t)sizeof(float);
+  return rlscan::gr::make_plan(fmt, E, T, D, backward != 0).floats * (int64_t)sizeof(float);
 }
 
 rlscan_status rlscan_gated_recurrence(rlscan_format fmt, rlscan_layout layout, const rlscan_heads* x,
@@ -118,7 +118,7 @@ rlscan_status rlscan_gated_recurrence(rlscan_format fmt, rlscan_layout layout, c
   if (st != RLSCAN_OK) return st;
   if (!layout_ok(layout)) return RLSCAN_ERR_PARAM;
   if (E * D == 0 || (T == 0 && !final_state)) return RLSCAN_OK;
-  const rlscan::gr::Plan p = rlscan::gr::make_plan(E, T, D, false);
+  const rlscan::gr::Plan p = rlscan::gr::make_plan(fmt, E, T, D, false);
   const int64_t need = p.floats * (int64_t)sizeof(float);
   rlscan::gr::Args a{};
   Spans io;
@@ -162,7 +162,7 @@ rlscan_status rlscan_gated_recurrence_backward(
   if (!layout_ok(layout)) return RLSCAN_ERR_PARAM;
   if (D == 0) return RLSCAN_OK;
   if (!rate || !d_rate) return RLSCAN_ERR_NULL;
-  const rlscan::gr::Plan p = rlscan::gr::make_plan(E, T, D, true);
+  const rlscan::gr::Plan p = rlscan::gr::make_plan(fmt, E, T, D, true);
   const int64_t need = E > 0 ? p.floats * (int64_t)sizeof(float) : 0;
   rlscan::gr::Args a{};
   Spans io;
