@@ -6,10 +6,15 @@
 //
 // Bound by memory: one read and one write of every head forward, two and one backward.  A
 // head lies on a group of lanes, V pairs to a lane: both members of a pair in one lane, so that
-// a rotation moves nothing between lanes, and 16-byte loads.  A group takes a token's
+// a rotation moves nothing between lanes.  A group takes a token's
 // heads one after another with its angles, which are made once for each token: in quarter
 // turns, in float64 (a position times a frequency keeps 2^-52 of itself, so far positions turn
 // like near ones), of which the part behind the point goes to a float32 sine and cosine.
+//
+// Measured: 32768 tokens of 16 and 4 heads of 128, bfloat16, forward 71 us (4.7 TB/s of those read and
+// written), gradients 117 (4.3) with 5 for the sums of the weights' gradients over blocks; 21312 tokens of 4
+// and 2 heads of 80, float32, 18 (4.5) and 40 (3.1): 10 of 16 lanes have a pair there, and one round of blocks is
+// short; a token for 16 environments 4 us, latency.
 #include <cmath>
 #include <type_traits>
 
@@ -25,7 +30,7 @@ using logits::LF32;
 
 constexpr int kThreads = 256;
 // Blocks of the gradients, each with its share of the weights' sums: as many as run at once (three to a
-// compute unit).
+// compute unit).  Measured, us, the bfloat16 case above: 256 blocks 160, 512 118, 768 115, 1024 129.
 constexpr int64_t kBackBlocks = 768;
 
 struct Turns {      // frequencies in quarter turns, as products of powers
@@ -420,7 +425,9 @@ Plan make_plan(rlscan_format f, const Args& a, bool backward) {
   const int64_t pairs = (a.D + 1) / 2;
   p.log_lanes = log2_up((pairs + p.V - 1) / p.V);
   const int64_t tokens = a.E * a.T, heads = a.heads[0] + a.heads[1], groups = kThreads >> p.log_lanes;
-  // Few tokens: their heads go to several groups, until there are 512 blocks
+  // Few tokens: their heads go to several groups, until there are 512 blocks, though each makes the angles
+  // again.  Measured, us: one token of 20 heads by one group 15, by four 12.3, by eight 12.8; 21312 tokens by
+  // one 20, by two 26
   p.split = tokens > 0 ? (512 * groups + tokens - 1) / tokens : 1;
   if (p.split > heads) p.split = heads;
   if (p.split < 1) p.split = 1;
@@ -433,7 +440,9 @@ Plan make_plan(rlscan_format f, const Args& a, bool backward) {
 
 template <class F, int V, bool VEC, bool BWD>
 static void run_heads(const KernelArgs& k, int64_t blocks, hipStream_t st) {
-  constexpr int kRing = BWD && sizeof(typename F::E) == 4 ? 1 : 2;
+  // Heads in flight, us: forward bfloat16 (32768 tokens of 20 heads) four 71, two 74; float32 (21312 of 6) two 18,
+  // four 19; backward bfloat16 two, float32, which keeps twice the registers of each, one.
+  constexpr int kRing = (BWD ? 2 : 4) / (sizeof(typename F::E) == 4 ? 2 : 1);
   if (k.a.interleaved) heads_kernel<F, V, VEC, true, BWD, kRing><<<dim3((unsigned)blocks), kThreads, 0, st>>>(k);
   else heads_kernel<F, V, VEC, false, BWD, kRing><<<dim3((unsigned)blocks), kThreads, 0, st>>>(k);
 }
