@@ -25,7 +25,8 @@ struct LookupArgs {
 };
 hipError_t launch_lookup(rlscan_format f, const LookupArgs& a, hipStream_t st);
 
-// How the gradient's tokens are sorted, or added up without; a function of R, N and D alone.
+// How the gradient's tokens are sorted, or added up without (all zero: by one launch, which needs no
+// workspace); a function of R, N and D alone.
 struct Plan {
   int64_t blocks, per;     // of the sort (or shares of the tokens), and tokens to each
   int passes, bits[2];     // digits, lowest first

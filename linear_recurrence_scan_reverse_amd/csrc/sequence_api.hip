@@ -361,8 +361,8 @@ rlscan_status rlscan_embed_tokens_backward(rlscan_format fmt, const void* d_out,
   const int es = elem_size(fmt);
   if (!stride_ok(N, table_stride, D) || !stride_ok(R, out_stride, D)) return RLSCAN_ERR_SHAPE;
   if (!std::isfinite(scale)) return RLSCAN_ERR_PARAM;
-  if (!d_table || !workspace || (R > 0 && (!d_out || !tokens))) return RLSCAN_ERR_NULL;
   const int64_t need = rlscan_embed_tokens_workspace(R, N, D);
+  if (!d_table || (need > 0 && !workspace) || (R > 0 && (!d_out || !tokens))) return RLSCAN_ERR_NULL;
   if (workspace_bytes < need) return RLSCAN_ERR_WORKSPACE;
   if (!aligned(d_table, es) || !aligned(tokens, 8) || !aligned(d_out, es) || !aligned(workspace, 16))
     return RLSCAN_ERR_ALIGN;

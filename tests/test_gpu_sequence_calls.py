@@ -233,10 +233,12 @@ def test_one_token_of_no_dimension():
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
-@pytest.mark.parametrize("R,N,D", [(1, 1, 1), (127, 31, 2), (128, 32, 2), (129, 7, 130), (700, 31, 129), (700, 32, 129),
-                                   (5000, 2, 1), (70000, 3, 3)])
+@pytest.mark.parametrize("R,N,D", [
+    (1, 1, 1), (3, 200, 64), (127, 31, 2), (256, 65, 130), (257, 64, 600), (1024, 33, 5), (1024, 3, 70),  # few tokens
+    (1025, 31, 2), (1025, 1, 130), (1500, 31, 129), (5000, 2, 1), (70000, 3, 3),                          # few kinds
+    (1025, 32, 130), (1500, 1000, 129), (1500, 1100, 3)])                                                 # sorted
 def test_few_kinds_and_more(R, N, D, dtype):
-    # both sides of the number of kinds that are added up without a sort; one share, several, and all of them
+    # both sides of the numbers of tokens and of kinds that are added up without a sort
     g = torch.Generator().manual_seed(R + N)
     tokens = torch.randint(-1, N + 1, (R,), generator=g)
     d_out = torch.randn(R, D + 2, generator=g).to(dtype)
@@ -249,15 +251,28 @@ def test_few_kinds_and_more(R, N, D, dtype):
         assert (big[:, :2] == 5).all() and (big[:, D + 2:] == 5).all()
 
 
-def test_few_kinds_not_finite():
-    tokens = torch.arange(600).remainder(5).cuda()
-    d_out = torch.randn(600, 40, device="cuda")
-    want = rl.embed_tokens_backward(d_out, tokens, 6)
-    d_out[7, 3], d_out[11, 4], d_out[599, 5] = math.inf, math.nan, -math.inf  # of tokens 2, 1 and 4
-    got = rl.embed_tokens_backward(d_out, tokens, 6)
-    bad = torch.zeros(6, 40, dtype=torch.bool, device="cuda")
+@pytest.mark.parametrize("R,N", [(600, 6), (2000, 6), (2000, 40), (2000, 2000)])
+def test_not_finite_stays_with_its_token(R, N):
+    tokens = torch.arange(R).remainder(5).cuda()
+    d_out = torch.randn(R, 40, device="cuda")
+    want = rl.embed_tokens_backward(d_out, tokens, N)
+    d_out[7, 3], d_out[11, 4], d_out[R - 1, 5] = math.inf, math.nan, -math.inf  # of tokens 2, 1 and 4
+    got = rl.embed_tokens_backward(d_out, tokens, N)
+    bad = torch.zeros(N, 40, dtype=torch.bool, device="cuda")
     bad[[2, 1, 4], [3, 4, 5]] = True
     assert torch.equal(torch.isfinite(got), ~bad) and torch.equal(got[~bad], want[~bad])
+
+
+@pytest.mark.parametrize("R,N", [(1024, 5000), (1024, 2), (3000, 5000), (3000, 2)])
+def test_one_token_many_times_and_padding_behind(R, N):
+    # all tokens but some padding are one; whole numbers, so that sums are exact
+    tokens = torch.full((R,), N - 1)
+    tokens[::7] = -1
+    tokens[-1] = N
+    d_out = torch.randint(-8, 9, (R, 30)).float()
+    want = d_out[tokens == N - 1].sum(0)
+    got = rl.embed_tokens_backward(d_out.cuda(), tokens.cuda(), N).cpu()
+    assert torch.equal(got[N - 1], want) and not got[:N - 1].any()
 
 
 def test_no_tokens():

@@ -240,7 +240,7 @@ def embed(lib, R=100, N=50, D=64, fmt=BF16, scale=1.0, table_stride=64, out_stri
     return lib.rlscan_embed_tokens(fmt, table, table_stride, tokens, out, out_stride, R, N, D, scale, None)
 
 
-def embed_backward(lib, R=100, N=50, D=64, fmt=BF16, scale=1.0, table_stride=64, out_stride=64, table=addr(0),
+def embed_backward(lib, R=2000, N=50, D=64, fmt=BF16, scale=1.0, table_stride=64, out_stride=64, table=addr(0),
                    tokens=addr(1), out=addr(2), ws=addr(3), need=None):
     if need is None:
         need = max(0, lib.rlscan_embed_tokens_workspace(R, N, D))
@@ -275,7 +275,8 @@ def test_table_refusals(lib, call):
 
 def test_table_workspace(lib):
     size = lib.rlscan_embed_tokens_workspace
-    assert size(0, 10, 8) > 0
+    assert size(1024, 1000, 8) == 0  # few tokens: one launch
+    assert size(1025, 10, 8) > 0 and size(1025, 1000, 8) > 0
     assert size(-1, 10, 8) == -1 and size(10, 0, 8) == -1 and size(10, 2 ** 21, 8) == -1 and size(10, 10, 0) == -1
     # four copies of the tokens, and two float32 rows for 32 tokens
     assert size(2 ** 20, 2 ** 16, 512) < 16 * 2 ** 20 + 2 ** 20 * 512 * 4 // 16 + (1 << 20)
