@@ -8,6 +8,11 @@
 // and dlog_a = e = 0 at a step that starts anew.  e runs backward like h runs forward, in
 // pairs of A and y.  The states h_{t-1} are computed again from the marks that the forward
 // call left every kMark steps.
+//
+// Bound by memory like the forward pass: four values read and three written a step.  A wave holds the 16
+// steps behind a mark.  What the decays are made of is read a round ahead, the rest (x, the input gate,
+// the mark) in the round that uses it, behind the barrier: all of it ahead would leave one wave to a SIMD.
+// Measured: 64 x 333 x 768 float32 91 us (5.0 TB/s), 8 x 4096 x 2048 bfloat16 212 (4.4).
 #include "rlscan_gr.hpp"
 #include "rlscan_sums.hpp"
 
@@ -285,7 +290,7 @@ static hipError_t backward_waves(const Args& a, hipStream_t st) {
   backward_kernel<F, S, W, NEAR><<<dim3((unsigned)(a.groups * a.nseg * tiles)), 64 * W, 0, st>>>(a, (uint32_t)tiles);
   e = hipGetLastError();
   if (e != hipSuccess || !a.rate_part) return e;
-  return sums::launch_columns(a.rate_part, a.groups * a.nseg, a.rate_more, a.d_rate, a.D, nullptr, 0, st);
+  return sums::launch_columns(a.rate_part, a.groups * a.nseg, a.d_rate, a.D, nullptr, 0, st);
 }
 
 template <class F>

@@ -1,6 +1,15 @@
 // The gated recurrence over whole rows (rlscan_gated_recurrence).
+//
+// Bound by memory: three values read and one written a step, against about 30 vector instructions, seven of
+// them transcendental.  A lane holds a channel, so that rows of 64 channels are read whole; a wave holds
+// eight steps, whose coefficients stay in registers between the two uses of them: the pair that the block's
+// other waves need, and the states once the one that enters is known.  One barrier for every W chunks, and the
+// next ones' loads in flight across it.
+//
+// Measured (bytes read and written once): 64 x 333 x 768 float32 54 us (4.8 TB/s), 8 x 4096 x 2048 bfloat16 135
+// (4.0), 1 x 32768 x 1280 bfloat16 in 12 segments 53 for their pairs and 82 for the states (2.5 in all).  Rows
+// of 64 bfloat16 are 128 bytes, and loads and stores of that size alone, four streams, take 110 us of the 135.
 #include "rlscan_gr.hpp"
-#include "rlscan_sums.hpp"
 
 namespace rlscan {
 namespace gr {
@@ -303,12 +312,11 @@ Plan make_plan(rlscan_format f, int64_t E, int64_t T, int64_t D, bool backward) 
   p.seg = p.nseg > 1 ? (E * p.nseg * D + 3) / 4 * 4 : 0;
   p.groups = E;
   if (backward) {
-    const int64_t columns = (D + 63) / 64, most = 8192 / (columns * p.nseg) + 1;
+    const int64_t columns = (D + 63) / 64, most = 4096 / (columns * p.nseg) + 1;  // about: blocks
     if (p.groups > most) p.groups = most;
     p.part = p.groups * p.nseg > 1 ? (p.groups * p.nseg * D + 3) / 4 * 4 : 0;
-    p.more = sums::more_floats(p.groups * p.nseg, D);
   }
-  p.floats = 2 * p.seg + p.part + p.more;
+  p.floats = 2 * p.seg + p.part;
   return p;
 }
 

@@ -469,7 +469,7 @@ static hipError_t run_fmt(rlscan_format f, const Args& a, hipStream_t st) {
   if (!BWD || e != hipSuccess || (!a.d_weight[0] && !a.d_weight[1])) return e;
   // the sums of a weight that is not asked for are left unread
   const int64_t D = a.D;
-  return sums::launch_columns(a.part, p.blocks, nullptr, a.d_weight[0], D, a.d_weight[1], D, st);
+  return sums::launch_columns(a.part, p.blocks, a.d_weight[0], D, a.d_weight[1], D, st);
 }
 
 hipError_t launch_forward(rlscan_format f, const Args& a, hipStream_t st) {

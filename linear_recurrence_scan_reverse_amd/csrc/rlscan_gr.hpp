@@ -46,7 +46,6 @@ struct Args {
   float* seg_y;
   float* d_rate;          // [D]
   float* rate_part;       // workspace [groups * nseg, D]
-  float* rate_more;       // workspace of the sum of rate_part's rows
   int64_t E, T, D;
   int64_t nseg, seg_steps;  // steps of a segment, a multiple of what a block takes at once
   int64_t groups;           // backward: blocks take the rows e, e + groups, ...
@@ -55,7 +54,7 @@ struct Args {
 struct Plan {
   int waves;           // of a block
   int64_t nseg, seg_steps, groups;
-  int64_t seg, part, more;  // floats of one array
+  int64_t seg, part;   // floats of one array
   int64_t floats;      // workspace in all
 };
 Plan make_plan(rlscan_format f, int64_t E, int64_t T, int64_t D, bool backward);

@@ -52,7 +52,6 @@ void fill_recurrence(rlscan::gr::Args& a, const rlscan::gr::Plan& p, rlscan_layo
   a.seg_a = ws;
   a.seg_y = ws + p.seg;
   a.rate_part = p.part > 0 ? ws + 2 * p.seg : nullptr;
-  a.rate_more = ws + 2 * p.seg + p.part;
 }
 
 // Sizes that the entries of the heads take.
