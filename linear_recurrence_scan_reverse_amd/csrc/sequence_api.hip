@@ -1,5 +1,6 @@
 // sequence_api.hip -- the C ABI of what a policy over token sequences has besides attention
-// and sampling (declared in include/rlscan.h): the gated recurrence.  Every entry validates
+// and sampling (declared in include/rlscan.h): the gated recurrence, normalised and rotated heads,
+// and rows of a table by token.  Every entry validates
 // on the host before any HIP call and enqueues its kernels on the caller's stream; scratch
 // memory comes from the caller.
 #include <cmath>
