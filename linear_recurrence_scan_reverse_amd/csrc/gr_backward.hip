@@ -67,7 +67,7 @@ __device__ __forceinline__ void decays(Decays<S>& c, const Chunk<F, S>& in, floa
 template <class F, int S, bool NEAR>
 struct Tensors {
   Stream<F, S, NEAR> g, dg, x, ig, dx, dig, ddg;
-  // bytes from a step to the next; NEAR: of d_out, of the inputs, of the outputs
+  // bytes from a step to the next
   int64_t g_st, dg_st, x_st, ig_st, dx_st, dig_st, ddg_st;
   const uint8_t* done;
   int64_t done_step, mark_step;
@@ -84,10 +84,10 @@ struct Tensors {
     g_st = p.dout.st * es;
     dg_st = p.dg.st * es;
     dx_st = p.dx.st * es;
-    x_st = NEAR ? dg_st : p.x.st * es;
-    ig_st = NEAR ? dg_st : p.ig.st * es;
-    dig_st = NEAR ? dx_st : p.dig.st * es;
-    ddg_st = NEAR ? dx_st : p.ddg.st * es;
+    x_st = p.x.st * es;
+    ig_st = p.ig.st * es;
+    dig_st = p.dig.st * es;
+    ddg_st = p.ddg.st * es;
   }
   __device__ __forceinline__ void load(Chunk<F, S>& c, int t, int end) const {
     dg.load(c.dg, t, end, Steps<S, NEAR>(dg_st, t, end), at);
@@ -296,9 +296,8 @@ static hipError_t backward_waves(const Args& a, hipStream_t st) {
 template <class F>
 static hipError_t backward_fmt(const Args& a, const Plan& p, hipStream_t st) {
   constexpr int64_t es = sizeof(typename F::E);
-  const View *in[] = {&a.dg, &a.x, &a.ig}, *out[] = {&a.dx, &a.dig, &a.ddg}, *grad[] = {&a.dout};
-  if (!near_alike(in, 3, es) || !near_alike(out, 3, es) || !near_alike(grad, 1, es))
-    return backward_waves<F, kMark, kBackWaves, false>(a, st);
+  const View* const v[] = {&a.dout, &a.x, &a.ig, &a.dg, &a.dx, &a.dig, &a.ddg};
+  if (!all_near(v, 7, es)) return backward_waves<F, kMark, 1, false>(a, st);  // as the forward pass
   switch (p.waves) {
     case 1: return backward_waves<F, kMark, 1, true>(a, st);
     case 4: return backward_waves<F, kMark, 4, true>(a, st);

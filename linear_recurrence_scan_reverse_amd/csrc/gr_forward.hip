@@ -71,7 +71,7 @@ __device__ __forceinline__ float states(const Coefficients<S>& c, float h, const
 template <class F, int S, bool NEAR>
 struct Inputs {
   Stream<F, S, NEAR> x, ig, dg;
-  int64_t st[NEAR ? 1 : 3];  // bytes from a step to the next
+  int64_t st[3];  // bytes from a step to the next
   const uint8_t* done;
   int64_t done_step;
   int lane;
@@ -81,22 +81,14 @@ struct Inputs {
       : x(p.x, e, d0), ig(p.ig, e, d0), dg(p.dg, e, d0), done(p.done ? p.done + e * p.d_se : nullptr),
         done_step(p.d_st), lane(lane_), at(col * (uint32_t)sizeof(typename F::E)) {
     st[0] = p.dg.st * (int64_t)sizeof(typename F::E);
-    if constexpr (!NEAR) {
-      st[1] = p.ig.st * (int64_t)sizeof(typename F::E);
-      st[2] = p.x.st * (int64_t)sizeof(typename F::E);
-    }
+    st[1] = p.ig.st * (int64_t)sizeof(typename F::E);
+    st[2] = p.x.st * (int64_t)sizeof(typename F::E);
   }
   __device__ __forceinline__ void load(Chunk<F, S>& c, int t, int end) const {
     using At = Steps<S, NEAR>;
-    const At steps(st[0], t, end);
-    dg.load(c.dg, t, end, steps, at);
-    if constexpr (NEAR) {
-      ig.load(c.ig, t, end, steps, at);
-      x.load(c.x, t, end, steps, at);
-    } else {
-      ig.load(c.ig, t, end, At(st[1], t, end), at);
-      x.load(c.x, t, end, At(st[2], t, end), at);
-    }
+    dg.load(c.dg, t, end, At(st[0], t, end), at);
+    ig.load(c.ig, t, end, At(st[1], t, end), at);
+    x.load(c.x, t, end, At(st[2], t, end), at);
     c.flag = load_flag<S>(done, done_step, t, end, lane);
   }
 };
@@ -240,8 +232,11 @@ static hipError_t forward_waves(const Args& a, hipStream_t st) {
 template <class F>
 static hipError_t forward_fmt(const Args& a, const Plan& p, hipStream_t st) {
   constexpr int64_t es = sizeof(typename F::E);
-  const View *in[] = {&a.x, &a.ig, &a.dg}, *out[] = {&a.out};
-  if (!near_alike(in, 3, es) || !near_alike(out, 1, es)) return forward_waves<F, 8, kMaxWaves, false>(a, st);
+  const View* const v[] = {&a.x, &a.ig, &a.dg, &a.out};
+  // Steps 2^27 bytes apart or more are those of time-major windows of a million tiles and more, for which a
+  // wave by itself is enough; 32-bit offsets take 13 and 23 us where 64-bit ones and blocks of 16 waves took 124
+  // and 383 (512 x 16 x 512, bfloat16).
+  if (!all_near(v, 4, es)) return forward_waves<F, 8, 1, false>(a, st);
   switch (p.waves) {
     case 1: return forward_waves<F, 8, 1, true>(a, st);
     case 4: return forward_waves<F, 8, 4, true>(a, st);

@@ -130,7 +130,7 @@ __device__ __forceinline__ uint16_t apart(uint16_t x) {
 }
 
 // The steps of a chunk as offsets from its first: t + k, or the row's last step where that is past
-// the end.  Tensors of equal strides share them.  NEAR: 32-bit offsets of buffer instructions.
+// the end.  NEAR: 32-bit offsets of buffer instructions.
 template <int S, bool NEAR>
 struct Steps {
   int64_t st;  // bytes from a step to the next
@@ -179,10 +179,10 @@ struct Stream {
   }
 };
 
-// Whether tensors go by one stride, with a chunk within 2^31 bytes.
-inline bool near_alike(const View* const* v, int n, int64_t es) {
+// Whether a chunk of each tensor lies within 2^31 bytes.
+inline bool all_near(const View* const* v, int n, int64_t es) {
   for (int i = 0; i < n; ++i)
-    if (v[i]->st != v[0]->st || v[i]->st * es >= (int64_t)1 << 27) return false;
+    if (v[i]->st * es >= (int64_t)1 << 27) return false;
   return true;
 }
 

@@ -144,6 +144,25 @@ def test_heads_and_rows_that_are_shared():
         rl.embed_tokens_backward(d_out, tokens, 7)
 
 
+@pytest.mark.parametrize("T", [1, 17, 40])
+def test_steps_far_apart(T):
+    # steps 2^27 bytes and more from one another: offsets of 64 bits
+    E, D, far = 2, 70, 2 ** 26 + 96
+    d = draw(E, T, D, torch.bfloat16, seed=23)
+    c = on_gpu(d)
+
+    def wide(x):
+        b = torch.empty((T - 1) * far + E * D, dtype=torch.bfloat16, device="cuda").as_strided((E, T, D), (D, far, 1))
+        return b.copy_(x)
+
+    s = dict(c, x=wide(c["x"]))
+    got = rl.gated_recurrence(s["x"], s["ig"], s["dg"], s["rate"], s["done"], s["init"], with_state=True,
+                              with_marks=True, out=wide(c["x"] * 0))
+    grads = rl.gated_recurrence_backward(s["d_out"], s["x"], s["ig"], s["dg"], s["rate"], got[2], s["done"],
+                                         s["d_final"], dx=wide(c["x"] * 0))
+    check(d, got, grads)
+
+
 # ------------------------------------------------------------------ rows in windows
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("T,cut", [(5, 1), (40, 16), (1300, 777), (2100, 1024)])
