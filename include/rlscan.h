@@ -623,7 +623,7 @@ rlscan_status rlscan_embed_tokens(rlscan_format fmt, const void *table, int64_t 
 /* Gradient of the table: d_table_n = scale * sum of d_out_r over the tokens n, in
  * float32 and in a fixed order, rounded once; every row is written, rows without a
  * token with zeros, and padding adds to none.  Results do not vary from run to run.
- * The workspace is of rlscan_embed_tokens_workspace bytes. */
+ * The workspace is of rlscan_embed_tokens_workspace bytes, none for up to 1024 tokens (it may then be NULL). */
 int64_t rlscan_embed_tokens_workspace(int64_t R, int64_t N, int64_t D);
 
 rlscan_status rlscan_embed_tokens_backward(rlscan_format fmt, const void *d_out, int64_t out_stride,

@@ -66,7 +66,7 @@ def gated_recurrence(x, input_gate, decay_gate, rate, done=None, init_state=None
     ``done`` has a_t = 0, whatever the state was: inf and NaN stay within their episode.
 
     x, input_gate, decay_gate [E, T, D] (``time_major``: [T, E, D]); rate [D] float32, not
-    negative; done [E, T]; init_state [E, D] float32; reset [E]: rows whose step before the first
+    negative; done [E, T] (or [T, E]); init_state [E, D] float32; reset [E]: rows whose step before the first
     ended an episode (the last column of the window before's done).  Returns out, h in x's dtype, followed
     by final_state [E, D] with ``with_state`` or ``final_state`` (what the next window takes as
     init_state) and by marks [E, ceil(T / 16), D] float32 with ``with_marks`` or ``marks``
