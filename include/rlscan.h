@@ -582,7 +582,7 @@ rlscan_status rlscan_gated_recurrence_step(rlscan_format fmt, const rlscan_heads
  * Angles are made in float64, sums and all else in float32 (mean(x^2) past its range: 0).
  * In:  q [E,T,H,D], k [E,T,Hk,D] in fmt (H or Hk may be 0); q_weight, k_weight [D]
  *      (optional: ones); positions [E,T] int32 in the layout, of either sign
- *      (not read, and optional, if rotate is 0).
+ *      (not read, and optional, if rotate is 0 or there are no heads).
  * Out: q_out, k_out like q, k, rounded once.
  * H + Hk <= 2^20, 1 <= D <= RLSCAN_MAX_NORM_DIM, rotate even and at most D, base > 0, eps >= 0 (with
  * eps 0 a row of zeros gives NaN). */

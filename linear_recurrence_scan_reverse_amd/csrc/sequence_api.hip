@@ -60,6 +60,7 @@ rlscan_status check_heads(rlscan_format f, int64_t E, int64_t T, int64_t H, int6
                           float base, float eps) {
   if (E < 0 || T < 0 || T >= RLSCAN_MAX_T || H < 0 || Hk < 0) return RLSCAN_ERR_SHAPE;
   if (D < 1 || D > RLSCAN_MAX_NORM_DIM || rotate < 0 || rotate > D || rotate % 2 != 0) return RLSCAN_ERR_SHAPE;
+  if (E > 0 && T > kMaxElems / E) return RLSCAN_ERR_SHAPE;  // tokens are counted where there are no heads too
   if (H > kMaxHeads || H + Hk > kMaxHeads || (E > 0 && H + Hk > kMaxElems / D / E)) return RLSCAN_ERR_SHAPE;
   if (E * (H + Hk) > 0 && T > kMaxElems / D / (E * (H + Hk))) return RLSCAN_ERR_SHAPE;
   if (elem_size(f) == 0) return RLSCAN_ERR_PARAM;
@@ -314,13 +315,14 @@ rlscan_status rlscan_norm_rotate_heads_backward(
     return RLSCAN_ERR_ALIGN;
   io.add_in(plain(q_weight, D * 4));
   io.add_in(plain(k_weight, D * 4));
-  if (rotate > 0) io.add_in(plain(positions, E * T * 4));
+  if (some && rotate > 0) io.add_in(plain(positions, E * T * 4));
   io.add_out(plain(d_q_weight, D * 4));
   io.add_out(plain(d_k_weight, D * 4));
   io.add_out(plain(workspace, need));
   if (io.clash()) return RLSCAN_ERR_ALIAS;
-  fill_heads(a, layout, q_weight, k_weight, positions, E, T, some ? H : 0, some ? Hk : 0, D, rotate, base, interleaved,
-             eps);
+  // Without heads there are no tokens either: their positions may be NULL, and only zeros are written.
+  fill_heads(a, layout, q_weight, k_weight, positions, some ? E : 0, T, some ? H : 0, some ? Hk : 0, D, rotate, base,
+             interleaved, eps);
   a.part = static_cast<float*>(workspace);
   a.d_weight[0] = d_q_weight;
   a.d_weight[1] = d_k_weight;
