@@ -522,7 +522,8 @@ rlscan_status rlscan_action_log_probs_backward(rlscan_format fmt, const float *d
  *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t,
  * the generic recurrence x_t = a_t x_{t-1} + b_t with coefficients made from the
  * two gates' logits i_t and r_t; a step after one flagged in `done` has a_t = 0,
- * whatever r_t is, so that inf and NaN stay within their episode.
+ * whatever r_t is, so that inf and NaN stay within their episode; an infinite state stays
+ * infinite as long as its episode lasts.
  * In:  x, input_gate (i), decay_gate (r) [E,T,D] in fmt (rlscan_heads with head
  *      unused); rate [D], >= 0 (below: NaN in the channel); done [E,T] in the
  *      layout (optional); reset [E] (optional): rows whose step before the first

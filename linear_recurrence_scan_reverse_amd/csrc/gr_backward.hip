@@ -32,34 +32,36 @@ struct Rest {
   float mark;
 };
 
-// sigmoid(r) and a - 1 of every step, the sum of y (logarithms of the decays) and what leaves
+// sigmoid(r) and the decay (decay_of) of every step, the sum of y (logarithms of the decays) and what leaves
 // the chunk to the steps before it for an entering e of 0.
 template <int S>
 struct Decays {
-  float sr[S], em1[S];
+  float sr[S], a[S];
   float L, out;
 };
 
-// CARE: some steps start anew (cut) or lie past the end (not live).
-template <class F, int S, bool CARE>
-__device__ __forceinline__ void decays(Decays<S>& c, const Chunk<F, S>& in, float rate2, uint32_t cut, uint32_t live) {
+// less: see decay_of, for kEvery.
+template <class F, int S, Form FORM>
+__device__ __forceinline__ void decays(Decays<S>& c, const Chunk<F, S>& in, float rate2, float less, uint32_t cut,
+                                       uint32_t live) {
+#pragma clang fp contract(off)
   c.L = c.out = 0.0f;
 #pragma unroll
   for (int k = S - 1; k >= 0; --k) {
-    const float dg = F::get(CARE ? apart(in.dg[k]) : in.dg[k]);
-    float g = F::get(CARE ? apart(in.g[k]) : in.g[k]);
-    float sr = sigmoid(dg), y = rate2 * sr, em1 = decay_less_1(y);
-    if (CARE) {
+    const float dg = F::get(FORM != kPlain ? apart(in.dg[k]) : in.dg[k]);
+    float g = F::get(FORM != kPlain ? apart(in.g[k]) : in.g[k]);
+    float sr = sigmoid(dg), y = rate2 * sr, a = decay_of<FORM>(y, FORM == kEvery ? less : 1.0f);
+    if (FORM != kPlain) {
       sr = keep(sr, spread(live & ~cut, k));  // the gate of a step that starts anew is not looked at: it may be NaN
-      em1 = keep(pick(spread(cut, k), -1.0f, em1), spread(live, k));
+      a = decay_before<FORM>(decay_behind<FORM>(a, spread(cut, k)), spread(live, k));
       y = keep(y, spread(live, k));
       g = keep(g, spread(live, k));
     }
     c.sr[k] = sr;
-    c.em1[k] = em1;
+    c.a[k] = a;
     c.L += y;
-    c.out = decayed(em1, c.out + g);
-    if (CARE) c.out = keep(c.out, ~spread(cut, k));
+    c.out = decayed<FORM>(a, c.out + g);
+    if (FORM != kPlain) c.out = keep(c.out, ~spread(cut, k));
   }
 }
 
@@ -102,117 +104,147 @@ struct Tensors {
 };
 
 // The gradients of a chunk, from the e that enters it, to memory; returns the e that leaves it.
-template <class F, int S, bool NEAR, bool CARE>
-__device__ __forceinline__ float gradients(const Decays<S>& c, const Chunk<F, S>& in, const Rest<F, S>& rest, float e,
-                                           float rate, float& d_rate, const Tensors<F, S, NEAR>& to, int t,
+template <class F, int S, bool NEAR, Form FORM>
+__device__ __forceinline__ float gradients(Decays<S>& c, const Chunk<F, S>& in, const Rest<F, S>& rest, float e,
+                                           float& odd, float rate, float& d_rate, const Tensors<F, S, NEAR>& to, int t,
                                            uint32_t out_at, uint32_t cut, uint32_t live) {
+#pragma clang fp contract(off)
   float before[S], u[S], si[S];
   float h = rest.mark;
 #pragma unroll
   for (int k = 0; k < S; ++k) {
-    si[k] = sigmoid(F::get(CARE ? apart(rest.ig[k]) : rest.ig[k]));
-    u[k] = si[k] * F::get(CARE ? apart(rest.x[k]) : rest.x[k]);
-    if (CARE) h = keep(h, ~spread(cut, k));
+    si[k] = sigmoid(F::get(FORM != kPlain ? apart(rest.ig[k]) : rest.ig[k]));
+    u[k] = si[k] * F::get(FORM != kPlain ? apart(rest.x[k]) : rest.x[k]);
+    if (FORM != kPlain) h = keep(h, ~spread(cut, k));
     before[k] = h;
-    h = decayed(c.em1[k], h) + __builtin_amdgcn_sqrtf(one_less_square(c.em1[k])) * u[k];
+    if (FORM == kCut && k % 2 == 1) odd = seen(odd, before[k - 1], h);  // the next cut would hide them
+    if (FORM == kEvery) c.a[k] = apart(c.a[k]);  // 16 masks of which is held as a - 1 would lie in scalars for long
+    h = __builtin_fmaf(__builtin_amdgcn_sqrtf(one_less_square<FORM>(c.a[k])), u[k], decayed<FORM>(c.a[k], h));
   }
+  if (FORM != kEvery) odd = seen(odd, h);
+  float after = 0.0f;
 #pragma unroll
   for (int k = S - 1; k >= 0; --k) {
-    float g = F::get(CARE ? apart(in.g[k]) : in.g[k]);
-    if (CARE) g = keep(g, spread(live, k));
+    float g = F::get(FORM != kPlain ? apart(in.g[k]) : in.g[k]);
+    if (FORM != kPlain) g = keep(g, spread(live, k));
     g += e;
-    const float m2 = one_less_square(c.em1[k]);
+    if (FORM == kCut && k % 2 == 0) odd = seen(odd, after, g);
+    after = g;
+    if (FORM == kEvery) c.a[k] = apart(c.a[k]);
+    const float m2 = one_less_square<FORM>(c.a[k]);
     const float over_m = m2 >= 1.1754944e-38f ? __builtin_amdgcn_rsqf(m2) : 0.0f;  // a held state has no part in u
     const float du = m2 * over_m * g, ud = u[k] * du;
-    e = decayed(c.em1[k], g);
-    if (CARE) e = keep(e, ~spread(cut, k));
+    e = decayed<FORM>(c.a[k], g);
+    if (FORM != kPlain) e = keep(e, ~spread(cut, k));
     // a g (h - u a / m): the gradient of log a
-    const float a = 1.0f + c.em1[k];
-    float part = c.sr[k] * (e * (before[k] - u[k] * over_m * a));
-    if (CARE) part = keep(part, spread(live & ~cut, k));
+    const float a = decayed<FORM>(c.a[k], 1.0f);
+    float part = c.sr[k] * (e * __builtin_fmaf(-(u[k] * over_m), a, before[k]));
+    if (FORM != kPlain) part = keep(part, spread(live & ~cut, k));
     d_rate -= part;
-    if (!CARE || (live >> k) & 1) {
+    if (FORM == kPlain || (live >> k) & 1) {
       to.dx.store(F::put(si[k] * du), t, k, to.dx_st, out_at);
-      to.dig.store(F::put(ud - ud * si[k]), t, k, to.dig_st, out_at);
-      to.ddg.store(F::put((rate * c.sr[k] - rate) * part), t, k, to.ddg_st, out_at);
+      float di = apart(__builtin_fmaf(-ud, si[k], ud));  // of float32 first: an instruction rounds to float16 at once
+      if (FORM == kEvery) di = __builtin_isinf(ud) ? ud * (1.0f - si[k]) : di;
+      to.dig.store(F::put(di), t, k, to.dig_st, out_at);
+      to.ddg.store(F::put(__builtin_fmaf(rate, c.sr[k], -rate) * part), t, k, to.ddg_st, out_at);
     }
   }
+  if (FORM != kEvery) odd = seen(odd, e);
   return e;
 }
 
 // The pair of each segment but the first: a wave takes a share of it, chunk after chunk, from the end.
+// Returns whether the share is for the walk that looks at everything (EVERY).
+template <class F, int S, int W, bool NEAR, bool EVERY>
+__device__ __forceinline__ bool fold_back_walk(const Args& p, uint32_t tile, uint32_t es, int w, int lane, float& A,
+                                               float& y) {
+  const uint32_t nseg = (uint32_t)p.nseg;
+  const int64_t seg = es % (nseg - 1) + 1, e = es / (nseg - 1), d0 = tile * 64;
+  const uint32_t col = d0 + lane < p.D ? lane : (uint32_t)(p.D - 1 - d0);  // loads stay inside the row
+  const float rate = rate_of(p.rate[d0 + col]), rate2 = kLog2E * rate;
+  const Tensors<F, S, NEAR> in(p, e, d0, lane, col);
+  const int share = (int)p.seg_steps / W, begin = (int)seg * (int)p.seg_steps + w * share;
+  const int end = (int)p.T < begin + share ? (int)p.T : begin + share;  // the last segment may be short
+  float total = 0.0f;
+  bool dropped = false;
+  A = 1.0f;
+  y = 0.0f;
+  if (begin >= end) return false;
+  if (!EVERY && any_quick(rate)) return true;
+  Chunk<F, S> one, two;
+  int t = begin + (end - begin - 1) / S * S;
+  in.load(one, t, end);
+  const float less = EVERY ? less_of(rate) : 1.0f;
+  auto fold = [&](const Chunk<F, S>& c, uint32_t live) __attribute__((always_inline)) {
+    const uint32_t cut = flag_word(c.flag, 1, 0);  // never the row's first step
+    Decays<S> k;
+    by_form<EVERY>(cut == 0 && live == (1u << S) - 1, [&](auto form) __attribute__((always_inline)) {
+      decays<F, S, form>(k, c, rate2, less, cut, live);
+    });
+    total += k.L;
+    dropped |= cut != 0;
+    y = enter<EVERY>(cut ? kDropped : exp2_fast(-k.L), k.out, y);
+  };
+  for (;;) {
+    in.load(two, t > begin ? t - S : begin, end);
+    fold(one, live_word<S>(t, end));
+    if (t == begin) break;
+    t -= S;
+    in.load(one, t > begin ? t - S : begin, end);
+    fold(two, (1u << S) - 1);
+    if (t == begin) break;
+    t -= S;
+  }
+  A = dropped ? kDropped : exp2_fast(-total);
+  return any_odd(seen(0.0f, y));
+}
+
 template <class F, int S, int W, bool NEAR>
 __global__ void __launch_bounds__(64 * W) fold_back_kernel(const Args p, uint32_t tiles) {
   __shared__ float s_a[W][64], s_y[W][64];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t tile = blockIdx.x % tiles, es = blockIdx.x / tiles, nseg = (uint32_t)p.nseg;
-  const int64_t seg = es % (nseg - 1) + 1, e = es / (nseg - 1), d0 = tile * 64;
-  const bool column = d0 + lane < p.D;
-  const uint32_t col = column ? lane : (uint32_t)(p.D - 1 - d0);  // loads stay inside the row
-  const float rate2 = kLog2E * p.rate[d0 + col];
-  const Tensors<F, S, NEAR> in(p, e, d0, lane, col);
-  const int share = (int)p.seg_steps / W, begin = (int)seg * (int)p.seg_steps + w * share;
-  const int end = (int)p.T < begin + share ? (int)p.T : begin + share;  // the last segment may be short
-  float total = 0.0f, y = 0.0f;
-  bool dropped = false;
-  auto fold = [&](const Chunk<F, S>& c, uint32_t live) __attribute__((always_inline)) {
-    const uint32_t cut = flag_word(c.flag, 1, 0);  // never the row's first step
-    Decays<S> k;
-    if (cut == 0 && live == (1u << S) - 1) decays<F, S, false>(k, c, rate2, 0, 0);
-    else decays<F, S, true>(k, c, rate2, cut, live);
-    total += k.L;
-    dropped |= cut != 0;
-    y = enter(cut ? kDropped : exp2_fast(-k.L), k.out, y);
-  };
-  if (begin < end) {
-    Chunk<F, S> one, two;
-    int t = begin + (end - begin - 1) / S * S;
-    in.load(one, t, end);
-    for (;;) {
-      in.load(two, t > begin ? t - S : begin, end);
-      fold(one, live_word<S>(t, end));
-      if (t == begin) break;
-      t -= S;
-      in.load(one, t > begin ? t - S : begin, end);
-      fold(two, (1u << S) - 1);
-      if (t == begin) break;
-      t -= S;
-    }
-  }
-  s_a[w][lane] = dropped ? kDropped : exp2_fast(-total);
+  const uint32_t tile = blockIdx.x % tiles, es = blockIdx.x / tiles;
+  float A, y;
+  if (fold_back_walk<F, S, W, NEAR, false>(p, tile, es, w, lane, A, y))
+    fold_back_walk<F, S, W, NEAR, true>(arguments_again(), again(tile), again(es), again(w), la::rarely(lane), A,
+                                        y);
+  s_a[w][lane] = A;
   s_y[w][lane] = y;
   __syncthreads();
-  if (w == 0 && column) {
+  const int64_t column = (int64_t)tile * 64 + lane;
+  if (w == 0 && column < p.D) {
     float A = 1.0f, out = 0.0f;
     for (int v = W - 1; v >= 0; --v) {
       out = enter(s_a[v][lane], s_y[v][lane], out);
       A = A < 0.0f || s_a[v][lane] < 0.0f ? kDropped : A * s_a[v][lane];
     }
-    const int64_t at = (e * p.nseg + seg) * p.D + d0 + lane;
+    const uint32_t nseg = (uint32_t)p.nseg;
+    const int64_t at = ((int64_t)(es / (nseg - 1)) * nseg + es % (nseg - 1) + 1) * p.D + column;
     p.seg_a[at] = A;
     p.seg_y[at] = out;
   }
 }
 
-// One block: 64 channels of the rows e, e + groups, ... (or of one segment of them), W waves of
-// S steps each at a time, from the end, the next ones' loads in flight meanwhile.
-template <class F, int S, int W, bool NEAR>
-__global__ void __launch_bounds__(64 * W) backward_kernel(const Args p, uint32_t tiles) {
-  static_assert(S == kMark, "a chunk begins at a marked state");
-  __shared__ Exchange<W> s;
-  const int lane = threadIdx.x & 63;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t tile = blockIdx.x % tiles, es = blockIdx.x / tiles, nseg = (uint32_t)p.nseg;
+// 64 channels of the rows group, group + groups, ... (or of one segment of them), W waves of S steps each at a
+// time, from the end, the next ones' loads in flight meanwhile; d_rate: their share of the rates' gradient.
+// Returns whether they are for the walk that looks at everything (EVERY).
+template <class F, int S, int W, bool NEAR, bool EVERY>
+__device__ __forceinline__ bool backward_walk(const Args& p, Exchange<W>& s, uint32_t tile, uint32_t es, int w, int lane,
+                                              float& d_rate) {
+  const uint32_t nseg = (uint32_t)p.nseg;
   const int64_t seg = es % nseg, group = es / nseg, d0 = tile * 64;
   const bool column = d0 + lane < p.D;
   const uint32_t col = column ? lane : (uint32_t)(p.D - 1 - d0);  // loads stay inside the row
-  const float rate = p.rate[d0 + col], rate2 = kLog2E * rate;
+  const float rate = rate_of(p.rate[d0 + col]), rate2 = kLog2E * rate;
+  d_rate = 0.0f;
+  if (!EVERY && any_quick(rate)) return true;
+  const float less = EVERY ? less_of(rate) : 1.0f;
   const int begin = (int)seg * (int)p.seg_steps;
   const int end = (int)(p.T < begin + p.seg_steps ? p.T : begin + p.seg_steps);
   constexpr int kStep = W * S;
   const int ahead = w * S;
-  float d_rate = 0.0f;
+  float odd = 0.0f;
   int buf = 0;
   for (int64_t e = group; e < p.E; e += p.groups) {
     const Tensors<F, S, NEAR> in(p, e, d0, lane, col);
@@ -230,18 +262,20 @@ __global__ void __launch_bounds__(64 * W) backward_kernel(const Args p, uint32_t
     }
     auto take = [&](const Chunk<F, S>& c, const Rest<F, S>& rest, int t) __attribute__((always_inline)) {
       const uint32_t cut = flag_word(c.flag, t, first), live = live_word<S>(t, end);
-      const bool care = cut != 0 || live != (1u << S) - 1;
+      const bool whole = cut == 0 && live == (1u << S) - 1;
       Decays<S> k;
-      if (!care) decays<F, S, false>(k, c, rate2, 0, 0);
-      else decays<F, S, true>(k, c, rate2, cut, live);
+      by_form<EVERY>(whole, [&](auto form) __attribute__((always_inline)) {
+        decays<F, S, form>(k, c, rate2, less, cut, live);
+      });
       float g = carry;  // e entering this wave's chunk
       if constexpr (W > 1) {
         s.put(buf, w, lane, exp2_fast(-k.L), k.out, cut);
         meet();
-        g = s.template entering<-1>(buf, w, lane);
+        g = s.template entering<-1, EVERY>(buf, w, lane);
       }
-      if (!care) g = gradients<F, S, NEAR, false>(k, c, rest, g, rate, d_rate, in, t, out_at, 0, 0);
-      else g = gradients<F, S, NEAR, true>(k, c, rest, g, rate, d_rate, in, t, out_at, cut, live);
+      by_form<EVERY>(whole, [&](auto form) __attribute__((always_inline)) {
+        g = gradients<F, S, NEAR, form>(k, c, rest, g, odd, rate, d_rate, in, t, out_at, cut, live);
+      });
       carry = g;
       if constexpr (W > 1) {  // what leaves the first wave enters the chunks before
         buf ^= 1;
@@ -268,6 +302,20 @@ __global__ void __launch_bounds__(64 * W) backward_kernel(const Args p, uint32_t
     }
     if (w == 0 && column && seg == 0 && p.d_init) p.d_init[e * p.D + d0 + lane] = carry;
   }
+  return any_odd(odd);
+}
+
+// One block for a tile of channels and a group of rows (or one segment of them).
+template <class F, int S, int W, bool NEAR>
+__global__ void __launch_bounds__(64 * W) backward_kernel(const Args p, uint32_t tiles) {
+  static_assert(S == kMark, "a chunk begins at a marked state");
+  __shared__ Exchange<W> s;
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t tile = blockIdx.x % tiles, es = blockIdx.x / tiles;
+  float d_rate;
+  if (s.any(w, lane, backward_walk<F, S, W, NEAR, false>(p, s, tile, es, w, lane, d_rate)))
+    backward_walk<F, S, W, NEAR, true>(arguments_again(), s, again(tile), again(es), again(w), la::rarely(lane), d_rate);
   if constexpr (W > 1) {
     __syncthreads();
     s.a[0][w][lane] = d_rate;
@@ -275,7 +323,8 @@ __global__ void __launch_bounds__(64 * W) backward_kernel(const Args p, uint32_t
     d_rate = 0.0f;
     for (int v = 0; v < W; ++v) d_rate += s.a[0][v][lane];
   }
-  if (w == 0 && column) (p.rate_part ? p.rate_part : p.d_rate)[(group * p.nseg + seg) * p.D + d0 + lane] = d_rate;
+  const int64_t column = (int64_t)tile * 64 + lane;
+  if (w == 0 && column < p.D) (p.rate_part ? p.rate_part : p.d_rate)[(int64_t)es * p.D + column] = d_rate;
 }
 
 template <class F, int S, int W, bool NEAR>

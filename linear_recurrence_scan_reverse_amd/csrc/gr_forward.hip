@@ -20,50 +20,56 @@ struct Chunk {
   uint8_t flag;
 };
 
-// a - 1 and the term of every step, the sum of y (logarithms of the decays) and what leaves the
-// chunk for a state of 0.
+// The decay (decay_of) and the term of every step, the sum of y (logarithms of the decays) and what leaves
+// the chunk for a state of 0.
 template <int S>
 struct Coefficients {
-  float em1[S], b[S];
+  float a[S], b[S];
   float L, out;
 };
 
-// CARE: some steps start anew (cut) or lie past the end (not live).
-template <class F, int S, bool CARE>
-__device__ __forceinline__ void coefficients(Coefficients<S>& c, const Chunk<F, S>& in, float rate2, uint32_t cut,
-                                             uint32_t live) {
+// less: see decay_of, for kEvery.
+template <class F, int S, Form FORM>
+__device__ __forceinline__ void coefficients(Coefficients<S>& c, const Chunk<F, S>& in, float rate2, float less,
+                                             uint32_t cut, uint32_t live) {
+#pragma clang fp contract(off)
   c.L = c.out = 0.0f;
 #pragma unroll
   for (int k = 0; k < S; ++k) {
-    const float dg = F::get(CARE ? apart(in.dg[k]) : in.dg[k]), ig = F::get(CARE ? apart(in.ig[k]) : in.ig[k]),
-                x = F::get(CARE ? apart(in.x[k]) : in.x[k]);
+    const float dg = F::get(FORM != kPlain ? apart(in.dg[k]) : in.dg[k]);
+    const float ig = F::get(FORM != kPlain ? apart(in.ig[k]) : in.ig[k]);
+    const float x = F::get(FORM != kPlain ? apart(in.x[k]) : in.x[k]);
     float y = rate2 * sigmoid(dg);
-    float em1 = decay_less_1(y);
-    if (CARE) em1 = pick(spread(cut, k), -1.0f, em1);
-    float b = __builtin_amdgcn_sqrtf(one_less_square(em1)) * (sigmoid(ig) * x);
-    if (CARE) {
-      em1 = keep(em1, spread(live, k));
+    float a = decay_of<FORM>(y, FORM == kEvery ? less : 1.0f);
+    if (FORM != kPlain) a = decay_behind<FORM>(a, spread(cut, k));
+    float b = __builtin_amdgcn_sqrtf(one_less_square<FORM>(a)) * (sigmoid(ig) * x);
+    if (FORM != kPlain) {
+      a = decay_before<FORM>(a, spread(live, k));
       b = keep(b, spread(live, k));
       y = keep(y, spread(live, k));
       c.out = keep(c.out, ~spread(cut, k));
     }
-    c.em1[k] = em1;
+    c.a[k] = a;
     c.b[k] = b;
     c.L += y;
-    c.out = decayed(em1, c.out) + b;
+    c.out = decayed<FORM>(a, c.out) + b;
   }
 }
 
 // The states of a chunk, from the one that enters it, to memory.  Returns the last.
-template <class F, int S, bool NEAR, bool CARE>
-__device__ __forceinline__ float states(const Coefficients<S>& c, float h, const Stream<F, S, NEAR>& out, int t,
-                                        int64_t st, uint32_t lane, uint32_t cut, uint32_t live) {
+template <class F, int S, bool NEAR, Form FORM>
+__device__ __forceinline__ float states(const Coefficients<S>& c, float h, float& odd, const Stream<F, S, NEAR>& out,
+                                        int t, int64_t st, uint32_t lane, uint32_t cut, uint32_t live) {
+#pragma clang fp contract(off)
 #pragma unroll
   for (int k = 0; k < S; ++k) {
-    if (CARE) h = keep(h, ~spread(cut, k));
-    h = decayed(c.em1[k], h) + c.b[k];
-    if (!CARE || (live >> k) & 1) out.store(F::put(h), t, k, st, lane);
+    if (FORM != kPlain) h = keep(h, ~spread(cut, k));
+    const float before = h;
+    h = decayed<FORM>(c.a[k], h) + c.b[k];
+    if (FORM == kCut && k % 2 == 1) odd = seen(odd, before, h);  // the next cut would hide them
+    if (FORM == kPlain || (live >> k) & 1) out.store(F::put(h), t, k, st, lane);
   }
+  if (FORM != kEvery) odd = seen(odd, h);
   return h;
 }
 
@@ -94,32 +100,34 @@ struct Inputs {
 };
 
 // The pair of each segment but the last: a wave takes a share of it, chunk after chunk.
-template <class F, int S, int W, bool NEAR, bool ALIKE>
-__global__ void __launch_bounds__(64 * W) fold_kernel(const Args p, uint32_t tiles) {
-  __shared__ float s_a[W][64], s_y[W][64];
-  const int lane = threadIdx.x & 63;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t tile = blockIdx.x % tiles, es = blockIdx.x / tiles, nseg = (uint32_t)p.nseg;
+// Returns whether the share is for the walk that looks at everything (EVERY).
+template <class F, int S, int W, bool NEAR, bool ALIKE, bool EVERY>
+__device__ __forceinline__ bool fold_walk(const Args& p, uint32_t tile, uint32_t es, int w, int lane, float& A,
+                                          float& y) {
+  const uint32_t nseg = (uint32_t)p.nseg;
   const int64_t seg = es % (nseg - 1), e = es / (nseg - 1), d0 = tile * 64;
-  const bool column = d0 + lane < p.D;
-  const uint32_t col = column ? lane : (uint32_t)(p.D - 1 - d0);  // loads stay inside the row
-  const float rate2 = kLog2E * p.rate[d0 + col];
+  const uint32_t col = d0 + lane < p.D ? lane : (uint32_t)(p.D - 1 - d0);  // loads stay inside the row
+  const float rate = rate_of(p.rate[d0 + col]), rate2 = kLog2E * rate;
   const Inputs<F, S, NEAR, ALIKE> in(p, e, d0, lane, col);
   const int share = (int)p.seg_steps / W, begin = (int)seg * (int)p.seg_steps + w * share, end = begin + share;
-  float total = 0.0f, y = 0.0f;
-  bool dropped = false;
   const uint32_t first = first_flag(p, e);
+  if (!EVERY && any_quick(rate)) return true;
+  Chunk<F, S> one, two;
+  in.load(one, begin, end);
+  const float less = EVERY ? less_of(rate) : 1.0f;
+  float total = 0.0f;
+  bool dropped = false;
+  y = 0.0f;
   auto fold = [&](const Chunk<F, S>& c, int t) __attribute__((always_inline)) {
     const uint32_t cut = flag_word(c.flag, t, first);
     Coefficients<S> k;
-    if (cut == 0) coefficients<F, S, false>(k, c, rate2, 0, 0);
-    else coefficients<F, S, true>(k, c, rate2, cut, (1u << S) - 1);
+    by_form<EVERY>(cut == 0, [&](auto form) __attribute__((always_inline)) {
+      coefficients<F, S, form>(k, c, rate2, less, cut, (1u << S) - 1);
+    });
     total += k.L;
     dropped |= cut != 0;
-    y = enter(cut ? kDropped : exp2_fast(-k.L), k.out, y);
+    y = enter<EVERY>(cut ? kDropped : exp2_fast(-k.L), k.out, y);
   };
-  Chunk<F, S> one, two;
-  in.load(one, begin, end);
   for (int t = begin;;) {  // a share holds whole chunks
     in.load(two, t + S, end);
     fold(one, t);
@@ -130,16 +138,31 @@ __global__ void __launch_bounds__(64 * W) fold_kernel(const Args p, uint32_t til
     t += S;
     if (t >= end) break;
   }
-  s_a[w][lane] = dropped ? kDropped : exp2_fast(-total);
+  A = dropped ? kDropped : exp2_fast(-total);
+  return any_odd(seen(0.0f, y));
+}
+
+template <class F, int S, int W, bool NEAR, bool ALIKE>
+__global__ void __launch_bounds__(64 * W) fold_kernel(const Args p, uint32_t tiles) {
+  __shared__ float s_a[W][64], s_y[W][64];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t tile = blockIdx.x % tiles, es = blockIdx.x / tiles;
+  float A, y;
+  if (fold_walk<F, S, W, NEAR, ALIKE, false>(p, tile, es, w, lane, A, y))
+    fold_walk<F, S, W, NEAR, ALIKE, true>(arguments_again(), again(tile), again(es), again(w), la::rarely(lane), A, y);
+  s_a[w][lane] = A;
   s_y[w][lane] = y;
   __syncthreads();
-  if (w == 0 && column) {
+  const int64_t column = (int64_t)tile * 64 + lane;
+  if (w == 0 && column < p.D) {
     float A = 1.0f, out = 0.0f;
     for (int u = 0; u < W; ++u) {
       out = enter(s_a[u][lane], s_y[u][lane], out);
       A = A < 0.0f || s_a[u][lane] < 0.0f ? kDropped : A * s_a[u][lane];
     }
-    const int64_t at = (e * p.nseg + seg) * p.D + d0 + lane;
+    const uint32_t nseg = (uint32_t)p.nseg;
+    const int64_t at = ((int64_t)(es / (nseg - 1)) * nseg + es % (nseg - 1)) * p.D + column;
     p.seg_a[at] = A;
     p.seg_y[at] = out;
   }
@@ -147,16 +170,15 @@ __global__ void __launch_bounds__(64 * W) fold_kernel(const Args p, uint32_t til
 
 // One block: 64 channels of one row (or of one segment of it), W waves of S steps each at a
 // time, the next ones' loads in flight meanwhile.
-template <class F, int S, int W, bool NEAR, bool ALIKE>
-__global__ void __launch_bounds__(64 * W) forward_kernel(const Args p, uint32_t tiles) {
-  __shared__ Exchange<W> s;
-  const int lane = threadIdx.x & 63;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t tile = blockIdx.x % tiles, es = blockIdx.x / tiles, nseg = (uint32_t)p.nseg;
+// Returns whether the segment is for the walk that looks at everything (EVERY).
+template <class F, int S, int W, bool NEAR, bool ALIKE, bool EVERY>
+__device__ __forceinline__ bool forward_walk(const Args& p, Exchange<W>& s, uint32_t tile, uint32_t es, int w,
+                                             int lane) {
+  const uint32_t nseg = (uint32_t)p.nseg;
   const int64_t seg = nseg - 1 - es % nseg, e = es / nseg, d0 = tile * 64;
   const bool column = d0 + lane < p.D;
   const uint32_t col = column ? lane : (uint32_t)(p.D - 1 - d0);  // loads stay inside the row
-  const float rate2 = kLog2E * p.rate[d0 + col];
+  const float rate = rate_of(p.rate[d0 + col]), rate2 = kLog2E * rate;
   const Inputs<F, S, NEAR, ALIKE> in(p, e, d0, lane, col);
   const Stream<F, S, NEAR> out(p.out, e, d0);
   const int64_t out_st = p.out.st * (int64_t)sizeof(typename F::E);
@@ -164,41 +186,46 @@ __global__ void __launch_bounds__(64 * W) forward_kernel(const Args p, uint32_t 
   const int begin = (int)seg * (int)p.seg_steps;
   const int end = (int)(p.T < begin + p.seg_steps ? p.T : begin + p.seg_steps);
   float* marks = p.marks ? p.marks + (e * ((p.T + kMark - 1) / kMark)) * p.D + d0 + lane : nullptr;
+  constexpr int kStep = W * S;
+  const int ahead = w * S;
+  const uint32_t first = first_flag(p, e);
+  Chunk<F, S> one, two;
+  if (begin < end) in.load(one, begin + ahead, end);
 
   float carry = p.init ? p.init[e * p.D + d0 + col] : 0.0f;  // the state entering the W chunks at hand
   for (int64_t u = 0; u < seg; ++u) {
     const int64_t at = (e * p.nseg + u) * p.D + d0 + col;
     carry = enter(p.seg_a[at], p.seg_y[at], carry);
   }
+  if (!EVERY && any_quick(rate)) return true;
+  const float less = EVERY ? less_of(rate) : 1.0f;
+  float odd = 0.0f;
   if (W > 1) s.carry[0][lane] = carry;  // the same from every wave
   int buf = 0;
-  const uint32_t first = first_flag(p, e);
   auto take = [&](const Chunk<F, S>& c, int t) __attribute__((always_inline)) {
     const uint32_t cut = flag_word(c.flag, t, first), live = live_word<S>(t, end);
-    const bool care = cut != 0 || live != (1u << S) - 1;
+    const bool whole = cut == 0 && live == (1u << S) - 1;
     Coefficients<S> k;
-    if (!care) coefficients<F, S, false>(k, c, rate2, 0, 0);
-    else coefficients<F, S, true>(k, c, rate2, cut, live);
+    by_form<EVERY>(whole, [&](auto form) __attribute__((always_inline)) {
+      coefficients<F, S, form>(k, c, rate2, less, cut, live);
+    });
     float h = carry;  // the state entering this wave's chunk
     if constexpr (W > 1) {
       s.put(buf, w, lane, exp2_fast(-k.L), k.out, cut);
       meet();
-      h = s.template entering<1>(buf, w, lane);
+      h = s.template entering<1, EVERY>(buf, w, lane);
     }
     if (marks && column && live && t % kMark == 0) marks[(int64_t)(t / kMark) * p.D] = h;
-    if (!care) h = states<F, S, NEAR, false>(k, h, out, t, out_st, out_at, 0, 0);
-    else h = states<F, S, NEAR, true>(k, h, out, t, out_st, out_at, cut, live);
+    by_form<EVERY>(whole, [&](auto form) __attribute__((always_inline)) {
+      h = states<F, S, NEAR, form>(k, h, odd, out, t, out_st, out_at, cut, live);
+    });
     carry = h;
     if constexpr (W > 1) {  // the last wave's state is what enters the chunks behind
       buf ^= 1;
       if (w == W - 1) s.carry[buf][lane] = h;
     }
   };
-  constexpr int kStep = W * S;
-  const int ahead = w * S;
   if (begin < end) {
-    Chunk<F, S> one, two;
-    in.load(one, begin + ahead, end);
     for (int t = begin;;) {
       in.load(two, t + kStep + ahead, end);
       take(one, t + ahead);
@@ -215,6 +242,18 @@ __global__ void __launch_bounds__(64 * W) forward_kernel(const Args p, uint32_t 
     const bool ended = in.done && p.T > 0 && in.done[(p.T - 1) * p.d_st] != 0;
     p.final_state[e * p.D + d0 + lane] = ended ? 0.0f : carry;
   }
+  return any_odd(odd);
+}
+
+template <class F, int S, int W, bool NEAR, bool ALIKE>
+__global__ void __launch_bounds__(64 * W) forward_kernel(const Args p, uint32_t tiles) {
+  __shared__ Exchange<W> s;
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t tile = blockIdx.x % tiles, es = blockIdx.x / tiles;
+  if (s.any(w, lane, forward_walk<F, S, W, NEAR, ALIKE, false>(p, s, tile, es, w, lane)))
+    forward_walk<F, S, W, NEAR, ALIKE, true>(arguments_again(), s, again(tile), again(es), again(w),
+                                             la::rarely(lane));
 }
 
 template <class F, int S, int W, bool NEAR, bool ALIKE>

@@ -23,9 +23,9 @@ __global__ void __launch_bounds__(256) step_kernel(const StepArgs p, int64_t til
   const float x = F::get(static_cast<const E*>(p.x)[e * p.x_se + d]);
   const float gi = F::get(static_cast<const E*>(p.ig)[e * p.ig_se + d]);
   const float gd = F::get(static_cast<const E*>(p.dg)[e * p.dg_se + d]);
-  const float em1 = fresh ? -1.0f : decay_less_1(kLog2E * p.rate[d] * sigmoid(gd));
-  const float b = __builtin_amdgcn_sqrtf(one_less_square(em1)) * (sigmoid(gi) * x);
-  const float h = decayed(em1, fresh ? 0.0f : *state) + b;
+  const float a = fresh ? 0.0f : decay_of<kEvery>(kLog2E * rate_of(p.rate[d]) * sigmoid(gd), 0.0f);
+  const float b = __builtin_amdgcn_sqrtf(one_less_square<kEvery>(a)) * (sigmoid(gi) * x);
+  const float h = decayed<kEvery>(a, fresh ? 0.0f : *state) + b;
   *state = h;
   *out = F::put(h);
 }

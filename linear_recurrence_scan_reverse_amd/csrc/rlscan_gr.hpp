@@ -9,10 +9,16 @@
 //
 // Numbers.  Everything is float32.  The decay is held as a - 1 (expm1), whose relative
 // error stays at a few 2^-24 however near a is to 1: h + (a - 1) h keeps memories of thousands
-// of steps exact, and 1 - a^2 = (1 - a)(1 + a) does not cancel.  A product of decays
-// is the exponential of a sum.
+// of steps exact, and 1 - a^2 = (1 - a)(1 + a) does not cancel.  What a fast decay leaves of a state
+// or a gradient would lose its bits that way (all of them for s > 17), and an infinite one would be
+// inf - inf.  Blocks with a rate of kQuick or more therefore hold a itself where s is above 0.17, and blocks
+// that met a value that is not finite walk their rows once more, looking at every value (kEvery): an infinite one
+// stays until its episode ends, however little its decays would leave of it.  A product of decays is the
+// exponential of a sum.
 #ifndef RLSCAN_GR_HPP
 #define RLSCAN_GR_HPP
+
+#include <type_traits>
 
 #include "rlscan_la.hpp"
 #include "rlscan_logits.hpp"
@@ -82,31 +88,6 @@ __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.0f + exp2_fast(-kLog2E * z));
 }
 
-// a - 1 = 2^-y - 1 for y >= 0 (y: s in units of log 2).  Below a quarter a cubic times y,
-// fitted to (1 - 2^-y) / y by least largest relative error, 2^-24 of the value; above it
-// 1 - a >= 0.16 loses at most three bits.
-__device__ __forceinline__ float decay_less_1(float y) {
-  const float far = exp2_fast(-y) - 1.0f;
-  float p = __builtin_fmaf(y, 0.008974975906f, -0.055404357612f);
-  p = __builtin_fmaf(y, p, 0.240221500397f);
-  p = __builtin_fmaf(y, p, -0.693147122860f);
-  return y < 0.25f ? y * p : far;
-}
-// 1 - a^2 from a - 1
-__device__ __forceinline__ float one_less_square(float em1) { return -em1 * (2.0f + em1); }
-
-// a h from a - 1
-__device__ __forceinline__ float decayed(float em1, float h) { return __builtin_fmaf(em1, h, h); }
-
-// A segment's pair in the workspace: A is kDropped where it holds a cut, which takes any c, inf
-// and NaN too, to y.
-constexpr float kDropped = -1.0f;
-__device__ __forceinline__ float enter(float A, float y, float c) { return A < 0.0f ? y : __builtin_fmaf(A, c, y); }
-
-// ------------------------------------------------------------------ chunks of S steps
-// A wave holds 64 channels of S steps in registers.  Addresses are scalars and the lane's
-// column, so that a step costs no vector instructions but its arithmetic.
-
 // Bit k of a chunk's words, as a mask of 32 bits.  An AND with it takes inf and NaN to 0 too.
 __device__ __forceinline__ uint32_t spread(uint32_t word, int k) { return (uint32_t)((int32_t)(word << (31 - k)) >> 31); }
 __device__ __forceinline__ float keep(float x, uint32_t mask) {
@@ -116,6 +97,111 @@ __device__ __forceinline__ float keep(float x, uint32_t mask) {
 __device__ __forceinline__ float pick(uint32_t mask, float x, float y) {
   return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x) & mask) | (__builtin_bit_cast(uint32_t, y) & ~mask));
 }
+
+// A rate as the kernels take it: NaN below 0, and -0 as 0.
+__device__ __forceinline__ float rate_of(float rate) {
+  return rate >= 0.0f ? __builtin_fabsf(rate) : __builtin_nanf("");
+}
+
+// What a chunk's arithmetic looks at: nothing but its steps; which of them start anew (cut) or lie past the end
+// (not live); and besides these how each decay is held and whether what it is multiplied with is infinite.
+// Finite values come out the same of each, to the last bit: sums and products are contracted by hand.
+enum Form { kPlain, kCut, kEvery };
+
+// f(form): the form that a chunk takes.  EVERY is known for a whole walk, so that each walk has its own forms alone.
+template <bool EVERY, class Call>
+__device__ __forceinline__ void by_form(bool whole, const Call& f) {
+  if constexpr (EVERY) f(std::integral_constant<Form, kEvery>());
+  else if (whole) f(std::integral_constant<Form, kPlain>());
+  else f(std::integral_constant<Form, kCut>());
+}
+
+// Rates from which on a block holds fast decays as a: below, a > 0.135 and a - 1 keeps it to 4 of 2^-24.  Measured,
+// us, forward and gradients by the first two forms and by kEvery: 8 x 4096 x 2048 bfloat16 353 and 465, 64 x 333 x 768
+// float32 152 and 166, 8000 x 128 x 64 bfloat16 300 and 400.
+constexpr float kQuick = 2.0f;
+__device__ __forceinline__ bool any_quick(float rate) { return __builtin_amdgcn_ballot_w64(rate >= kQuick) != 0; }
+// 1 in the sum a - less that is held for such a, 0 in blocks with a quick rate.
+__device__ __forceinline__ float less_of(float rate) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(any_quick(rate) ? 0 : 0x3f800000));
+}
+// The same number, unknown to the compiler, and the kernel's argument read from memory once more: what the second
+// walk computes from them stays there, and the first walk's registers are its own.
+__device__ __forceinline__ uint32_t again(uint32_t x) {
+  asm volatile("" : "+s"(x));
+  return x;
+}
+__device__ __forceinline__ Args arguments_again() {
+  auto* p = __builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const Args*)p;
+}
+
+// `odd` once it has seen an x that is not finite, or an x or a y that is infinite, is infinite.
+__device__ __forceinline__ float seen(float odd, float x) {
+  return __builtin_fabsf(x) < __builtin_inff() ? odd : __builtin_inff();
+}
+__device__ __forceinline__ float seen(float odd, float x, float y) {
+  return __builtin_fmaxf(__builtin_fmaxf(odd, __builtin_fabsf(x)), __builtin_fabsf(y));
+}
+__device__ __forceinline__ bool any_odd(float odd) {
+  return __builtin_amdgcn_ballot_w64(odd == __builtin_inff()) != 0;
+}
+
+// A decay a = 2^-y for y >= 0 (y: s in units of log 2): a - 1, with the sign bit set (a = 1: -0).  For y below a
+// quarter a cubic times y, fitted to (1 - 2^-y) / y by least largest relative error, 2^-24 of the value; above it
+// 1 - a >= 0.16 loses at most three bits.  With less = 0 a itself is held there, with the sign bit clear; below
+// the normal numbers the smallest of these, so that an infinite value stays.
+template <Form FORM>
+__device__ __forceinline__ float decay_of(float y, float less) {
+  const float a = exp2_fast(-y), far = (FORM == kEvery && y == y ? __builtin_fmaxf(a, 1.17549435e-38f) : a) - less;
+  float p = __builtin_fmaf(y, 0.008974975906f, -0.055404357612f);
+  p = __builtin_fmaf(y, p, 0.240221500397f);
+  p = __builtin_fmaf(y, p, -0.693147122860f);
+  return y < 0.25f ? y * p : far;
+}
+
+// Whether a decay is held as a - 1, as a mask of 32 bits.
+__device__ __forceinline__ uint32_t near_one(float decay) {
+  return (uint32_t)(__builtin_bit_cast(int32_t, decay) >> 31);
+}
+// The decay of a step that starts anew (a = 0) or not, and that lies before the end or (a = 1) not.
+template <Form FORM>
+__device__ __forceinline__ float decay_behind(float decay, uint32_t cut) {
+  return FORM == kEvery ? keep(decay, ~cut) : pick(cut, -1.0f, decay);
+}
+template <Form FORM>
+__device__ __forceinline__ float decay_before(float decay, uint32_t live) {
+  return FORM == kEvery ? pick(live, decay, -0.0f) : keep(decay, live);
+}
+// 1 - a^2
+template <Form FORM>
+__device__ __forceinline__ float one_less_square(float decay) {
+  const float twice = -2.0f * decay;
+  return __builtin_fmaf(-decay, decay, FORM == kEvery ? pick(near_one(decay), twice, 1.0f) : twice);
+}
+// a h
+template <Form FORM>
+__device__ __forceinline__ float decayed(float decay, float h) {
+  if (FORM != kEvery) return __builtin_fmaf(decay, h, h);
+  // h + (a - 1) h is inf - inf for an infinite h, so the largest number stands for it in the product
+  const uint32_t near = near_one(decay);
+  const float most = __builtin_amdgcn_fmed3f(h, -3.40282347e38f, 3.40282347e38f);
+  return __builtin_fmaf(decay, pick(near, most, h), keep(h, near));
+}
+
+// A segment's pair in the workspace: A is kDropped where it holds a cut, which takes any c, inf
+// and NaN too, to y.
+constexpr float kDropped = -1.0f;
+// EVERY: c may be infinite, and stays so where A is too little for float32.
+template <bool EVERY = true>
+__device__ __forceinline__ float enter(float A, float y, float c) {
+  return A < 0.0f ? y : EVERY && __builtin_isinf(c) ? c + y : __builtin_fmaf(A, c, y);
+}
+
+// ------------------------------------------------------------------ chunks of S steps
+// A wave holds 64 channels of S steps in registers.  Addresses are scalars and the lane's
+// column, so that a step costs no vector instructions but its arithmetic.
 
 // The same value, of which the compiler knows nothing: keeps it from doing the work that both
 // forms of a branch begin with before the branch, where its results lie in registers for long.
@@ -223,16 +309,24 @@ __device__ __forceinline__ void meet() {
 template <int W>
 struct Exchange {
   float a[2][W][64], y[2][W][64], carry[2][64];
-  uint32_t cut[2][W];
+  uint32_t cut[2][W], odd[W];
 
   __device__ __forceinline__ void put(int buf, int w, int lane, float A, float out, uint32_t cut_word) {
     a[buf][w][lane] = A;
     y[buf][w][lane] = out;
     if (lane == 0) cut[buf][w] = cut_word;
   }
+  // Whether a wave of the block says so; all of them are done with the walk behind them.
+  __device__ __forceinline__ bool any(int w, int lane, bool mine) {
+    if constexpr (W == 1) return mine;
+    if (lane == 0) odd[w] = mine;
+    meet();
+    return __builtin_amdgcn_ballot_w64(lane < W && odd[lane < W ? lane : 0] != 0) != 0;
+  }
   // What enters wave w's chunk from the chunks `before` it (STEP 1: lower waves, -1: higher ones).
   // A wave with a cut takes anything to its y, so the walk begins behind the nearest of these.
-  template <int STEP>
+  // EVERY: what enters may be infinite.
+  template <int STEP, bool EVERY>
   __device__ __forceinline__ float entering(int buf, int w, int lane) const {
     const uint32_t cuts = (uint32_t)__builtin_amdgcn_ballot_w64(lane < W && cut[buf][lane < W ? lane : 0] != 0);
     float c = carry[buf][lane];
@@ -255,7 +349,8 @@ struct Exchange {
       for (int j = 0; j < B; ++j) {
         const int i = STEP > 0 ? j : B - 1 - j, u = base + i;
         if (mine && u == from) c = Y[i];
-        else if (STEP > 0 ? u >= from && u < w : u <= from && u > w) c = __builtin_fmaf(A[i], c, Y[i]);
+        else if (STEP > 0 ? u >= from && u < w : u <= from && u > w)
+          c = EVERY ? enter(A[i], Y[i], c) : __builtin_fmaf(A[i], c, Y[i]);
       }
     }
     return c;
