@@ -22,7 +22,7 @@ namespace gr {
 // What the decays of a chunk are made of; the rest is asked for when these are at hand, and used
 // behind the barrier.
 template <class F, int S>
-struct Chunk {
+struct Ahead {
   typename F::E g[S], dg[S];
   uint8_t flag;
 };
@@ -42,7 +42,7 @@ struct Decays {
 
 // less: see decay_of, for kEvery.
 template <class F, int S, Form FORM>
-__device__ __forceinline__ void decays(Decays<S>& c, const Chunk<F, S>& in, float rate2, float less, uint32_t cut,
+__device__ __forceinline__ void decays(Decays<S>& c, const Ahead<F, S>& in, float rate2, float less, uint32_t cut,
                                        uint32_t live) {
 #pragma clang fp contract(off)
   c.L = c.out = 0.0f;
@@ -91,7 +91,7 @@ struct Tensors {
     dig_st = p.dig.st * es;
     ddg_st = p.ddg.st * es;
   }
-  __device__ __forceinline__ void load(Chunk<F, S>& c, int t, int end) const {
+  __device__ __forceinline__ void load(Ahead<F, S>& c, int t, int end) const {
     dg.load(c.dg, t, end, Steps<S, NEAR>(dg_st, t, end), at);
     g.load(c.g, t, end, Steps<S, NEAR>(g_st, t, end), at);
     c.flag = load_flag<S>(done, done_step, t, end, lane);
@@ -105,7 +105,7 @@ struct Tensors {
 
 // The gradients of a chunk, from the e that enters it, to memory; returns the e that leaves it.
 template <class F, int S, bool NEAR, Form FORM>
-__device__ __forceinline__ float gradients(Decays<S>& c, const Chunk<F, S>& in, const Rest<F, S>& rest, float e,
+__device__ __forceinline__ float gradients(Decays<S>& c, const Ahead<F, S>& in, const Rest<F, S>& rest, float e,
                                            float& odd, float rate, float& d_rate, const Tensors<F, S, NEAR>& to, int t,
                                            uint32_t out_at, uint32_t cut, uint32_t live) {
 #pragma clang fp contract(off)
@@ -171,11 +171,11 @@ __device__ __forceinline__ bool fold_back_walk(const Args& p, uint32_t tile, uin
   y = 0.0f;
   if (begin >= end) return false;
   if (!EVERY && any_quick(rate)) return true;
-  Chunk<F, S> one, two;
+  Ahead<F, S> one, two;
   int t = begin + (end - begin - 1) / S * S;
   in.load(one, t, end);
   const float less = EVERY ? less_of(rate) : 1.0f;
-  auto fold = [&](const Chunk<F, S>& c, uint32_t live) __attribute__((always_inline)) {
+  auto fold = [&](const Ahead<F, S>& c, uint32_t live) __attribute__((always_inline)) {
     const uint32_t cut = flag_word(c.flag, 1, 0);  // never the row's first step
     Decays<S> k;
     by_form<EVERY>(cut == 0 && live == (1u << S) - 1, [&](auto form) __attribute__((always_inline)) {
@@ -260,7 +260,7 @@ __device__ __forceinline__ bool backward_walk(const Args& p, Exchange<W>& s, uin
       meet();  // the row before has been read
       s.carry[buf][lane] = carry;  // the same from every wave
     }
-    auto take = [&](const Chunk<F, S>& c, const Rest<F, S>& rest, int t) __attribute__((always_inline)) {
+    auto take = [&](const Ahead<F, S>& c, const Rest<F, S>& rest, int t) __attribute__((always_inline)) {
       const uint32_t cut = flag_word(c.flag, t, first), live = live_word<S>(t, end);
       const bool whole = cut == 0 && live == (1u << S) - 1;
       Decays<S> k;
@@ -283,7 +283,7 @@ __device__ __forceinline__ bool backward_walk(const Args& p, Exchange<W>& s, uin
       }
     };
     if (begin < end) {
-      Chunk<F, S> one, two;
+      Ahead<F, S> one, two;
       Rest<F, S> rest;
       int t = begin + (end - begin - 1) / kStep * kStep;
       in.load(one, t + ahead, end);
