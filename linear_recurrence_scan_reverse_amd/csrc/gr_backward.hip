@@ -170,7 +170,7 @@ __device__ __forceinline__ bool fold_back_walk(const Args& p, uint32_t tile, uin
   A = 1.0f;
   y = 0.0f;
   if (begin >= end) return false;
-  if (!EVERY && any_quick(rate)) return true;
+  if (!EVERY && __builtin_expect(any_quick(rate), false)) return true;
   Ahead<F, S> one, two;
   int t = begin + (end - begin - 1) / S * S;
   in.load(one, t, end);
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(64 * W) fold_back_kernel(const Args p, uint32_
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t tile = blockIdx.x % tiles, es = blockIdx.x / tiles;
   float A, y;
-  if (fold_back_walk<F, S, W, NEAR, false>(p, tile, es, w, lane, A, y))
+  if (__builtin_expect(fold_back_walk<F, S, W, NEAR, false>(p, tile, es, w, lane, A, y), false))
     fold_back_walk<F, S, W, NEAR, true>(arguments_again(), again(tile), again(es), again(w), la::rarely(lane), A,
                                         y);
   s_a[w][lane] = A;
@@ -214,11 +214,16 @@ __global__ void __launch_bounds__(64 * W) fold_back_kernel(const Args p, uint32_
   __syncthreads();
   const int64_t column = (int64_t)tile * 64 + lane;
   if (w == 0 && column < p.D) {
-    float A = 1.0f, out = 0.0f;
-    for (int v = W - 1; v >= 0; --v) {
-      out = enter(s_a[v][lane], s_y[v][lane], out);
-      A = A < 0.0f || s_a[v][lane] < 0.0f ? kDropped : A * s_a[v][lane];
-    }
+    float A = 1.0f;
+    const float out = joined([&](auto every) {
+      A = 1.0f;
+      float out = 0.0f;
+      for (int v = W - 1; v >= 0; --v) {
+        out = enter<every>(s_a[v][lane], s_y[v][lane], out);
+        A = A < 0.0f || s_a[v][lane] < 0.0f ? kDropped : A * s_a[v][lane];
+      }
+      return out;
+    });
     const uint32_t nseg = (uint32_t)p.nseg;
     const int64_t at = ((int64_t)(es / (nseg - 1)) * nseg + es % (nseg - 1) + 1) * p.D + column;
     p.seg_a[at] = A;
@@ -238,7 +243,7 @@ __device__ __forceinline__ bool backward_walk(const Args& p, Exchange<W>& s, uin
   const uint32_t col = column ? lane : (uint32_t)(p.D - 1 - d0);  // loads stay inside the row
   const float rate = rate_of(p.rate[d0 + col]), rate2 = kLog2E * rate;
   d_rate = 0.0f;
-  if (!EVERY && any_quick(rate)) return true;
+  if (!EVERY && __builtin_expect(any_quick(rate), false)) return true;
   const float less = EVERY ? less_of(rate) : 1.0f;
   const int begin = (int)seg * (int)p.seg_steps;
   const int end = (int)(p.T < begin + p.seg_steps ? p.T : begin + p.seg_steps);
@@ -250,11 +255,18 @@ __device__ __forceinline__ bool backward_walk(const Args& p, Exchange<W>& s, uin
     const Tensors<F, S, NEAR> in(p, e, d0, lane, col);
     const uint32_t out_at = column ? in.at : kNoColumn;
     const uint32_t first = first_flag(p, e);
-    float carry = 0.0f;  // e entering the W chunks at hand from the steps behind them
-    if (p.d_final && !(in.done && p.T > 0 && in.done[(p.T - 1) * p.d_st] != 0)) carry = p.d_final[e * p.D + d0 + col];
-    for (int64_t v = p.nseg - 1; v > seg; --v) {
-      const int64_t at = (e * p.nseg + v) * p.D + d0 + col;
-      carry = enter(p.seg_a[at], p.seg_y[at], carry);
+    float start = 0.0f;
+    if (p.d_final && !(in.done && p.T > 0 && in.done[(p.T - 1) * p.d_st] != 0)) start = p.d_final[e * p.D + d0 + col];
+    float carry = start;  // e entering the W chunks at hand from the steps behind them
+    if (seg < p.nseg - 1) {
+      carry = joined([&](auto every) {
+        float c = start;
+        for (int64_t v = p.nseg - 1; v > seg; --v) {
+          const int64_t at = (e * p.nseg + v) * p.D + d0 + col;
+          c = enter<every>(p.seg_a[at], p.seg_y[at], c);
+        }
+        return c;
+      });
     }
     if (W > 1) {
       meet();  // the row before has been read
@@ -314,7 +326,7 @@ __global__ void __launch_bounds__(64 * W) backward_kernel(const Args p, uint32_t
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t tile = blockIdx.x % tiles, es = blockIdx.x / tiles;
   float d_rate;
-  if (s.any(w, lane, backward_walk<F, S, W, NEAR, false>(p, s, tile, es, w, lane, d_rate)))
+  if (__builtin_expect(s.any(w, lane, backward_walk<F, S, W, NEAR, false>(p, s, tile, es, w, lane, d_rate)), false))
     backward_walk<F, S, W, NEAR, true>(arguments_again(), s, again(tile), again(es), again(w), la::rarely(lane), d_rate);
   if constexpr (W > 1) {
     __syncthreads();

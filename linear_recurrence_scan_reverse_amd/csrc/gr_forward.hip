@@ -111,7 +111,7 @@ __device__ __forceinline__ bool fold_walk(const Args& p, uint32_t tile, uint32_t
   const Inputs<F, S, NEAR, ALIKE> in(p, e, d0, lane, col);
   const int share = (int)p.seg_steps / W, begin = (int)seg * (int)p.seg_steps + w * share, end = begin + share;
   const uint32_t first = first_flag(p, e);
-  if (!EVERY && any_quick(rate)) return true;
+  if (!EVERY && __builtin_expect(any_quick(rate), false)) return true;
   Chunk<F, S> one, two;
   in.load(one, begin, end);
   const float less = EVERY ? less_of(rate) : 1.0f;
@@ -149,18 +149,23 @@ __global__ void __launch_bounds__(64 * W) fold_kernel(const Args p, uint32_t til
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t tile = blockIdx.x % tiles, es = blockIdx.x / tiles;
   float A, y;
-  if (fold_walk<F, S, W, NEAR, ALIKE, false>(p, tile, es, w, lane, A, y))
+  if (__builtin_expect(fold_walk<F, S, W, NEAR, ALIKE, false>(p, tile, es, w, lane, A, y), false))
     fold_walk<F, S, W, NEAR, ALIKE, true>(arguments_again(), again(tile), again(es), again(w), la::rarely(lane), A, y);
   s_a[w][lane] = A;
   s_y[w][lane] = y;
   __syncthreads();
   const int64_t column = (int64_t)tile * 64 + lane;
   if (w == 0 && column < p.D) {
-    float A = 1.0f, out = 0.0f;
-    for (int u = 0; u < W; ++u) {
-      out = enter(s_a[u][lane], s_y[u][lane], out);
-      A = A < 0.0f || s_a[u][lane] < 0.0f ? kDropped : A * s_a[u][lane];
-    }
+    float A = 1.0f;
+    const float out = joined([&](auto every) {
+      A = 1.0f;
+      float out = 0.0f;
+      for (int u = 0; u < W; ++u) {
+        out = enter<every>(s_a[u][lane], s_y[u][lane], out);
+        A = A < 0.0f || s_a[u][lane] < 0.0f ? kDropped : A * s_a[u][lane];
+      }
+      return out;
+    });
     const uint32_t nseg = (uint32_t)p.nseg;
     const int64_t at = ((int64_t)(es / (nseg - 1)) * nseg + es % (nseg - 1)) * p.D + column;
     p.seg_a[at] = A;
@@ -192,12 +197,19 @@ __device__ __forceinline__ bool forward_walk(const Args& p, Exchange<W>& s, uint
   Chunk<F, S> one, two;
   if (begin < end) in.load(one, begin + ahead, end);
 
-  float carry = p.init ? p.init[e * p.D + d0 + col] : 0.0f;  // the state entering the W chunks at hand
-  for (int64_t u = 0; u < seg; ++u) {
-    const int64_t at = (e * p.nseg + u) * p.D + d0 + col;
-    carry = enter(p.seg_a[at], p.seg_y[at], carry);
+  const float start = p.init ? p.init[e * p.D + d0 + col] : 0.0f;
+  float carry = start;  // the state entering the W chunks at hand
+  if (seg > 0) {
+    carry = joined([&](auto every) {
+      float c = start;
+      for (int64_t u = 0; u < seg; ++u) {
+        const int64_t at = (e * p.nseg + u) * p.D + d0 + col;
+        c = enter<every>(p.seg_a[at], p.seg_y[at], c);
+      }
+      return c;
+    });
   }
-  if (!EVERY && any_quick(rate)) return true;
+  if (!EVERY && __builtin_expect(any_quick(rate), false)) return true;
   const float less = EVERY ? less_of(rate) : 1.0f;
   float odd = 0.0f;
   if (W > 1) s.carry[0][lane] = carry;  // the same from every wave
@@ -251,7 +263,7 @@ __global__ void __launch_bounds__(64 * W) forward_kernel(const Args p, uint32_t 
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t tile = blockIdx.x % tiles, es = blockIdx.x / tiles;
-  if (s.any(w, lane, forward_walk<F, S, W, NEAR, ALIKE, false>(p, s, tile, es, w, lane)))
+  if (__builtin_expect(s.any(w, lane, forward_walk<F, S, W, NEAR, ALIKE, false>(p, s, tile, es, w, lane)), false))
     forward_walk<F, S, W, NEAR, ALIKE, true>(arguments_again(), s, again(tile), again(es), again(w),
                                              la::rarely(lane));
 }

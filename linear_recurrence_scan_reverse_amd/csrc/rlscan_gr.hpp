@@ -194,9 +194,16 @@ __device__ __forceinline__ float decayed(float decay, float h) {
 // and NaN too, to y.
 constexpr float kDropped = -1.0f;
 // EVERY: c may be infinite, and stays so where A is too little for float32.
-template <bool EVERY = true>
+template <bool EVERY>
 __device__ __forceinline__ float enter(float A, float y, float c) {
   return A < 0.0f ? y : EVERY && __builtin_isinf(c) ? c + y : __builtin_fmaf(A, c, y);
+}
+// join(every): pairs joined one after the other; once more with care where the result is not finite.
+template <class Join>
+__device__ __forceinline__ float joined(const Join& join) {
+  float c = join(std::false_type());
+  if (__builtin_expect(any_odd(seen(0.0f, c)), false)) c = join(std::true_type());
+  return c;
 }
 
 // ------------------------------------------------------------------ chunks of S steps
@@ -350,7 +357,7 @@ struct Exchange {
         const int i = STEP > 0 ? j : B - 1 - j, u = base + i;
         if (mine && u == from) c = Y[i];
         else if (STEP > 0 ? u >= from && u < w : u <= from && u > w)
-          c = EVERY ? enter(A[i], Y[i], c) : __builtin_fmaf(A[i], c, Y[i]);
+          c = EVERY ? enter<true>(A[i], Y[i], c) : __builtin_fmaf(A[i], c, Y[i]);
       }
     }
     return c;
