@@ -580,7 +580,9 @@ rlscan_status rlscan_gated_recurrence_step(rlscan_format fmt, const rlscan_heads
  *   y_a = z_a cos - z_b sin,  y_b = z_b cos + z_a sin   for the pairs (a, b) of the
  * first `rotate` elements, by the angle positions[e,t] base^(-2j / rotate) for pair j:
  * (2j, 2j + 1) if interleaved, else (j, j + rotate / 2).  The rest of z is passed on.
- * Angles are made in float64, sums and all else in float32 (mean(x^2) past its range: 0).
+ * Angles are made in float64, sums and all else in float32 (where mean(x^2) is past its range the head
+ * is 0; a mean below its normal numbers may count as 0).  An angle is off by at most 2^-49 of itself: far
+ * less than float32's own rounding up to positions of 2^25, 2^-18 at 2^31.
  * In:  q [E,T,H,D], k [E,T,Hk,D] in fmt (H or Hk may be 0); q_weight, k_weight [D]
  *      (optional: ones); positions [E,T] int32 in the layout, of either sign
  *      (not read, and optional, if rotate is 0 or there are no heads).
@@ -611,9 +613,9 @@ rlscan_status rlscan_norm_rotate_heads_backward(
 
 /* Rows of a table by token: out_r = scale table[tokens_r], zeros for a token outside
  * [0,N) (padding).
- * In:  table [N,D] in fmt, rows table_stride apart; tokens [R] int64 (as
+ * In:  table [N,D] in fmt, rows table_stride >= D apart; tokens [R] int64 (as
  *      rlscan_sample_actions gives them).
- * Out: out [R,D] in fmt, rows out_stride apart, rounded once.
+ * Out: out [R,D] in fmt, rows out_stride >= D apart, rounded once.
  * 1 <= N <= 2^20, 1 <= D <= RLSCAN_MAX_TABLE_DIM, R <= 2^26 and R ceil(D/64) < 2^26. */
 #define RLSCAN_MAX_TABLE_DIM 32768
 
@@ -623,7 +625,8 @@ rlscan_status rlscan_embed_tokens(rlscan_format fmt, const void *table, int64_t 
 
 /* Gradient of the table: d_table_n = scale * sum of d_out_r over the tokens n, in
  * float32 and in a fixed order, rounded once; every row is written, rows without a
- * token with zeros, and padding adds to none.  Results do not vary from run to run.
+ * token with zeros, and padding adds to none.  Results do not vary from run to run.  Rows of d_out, too,
+ * are at least D apart: one gradient for all tokens has to be laid out for each.
  * The workspace is of rlscan_embed_tokens_workspace bytes, none for up to 1024 tokens (it may then be NULL). */
 int64_t rlscan_embed_tokens_workspace(int64_t R, int64_t N, int64_t D);
 

@@ -12,7 +12,7 @@
 // Bound by memory like the forward pass: four values read and three written a step.  A wave holds the 16
 // steps behind a mark.  What the decays are made of is read a round ahead, the rest (x, the input gate,
 // the mark) in the round that uses it, behind the barrier: all of it ahead would leave one wave to a SIMD.
-// Measured: 64 x 333 x 768 float32 92 us (5.0 TB/s), 8 x 4096 x 2048 bfloat16 217 (4.3).
+// Measured: 64 x 333 x 768 float32 93 us (4.9 TB/s), 8 x 4096 x 2048 bfloat16 214 (4.4).
 #include "rlscan_gr.hpp"
 #include "rlscan_sums.hpp"
 

@@ -6,9 +6,9 @@
 // other waves need, and the states once the one that enters is known.  One barrier for every W chunks, and the
 // next ones' loads in flight across it.
 //
-// Measured (bytes read and written once): 64 x 333 x 768 float32 54 us (4.8 TB/s), 8 x 4096 x 2048 bfloat16 135
-// (4.0), 1 x 32768 x 1280 bfloat16 in 12 segments 53 for their pairs and 82 for the states (2.5 in all).  Rows
-// of 64 bfloat16 are 128 bytes, and loads and stores of that size alone, four streams, take 110 us of the 135.
+// Measured (bytes read and written once): 64 x 333 x 768 float32 54 us (4.8 TB/s), 8 x 4096 x 2048 bfloat16 134
+// (4.0), 1 x 32768 x 1280 bfloat16 in 12 segments 55 for their pairs and 84 for the states (2.4 in all).  Rows
+// of 64 bfloat16 are 128 bytes, and loads and stores of that size alone, four streams, take 110 us of the 134.
 #include "rlscan_gr.hpp"
 
 namespace rlscan {
@@ -314,14 +314,14 @@ hipError_t launch_forward(rlscan_format f, const Args& a, const Plan& p, hipStre
 // compute unit; of blocks of four a compute unit takes several, which fill each other's waits, and short
 // rows waste less of them.  A wave by itself waits for no other: for rows of one chunk, and where there are
 // many tiles and the last round of four would waste much.  Measured, bfloat16, us forward and backward:
-//   256 tiles of 4096 steps   16 waves 151 and 228   4 waves 179 and 251
-//   264 tiles of 4096                  245     333           218     300   (in segments, see below)
-//   384 tiles of 333                    28      49            26      42
-//   800 tiles of 128                    24      44            17      33   1 wave 20 and 33
-//   3200 tiles of 64                                          25      59          24     48
-//   3200 tiles of 16                                          16      60          12     22
-//   8000 tiles of 128                                        110     235         119    213
-//   8192 tiles of 256                                        229     425         240    487
+//   256 tiles of 4096 steps   16 waves 144 and 225   4 waves 179 and 251
+//   264 tiles of 4096                  245     397           264     364  (in segments 210 and 297, see below)
+//   384 tiles of 333                    30      53            27      46
+//   800 tiles of 128                    27      47            18      36   1 wave 21 and 36
+//   3200 tiles of 64                                          27      67          25     55
+//   3200 tiles of 16                                          18      65          10     27
+//   8000 tiles of 128                                        114     229         107    199
+//   8192 tiles of 256                                        213     406         216    388
 static int waves_of(int64_t tiles, int64_t T, bool backward) {
   if (T <= kMark || (tiles >= 2048 && T < (backward ? 256 : 128))) return 1;
   return T <= 4 * kMark || tiles > 256 ? 4 : kMaxWaves;
@@ -332,10 +332,11 @@ static int waves_of(int64_t tiles, int64_t T, bool backward) {
 // of the time of the walk.  A compute unit takes its blocks one after another if they are of sixteen waves,
 // and if they are of four each adds about 0.6 of the time of the first.  The count that is done first by that
 // reckoning.  Measured, bfloat16, us forward and backward with them and without: 20 tiles of 32768 steps 149
-// and 197 against 907 and 1491, 64 tiles of 4096 61 and 80 against 119 and 199, 264 tiles of 4096 222 and 314
-// against 266 and 382; and where the reckoning takes none, 384 tiles of 4096 forward 276 against 273.  Float32
-// is nearer to what memory gives, and more of its time is the second pass: 384 tiles 452 and 676 against 350 and
-// 619, 264 tiles 372 and 517 against 310 and 569.
+// and 193 against 919 and 1505, 64 tiles of 4096 63 and 81 against 119 and 199, 264 tiles of 4096 210 and 297
+// against 265 and 367; and where the reckoning takes none, 384 tiles of 4096 in two 265 and 363 against 267 and 378.
+// Float32 is nearer to what memory gives, and more of its time is the second pass.  In two and whole: 264 tiles of
+// 4096 363 and 542 against 307 and 540, 264 of 1024 85 and 136 against 79 and 141, 300 of 8192 744 and 1112 against
+// 626 and 1111, 384 of 4096 441 and 647 against 334 and 592, 520 of 2048 323 and 474 against 259 and 470.
 Plan make_plan(rlscan_format f, int64_t E, int64_t T, int64_t D, bool backward) {
   Plan p{};
   const int64_t tiles = E * ((D + 63) / 64);

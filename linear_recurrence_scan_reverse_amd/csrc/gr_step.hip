@@ -1,6 +1,6 @@
 // The gated recurrence for one step of many environments (rlscan_gated_recurrence_step):
 // the state of each row's slot is updated in place.  A lane for a channel: nothing is shared, and the
-// time is latency (256 rows of 2048, float16, in a pool 4.6 us, of which 1.6 would be their bytes; one row of
+// time is latency (256 rows of 2048, float16, in a pool 4.5 us, of which 1.6 would be their bytes; one row of
 // 2048 2.8).
 #include "rlscan_gr.hpp"
 

@@ -11,9 +11,9 @@
 // turns, in float64 (a position times a frequency keeps 2^-52 of itself, so far positions turn
 // like near ones), of which the part behind the point goes to a float32 sine and cosine.
 //
-// Measured: 32768 tokens of 16 and 4 heads of 128, bfloat16, forward 71 us (4.7 TB/s of those read and
-// written), gradients 117 (4.3) with 5 for the sums of the weights' gradients over blocks; 21312 tokens of 4
-// and 2 heads of 80, float32, 18 (4.5) and 40 (3.1): 10 of 16 lanes have a pair there, and one round of blocks is
+// Measured: 32768 tokens of 16 and 4 heads of 128, bfloat16, forward 68 us (4.9 TB/s of those read and
+// written), gradients 120 (4.2) with 5 for the sums of the weights' gradients over blocks; 21312 tokens of 4
+// and 2 heads of 80, float32, 21 (4.0) and 35 (3.5): 10 of 16 lanes have a pair there, and one round of blocks is
 // short; a token for 16 environments 4 us, latency.
 #include <cmath>
 #include <type_traits>
@@ -386,7 +386,8 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(B
 // Pairs to a lane, side by side: pieces of 8 bytes, 16 for float32's gradients.  Measured, us forward and
 // backward, 32768 tokens of 16 and 4 heads of 128, bfloat16: four pairs 75 and 115, eight 78 and (with fewer
 // waves to a compute unit) 150; 65536 tokens of 8 and 8 heads of 64, float32: two 97 and 165, four 100 and 165.
-// Pairs one by one, where addresses or sizes do not fit, take 109 and 168, and 155 and 194.
+// Pairs one by one, where addresses or sizes do not fit, take 109 and 168, and 155 and 194; as many heads in flight
+// as of pieces are more than their registers hold there, and some go through memory.
 static constexpr int widest(int es, bool backward) { return es == 4 && !backward ? 2 : 4; }
 
 static int log2_up(int64_t n) {
@@ -441,7 +442,8 @@ Plan make_plan(rlscan_format f, const Args& a, bool backward) {
 template <class F, int V, bool VEC, bool BWD>
 static void run_heads(const KernelArgs& k, int64_t blocks, hipStream_t st) {
   // Heads in flight, us: forward bfloat16 (32768 tokens of 20 heads) four 71, two 74; float32 (21312 of 6) two 18,
-  // four 19; backward bfloat16 two, float32, which keeps twice the registers of each, one.
+  // four 19; backward bfloat16 two, float32, which keeps twice the registers of each, one (21312 of 6 37.4, two 37.7;
+  // 32768 of 20 204, two 203).
   constexpr int kRing = (BWD ? 2 : 4) / (sizeof(typename F::E) == 4 ? 2 : 1);
   if (k.a.interleaved) heads_kernel<F, V, VEC, true, BWD, kRing><<<dim3((unsigned)blocks), kThreads, 0, st>>>(k);
   else heads_kernel<F, V, VEC, false, BWD, kRing><<<dim3((unsigned)blocks), kThreads, 0, st>>>(k);

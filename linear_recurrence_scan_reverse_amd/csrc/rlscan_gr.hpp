@@ -117,8 +117,8 @@ __device__ __forceinline__ void by_form(bool whole, const Call& f) {
 }
 
 // Rates from which on a block holds fast decays as a: below, a > 0.135 and a - 1 keeps it to 4 of 2^-24.  Measured,
-// us, forward and gradients by the first two forms and by kEvery: 8 x 4096 x 2048 bfloat16 353 and 465, 64 x 333 x 768
-// float32 152 and 166, 8000 x 128 x 64 bfloat16 300 and 400.
+// us, forward and gradients by the first two forms and by kEvery: 8 x 4096 x 2048 bfloat16 351 and 484, 64 x 333 x 768
+// float32 152 and 171, 8000 x 128 x 64 bfloat16 300 and 431.
 constexpr float kQuick = 2.0f;
 __device__ __forceinline__ bool any_quick(float rate) { return __builtin_amdgcn_ballot_w64(rate >= kQuick) != 0; }
 // 1 in the sum a - less that is held for such a, 0 in blocks with a quick rate.

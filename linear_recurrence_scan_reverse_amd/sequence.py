@@ -63,7 +63,8 @@ def gated_recurrence(x, input_gate, decay_gate, rate, done=None, init_state=None
 
     Per row and channel s_t = rate sigmoid(decay_gate_t), a_t = exp(-s_t) and
     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(input_gate_t) x_t; the step after one flagged in
-    ``done`` has a_t = 0, whatever the state was: inf and NaN stay within their episode.
+    ``done`` has a_t = 0, whatever the state was: inf and NaN stay within their episode, and an
+    infinite state stays infinite as long as it lasts.
 
     x, input_gate, decay_gate [E, T, D] (``time_major``: [T, E, D]); rate [D] float32, not
     negative; done [E, T] (or [T, E]); init_state [E, D] float32; reset [E]: rows whose step before the first
@@ -293,7 +294,8 @@ def embed_tokens_backward(d_out, tokens, N, *, scale=1.0, d_table=None, stream=N
     """Gradient of the table of ``embed_tokens``: [N, D] in d_out's dtype.
 
     Row n is scale times the sum of d_out [..., D] over the tokens that are n, in float32 and
-    in a fixed order: the same from run to run.  Rows without a token are zero."""
+    in a fixed order: the same from run to run.  Rows without a token are zero.  An expanded
+    d_out (rows that are one row) is refused: pass it as ``d_out.contiguous()``."""
     if _p.torch is None:
         _p._import_torch()
     torch = _p.torch
