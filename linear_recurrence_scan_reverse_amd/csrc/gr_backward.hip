@@ -50,16 +50,15 @@ __device__ __forceinline__ void decays(Decays<S>& c, const Ahead<F, S>& in, floa
   for (int k = S - 1; k >= 0; --k) {
     const float dg = F::get(FORM != kPlain ? apart(in.dg[k]) : in.dg[k]);
     float g = F::get(FORM != kPlain ? apart(in.g[k]) : in.g[k]);
-    float sr = sigmoid(dg), y = rate2 * sr, a = decay_of<FORM>(y, FORM == kEvery ? less : 1.0f);
+    float sr = sigmoid(dg), a = decay_of<FORM>(rate2 * sr, FORM == kEvery ? less : 1.0f);
     if (FORM != kPlain) {
       sr = keep(sr, spread(live & ~cut, k));  // the gate of a step that starts anew is not looked at: it may be NaN
       a = decay_before<FORM>(decay_behind<FORM>(a, spread(cut, k)), spread(live, k));
-      y = keep(y, spread(live, k));
       g = keep(g, spread(live, k));
     }
     c.sr[k] = sr;
     c.a[k] = a;
-    c.L += y;
+    c.L = __builtin_fmaf(rate2, sr, c.L);
     c.out = decayed<FORM>(a, c.out + g);
     if (FORM != kPlain) c.out = keep(c.out, ~spread(cut, k));
   }
@@ -117,7 +116,7 @@ __device__ __forceinline__ float gradients(Decays<S>& c, const Ahead<F, S>& in, 
     u[k] = si[k] * F::get(FORM != kPlain ? apart(rest.x[k]) : rest.x[k]);
     if (FORM != kPlain) h = keep(h, ~spread(cut, k));
     before[k] = h;
-    if (FORM == kCut && k % 2 == 1) odd = seen(odd, before[k - 1], h);  // the next cut would hide them
+    if (FORM == kCut && k % 2 == 1) odd = seen(odd, before[k - 1], h);  // what each step takes: the next cut may hide it
     if (FORM == kEvery) c.a[k] = apart(c.a[k]);  // 16 masks of which is held as a - 1 would lie in scalars for long
     h = __builtin_fmaf(__builtin_amdgcn_sqrtf(one_less_square<FORM>(c.a[k])), u[k], decayed<FORM>(c.a[k], h));
   }
@@ -143,9 +142,7 @@ __device__ __forceinline__ float gradients(Decays<S>& c, const Ahead<F, S>& in, 
     d_rate -= part;
     if (FORM == kPlain || (live >> k) & 1) {
       to.dx.store(F::put(si[k] * du), t, k, to.dx_st, out_at);
-      float di = apart(__builtin_fmaf(-ud, si[k], ud));  // of float32 first: an instruction rounds to float16 at once
-      if (FORM == kEvery) di = __builtin_isinf(ud) ? ud * (1.0f - si[k]) : di;
-      to.dig.store(F::put(di), t, k, to.dig_st, out_at);
+      to.dig.store(F::put(ud * (1.0f - si[k])), t, k, to.dig_st, out_at);
       to.ddg.store(F::put(__builtin_fmaf(rate, c.sr[k], -rate) * part), t, k, to.ddg_st, out_at);
     }
   }
@@ -214,16 +211,8 @@ __global__ void __launch_bounds__(64 * W) fold_back_kernel(const Args p, uint32_
   __syncthreads();
   const int64_t column = (int64_t)tile * 64 + lane;
   if (w == 0 && column < p.D) {
-    float A = 1.0f;
-    const float out = joined([&](auto every) {
-      A = 1.0f;
-      float out = 0.0f;
-      for (int v = W - 1; v >= 0; --v) {
-        out = enter<every>(s_a[v][lane], s_y[v][lane], out);
-        A = A < 0.0f || s_a[v][lane] < 0.0f ? kDropped : A * s_a[v][lane];
-      }
-      return out;
-    });
+    float A;
+    const float out = joined_shares<W, -1>(s_a, s_y, lane, A);
     const uint32_t nseg = (uint32_t)p.nseg;
     const int64_t at = ((int64_t)(es / (nseg - 1)) * nseg + es % (nseg - 1) + 1) * p.D + column;
     p.seg_a[at] = A;
@@ -259,7 +248,7 @@ __device__ __forceinline__ bool backward_walk(const Args& p, Exchange<W>& s, uin
     if (p.d_final && !(in.done && p.T > 0 && in.done[(p.T - 1) * p.d_st] != 0)) start = p.d_final[e * p.D + d0 + col];
     float carry = start;  // e entering the W chunks at hand from the steps behind them
     if (seg < p.nseg - 1) {
-      carry = joined([&](auto every) {
+      carry = joined([&](auto every) __attribute__((always_inline)) {
         float c = start;
         for (int64_t v = p.nseg - 1; v > seg; --v) {
           const int64_t at = (e * p.nseg + v) * p.D + d0 + col;

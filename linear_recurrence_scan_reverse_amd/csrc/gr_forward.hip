@@ -39,20 +39,21 @@ __device__ __forceinline__ void coefficients(Coefficients<S>& c, const Chunk<F, 
     const float dg = F::get(FORM != kPlain ? apart(in.dg[k]) : in.dg[k]);
     const float ig = F::get(FORM != kPlain ? apart(in.ig[k]) : in.ig[k]);
     const float x = F::get(FORM != kPlain ? apart(in.x[k]) : in.x[k]);
-    float y = rate2 * sigmoid(dg);
-    float a = decay_of<FORM>(y, FORM == kEvery ? less : 1.0f);
+    float sr = sigmoid(dg);
+    float a = decay_of<FORM>(rate2 * sr, FORM == kEvery ? less : 1.0f);
     if (FORM != kPlain) a = decay_behind<FORM>(a, spread(cut, k));
-    float b = __builtin_amdgcn_sqrtf(one_less_square<FORM>(a)) * (sigmoid(ig) * x);
+    float m = __builtin_amdgcn_sqrtf(one_less_square<FORM>(a)), u = sigmoid(ig) * x;
     if (FORM != kPlain) {
       a = decay_before<FORM>(a, spread(live, k));
-      b = keep(b, spread(live, k));
-      y = keep(y, spread(live, k));
+      m = keep(m, spread(live, k));
+      u = keep(u, spread(live, k));
+      sr = keep(sr, spread(live, k));
       c.out = keep(c.out, ~spread(cut, k));
     }
     c.a[k] = a;
-    c.b[k] = b;
-    c.L += y;
-    c.out = decayed<FORM>(a, c.out) + b;
+    c.b[k] = m * u;
+    c.L = __builtin_fmaf(rate2, sr, c.L);
+    c.out = __builtin_fmaf(m, u, decayed<FORM>(a, c.out));
   }
 }
 
@@ -61,12 +62,13 @@ template <class F, int S, bool NEAR, Form FORM>
 __device__ __forceinline__ float states(const Coefficients<S>& c, float h, float& odd, const Stream<F, S, NEAR>& out,
                                         int t, int64_t st, uint32_t lane, uint32_t cut, uint32_t live) {
 #pragma clang fp contract(off)
+  float before = 0.0f;
 #pragma unroll
   for (int k = 0; k < S; ++k) {
     if (FORM != kPlain) h = keep(h, ~spread(cut, k));
-    const float before = h;
+    if (FORM == kCut && k % 2 == 1) odd = seen(odd, before, h);  // what each step takes: the next cut may hide it
+    before = h;
     h = decayed<FORM>(c.a[k], h) + c.b[k];
-    if (FORM == kCut && k % 2 == 1) odd = seen(odd, before, h);  // the next cut would hide them
     if (FORM == kPlain || (live >> k) & 1) out.store(F::put(h), t, k, st, lane);
   }
   if (FORM != kEvery) odd = seen(odd, h);
@@ -156,16 +158,8 @@ __global__ void __launch_bounds__(64 * W) fold_kernel(const Args p, uint32_t til
   __syncthreads();
   const int64_t column = (int64_t)tile * 64 + lane;
   if (w == 0 && column < p.D) {
-    float A = 1.0f;
-    const float out = joined([&](auto every) {
-      A = 1.0f;
-      float out = 0.0f;
-      for (int u = 0; u < W; ++u) {
-        out = enter<every>(s_a[u][lane], s_y[u][lane], out);
-        A = A < 0.0f || s_a[u][lane] < 0.0f ? kDropped : A * s_a[u][lane];
-      }
-      return out;
-    });
+    float A;
+    const float out = joined_shares<W, 1>(s_a, s_y, lane, A);
     const uint32_t nseg = (uint32_t)p.nseg;
     const int64_t at = ((int64_t)(es / (nseg - 1)) * nseg + es % (nseg - 1)) * p.D + column;
     p.seg_a[at] = A;
@@ -200,7 +194,7 @@ __device__ __forceinline__ bool forward_walk(const Args& p, Exchange<W>& s, uint
   const float start = p.init ? p.init[e * p.D + d0 + col] : 0.0f;
   float carry = start;  // the state entering the W chunks at hand
   if (seg > 0) {
-    carry = joined([&](auto every) {
+    carry = joined([&](auto every) __attribute__((always_inline)) {
       float c = start;
       for (int64_t u = 0; u < seg; ++u) {
         const int64_t at = (e * p.nseg + u) * p.D + d0 + col;

@@ -205,10 +205,30 @@ __device__ __forceinline__ float joined(const Join& join) {
   if (__builtin_expect(any_odd(seen(0.0f, c)), false)) c = join(std::true_type());
   return c;
 }
-
-// ------------------------------------------------------------------ chunks of S steps
-// A wave holds 64 channels of S steps in registers.  Addresses are scalars and the lane's
-// column, so that a step costs no vector instructions but its arithmetic.
+// The pair of a block's shares, of which STEP 1: the lowest wave's, -1: the highest one's comes first.
+template <int W, int STEP>
+__device__ __forceinline__ float joined_shares(const float (&s_a)[W][64], const float (&s_y)[W][64], int lane, float& A) {
+  float a[W], y[W];  // asked for all at once, and no branches between
+#pragma unroll
+  for (int u = 0; u < W; ++u) {
+    a[u] = s_a[STEP > 0 ? u : W - 1 - u][lane];
+    y[u] = s_y[STEP > 0 ? u : W - 1 - u][lane];
+  }
+  bool dropped = false;
+  A = 1.0f;
+#pragma unroll
+  for (int u = 0; u < W; ++u) {
+    dropped |= a[u] < 0.0f;
+    A *= a[u];
+  }
+  if (dropped) A = kDropped;
+  return joined([&](auto every) __attribute__((always_inline)) {
+    float c = 0.0f;
+#pragma unroll
+    for (int u = 0; u < W; ++u) c = enter<every>(a[u], y[u], c);
+    return c;
+  });
+}
 
 // The same value, of which the compiler knows nothing: keeps it from doing the work that both
 // forms of a branch begin with before the branch, where its results lie in registers for long.

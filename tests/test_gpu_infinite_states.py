@@ -82,3 +82,22 @@ def test_infinite_states_of_single_steps(rate):
     want = torch.zeros(4, 40)
     want[0, 3], want[1, 4] = 1, -1
     assert torch.equal(kinds(out), want.double()) and torch.equal(out, state)
+
+
+@pytest.mark.parametrize("T,D", [(1, 5), (2, 64), (7, 33), (64, 7), (300, 40)])
+@pytest.mark.parametrize("p_done", [0.2, 0.5, 0.9])
+def test_infinite_values_between_many_ends(T, D, p_done):
+    # episodes of one step and more: an infinite value may enter any step, and be dropped behind it
+    E = 60
+    d = draw(E, T, D, torch.float32, seed=53, p_done=p_done)
+    g = torch.Generator().manual_seed(100 * T + D)
+    for name, rate in (("x", 0.02), ("init", 0.1), ("d_out", 0.02), ("d_final", 0.1)):
+        at = torch.rand(d[name].shape, generator=g) < rate
+        sign = torch.where(torch.rand(d[name].shape, generator=g) < 0.5, -math.inf, math.inf)
+        d[name] = torch.where(at, sign, d[name])
+    got, grads = both(on_gpu(d))
+    want = so.Recurrence(d["x"], d["ig"], d["dg"], d["rate"], d["done"], d["init"], d["d_out"], d["d_final"])
+    for name, a, b in (("out", got[0], want.out), ("final state", got[1], want.final), ("dx", grads[0], want.dx),
+                       ("d_input_gate", grads[1], want.di), ("d_decay_gate", grads[2], want.dr),
+                       ("d_init_state", grads[4], want.d_init)):
+        assert torch.equal(kinds(a), kinds(b)), name
